@@ -11,8 +11,7 @@
 
 #include <hip/hip_runtime.h>
 
-#include <initializer_list>
-
+#include "api_checks.h"
 #include "glu_launch.h"
 
 namespace {
@@ -21,6 +20,14 @@ using glu::BF16Args;
 using glu::MxArgs;
 using glu::NvArgs;
 using glu::GemmArgs;
+using glu::aligned16;
+using glu::any_overflow;
+using glu::check_no_overlap;
+using glu::kOffsetLimit;
+using glu::mat;
+using glu::Operand;
+using glu::overlaps;
+using glu::status_of;
 
 // Upper bound on MXFP8 tiles per launch (counted with the smallest tile, 32 x 64), so the
 // tile index and the workgroup count stay within 32 bits.
@@ -36,58 +43,12 @@ constexpr int64_t kMaxMxOutPitch = (int64_t)1 << 24;
 // per-row base with 32-bit offsets (FP32 hook loads 4 bytes per column; 128x4 scales of the
 // backward's [M, 2N] reach 16 bytes per column) that must stay below 2^31.
 constexpr int64_t kMaxNvWidth = (int64_t)1 << 26;
-// Bytes an operand or output of the GEMM kernels may span (32-bit offsets from its base).
-constexpr int64_t kOffsetLimit = (int64_t)1 << 31;
-
 // Output pitches of an MXFP8 launch whose quantized matrix is [M, width].
 glu_status check_mx_pitch(int flags, int64_t M, int64_t width) {
   if ((flags & glu::ROWWISE) && width > kMaxMxOutPitch) return GLU_ERR_SHAPE;
   if ((flags & glu::COLWISE) && M > kMaxMxOutPitch) return GLU_ERR_SHAPE;
   return GLU_OK;
 }
-
-// Byte extent of a row-major matrix: ((rows - 1) * ld + cols) * esz, or -1 on overflow.
-int64_t extent_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t esz) {
-  int64_t a, b, c;
-  if (__builtin_mul_overflow(rows - 1, ld, &a)) return -1;
-  if (__builtin_add_overflow(a, cols, &b)) return -1;
-  if (__builtin_mul_overflow(b, esz, &c)) return -1;
-  return c;
-}
-
-struct Operand {
-  uintptr_t base;
-  int64_t rows, cols, ld, esz;  // cols and ld in elements
-  int64_t bytes;                // extent, -1 on overflow
-};
-
-Operand mat(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t esz) {
-  return Operand{(uintptr_t)p, rows, cols, ld, esz, extent_bytes(rows, cols, ld, esz)};
-}
-
-// True when the two operands may share a byte.  Operands with the same byte row stride
-// are tested row by row (so [gate | up] halves of one buffer, or [dGate | dUp] outputs, do
-// not count as overlapping); otherwise the byte spans are compared, which can only err
-// on the side of rejecting.
-bool overlaps(const Operand& A, const Operand& B) {
-  if (A.base == 0 || B.base == 0) return false;
-  const uintptr_t ahi = A.base + (uintptr_t)A.bytes, bhi = B.base + (uintptr_t)B.bytes;
-  if (!(A.base < bhi && B.base < ahi)) return false;
-  const int64_t L = A.ld * A.esz;
-  if (L != B.ld * B.esz || L <= 0) return true;
-  const int64_t wa = A.cols * A.esz, wb = B.cols * B.esz;
-  const int64_t d = (int64_t)(B.base - A.base);  // two's complement difference
-  // rows r of A and r' of B meet iff d - k L lies in (-wb, wa) for k = r - r'
-  auto floordiv = [](int64_t x, int64_t y) { return x / y - ((x % y != 0) && ((x < 0) != (y < 0))); };
-  for (int64_t k = floordiv(d - wa, L); k <= floordiv(d + wb, L) + 1; k++) {
-    if (k > A.rows - 1 || k < -(B.rows - 1)) continue;
-    const int64_t off = d - k * L;
-    if (off > -wb && off < wa) return true;
-  }
-  return false;
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 bool valid_act(int act) { return act >= glu::SWIGLU && act <= glu::RELU2; }
 bool valid_layout(int l) { return l == glu::SPLIT || l == glu::PAIRED; }
@@ -115,22 +76,6 @@ Operand mx_scales(const void* p, int64_t rows, int64_t nb, int flags) {
   return mat(p, 1, bytes, bytes, 1);
 }
 
-bool any_overflow(std::initializer_list<Operand> ops) {
-  for (const Operand& o : ops)
-    if (o.base != 0 && (o.bytes < 0 || o.base + (uintptr_t)o.bytes < o.base)) return true;
-  return false;
-}
-
-glu_status check_no_overlap(std::initializer_list<Operand> outs, std::initializer_list<Operand> ins) {
-  for (auto i = outs.begin(); i != outs.end(); ++i) {
-    for (const Operand& in : ins)
-      if (overlaps(*i, in)) return GLU_ERR_OVERLAP;
-    for (auto j = i + 1; j != outs.end(); ++j)
-      if (overlaps(*i, *j)) return GLU_ERR_OVERLAP;
-  }
-  return GLU_OK;
-}
-
 glu_status check_mx_outputs(int flags, uint8_t* q_row, uint8_t* s_row, uint8_t* q_col,
                             uint8_t* s_col) {
   if (!valid_flags(flags)) return GLU_ERR_ARG;
@@ -146,8 +91,6 @@ glu_status check_mx_outputs(int flags, uint8_t* q_row, uint8_t* s_row, uint8_t* 
   }
   return GLU_OK;
 }
-
-glu_status status_of(hipError_t e) { return e == hipSuccess ? GLU_OK : GLU_ERR_HIP; }
 
 }  // namespace
 
