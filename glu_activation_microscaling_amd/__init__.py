@@ -22,6 +22,8 @@ Entry points (C names in include/glu_mx.h):
   (fmt "mxfp8": E4M3 codes, or "mxfp4": packed E2M1 codes; w_layout "split" or "paired")
   glu_quant_mxfp8_f32(x, rowwise=, colwise=)                -> (q_row, q_col, s_row, s_col)
   glu_quant_nvfp4_f32(x, sf_layout=)                        -> (q, sf)
+The operators around the GLU (ffn.py: glu_block_norm*, glu_linear*, glu_moe_*) are names of
+the package too.
 A disabled MXFP8 direction comes back as zero-sized tensors (fixed arity), as in the
 MXFP8 page's API section.  Codes and scales are uint8 tensors; BF16 data is torch.bfloat16.
 """
@@ -45,7 +47,7 @@ STATUS = {
     5: "GLU_ERR_ARG", 6: "GLU_ERR_OVERLAP", 7: "GLU_ERR_UNSUPPORTED", 8: "GLU_ERR_HIP",
 }
 
-_i64, _int, _p = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
+_i64, _int, _p, _f = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_float
 _SIGNATURES = {
     "glu_fwd": [_int, _int, _i64, _i64, _p, _p, _i64, _p, _i64, _p],
     "glu_bwd": [_int, _int, _i64, _i64, _p, _p, _i64, _p, _i64, _p, _p, _i64, _p],
@@ -81,6 +83,28 @@ _SIGNATURES = {
     "glu_check_stream_probe": [_int, _p, _int, _p, _i64, _int],
 }
 
+_FFN_SIGNATURES = {  # without the stream: the arguments that glu_check_* takes too
+    "block_norm": [_int, _int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _f, _f, _p, _i64, _p, _i64, _p],
+    "block_norm_mxfp8": [_int, _int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _f, _f, _p, _i64, _p, _p, _p],
+    "block_norm_bwd": [_int, _int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i64, _p, _p, _p, _f,
+                           _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _i64],
+    "linear": [_int, _i64, _i64, _i64, _i64, _p, _p, _i64, _p, _p, _p, _i64, _p, _i64, _p, _p, _i64],
+    "linear_bwd": [_int, _i64, _i64, _i64, _i64, _p, _p, _i64, _p, _i64, _p, _p, _p, _i64, _p, _p, _p, _i64],
+    "moe_sort": [_i64, _i64, _int, _p, _int, _p, _p, _p, _i64],
+    "moe_permute": [_i64, _i64, _int, _i64, _p, _i64, _p, _p, _p, _i64],
+    "moe_combine": [_i64, _i64, _i64, _p, _i64, _p, _p, _p, _i64, _p, _i64],
+    "moe_combine_bwd": [_i64, _i64, _i64, _int, _p, _i64, _p, _i64, _p, _p, _p, _p, _i64, _p],
+}
+for _n, _args in _FFN_SIGNATURES.items():
+    _SIGNATURES["glu_" + _n] = _args + [_p]
+    _SIGNATURES["glu_check_" + _n] = _args
+_SIZES = {   # functions that give a number of bytes
+    "glu_nvfp4_sf_bytes": [_i64, _i64, _int], "glu_mxfp8_sf_bytes": [_i64, _i64, _int],
+    "glu_block_norm_bwd_work_bytes": [_i64, _i64, _i64], "glu_linear_work_bytes": [_i64, _i64, _i64, _i64],
+    "glu_linear_bwd_work_bytes": [_int, _i64, _i64, _i64, _i64, _int],
+    "glu_moe_sort_work_bytes": [_i64, _i64, _int],
+}
+
 _lib = None
 
 
@@ -104,10 +128,10 @@ def lib():
             f.restype = ctypes.c_int
         L.glu_status_string.argtypes = [ctypes.c_int]
         L.glu_status_string.restype = ctypes.c_char_p
-        L.glu_nvfp4_sf_bytes.argtypes = [_i64, _i64, _int]
-        L.glu_nvfp4_sf_bytes.restype = _i64
-        L.glu_mxfp8_sf_bytes.argtypes = [_i64, _i64, _int]
-        L.glu_mxfp8_sf_bytes.restype = _i64
+        for name, args in _SIZES.items():
+            f = getattr(L, name)
+            f.argtypes = args
+            f.restype = _i64
         L.glu_version.restype = ctypes.c_int
         _lib = L
     return _lib
@@ -453,3 +477,6 @@ def glu_stream_probe(srcs, dsts):
     _call("glu_stream_probe", len(srcs), ctypes.cast(src, ctypes.c_void_p), len(dsts),
           ctypes.cast(dst, ctypes.c_void_p), n // 16, width, _stream(srcs[0]))
 
+
+from .ffn import (glu_block_norm, glu_block_norm_bwd, glu_block_norm_mxfp8, glu_linear,  # noqa: E402,F401
+                  glu_linear_bwd, glu_moe_combine, glu_moe_combine_bwd, glu_moe_permute, glu_moe_sort)

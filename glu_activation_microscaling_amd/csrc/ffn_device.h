@@ -1,0 +1,144 @@
+// Device helpers of the operators around the GLU: rows in 16-byte vectors at any alignment,
+// and sums over a wave or a workgroup.
+#pragma once
+
+#include "glu_device.h"
+
+namespace glu {
+
+struct __attribute__((packed, aligned(2))) Vec16 {
+  u32x4 v;
+};
+
+// Eight elements as loaded: BF16 in one 16-byte vector, FP32 in two.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  u32x4 a;
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      f[2 * i] = bf_lo(a[i]);
+      f[2 * i + 1] = bf_hi(a[i]);
+    }
+  }
+};
+template <>
+struct Raw<float> {
+  u32x4 a, b;
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      f[i] = __uint_as_float(a[i]);
+      f[4 + i] = __uint_as_float(b[i]);
+    }
+  }
+};
+
+// Loads elements 0..n-1 of p (n <= 0: none, n >= 8: all eight); the others read zero.
+template <bool RAGGED>
+__device__ __forceinline__ void load(Raw<uint16_t>& r, const uint16_t* p, int n) {
+  r.a = (u32x4)0u;
+  if (n >= 8) {
+    r.a = RAGGED ? reinterpret_cast<const Vec16*>(p)->v : *reinterpret_cast<const u32x4*>(p);
+  } else if (RAGGED) {
+#pragma unroll
+    for (int i = 0; i < 7; i++)
+      if (i < n) r.a[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+  }
+}
+template <bool RAGGED>
+__device__ __forceinline__ void load(Raw<float>& r, const float* p, int n) {
+  r.a = (u32x4)0u;
+  r.b = (u32x4)0u;
+  if (n >= 8) {
+    if (RAGGED) {
+      r.a = reinterpret_cast<const Vec16*>(p)[0].v;
+      r.b = reinterpret_cast<const Vec16*>(p)[1].v;
+    } else {
+      r.a = reinterpret_cast<const u32x4*>(p)[0];
+      r.b = reinterpret_cast<const u32x4*>(p)[1];
+    }
+  } else if (RAGGED) {
+#pragma unroll
+    for (int i = 0; i < 7; i++)
+      if (i < n) {
+        if (i < 4) r.a[i & 3] = __float_as_uint(p[i]);
+        else r.b[i & 3] = __float_as_uint(p[i]);
+      }
+  }
+}
+
+template <bool RAGGED>
+__device__ __forceinline__ void store(uint16_t* p, const float (&f)[8], int n) {
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; i++) v[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+  if (n >= 8) {
+    if (RAGGED) reinterpret_cast<Vec16*>(p)->v = v;
+    else *reinterpret_cast<u32x4*>(p) = v;
+  } else if (RAGGED) {
+#pragma unroll
+    for (int i = 0; i < 7; i++)
+      if (i < n) p[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+  }
+}
+template <bool RAGGED>
+__device__ __forceinline__ void store(float* p, const float (&f)[8], int n) {
+  const u32x4 a = {__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+  const u32x4 b = {__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])};
+  if (n >= 8) {
+    if (RAGGED) {
+      reinterpret_cast<Vec16*>(p)[0].v = a;
+      reinterpret_cast<Vec16*>(p)[1].v = b;
+    } else {
+      reinterpret_cast<u32x4*>(p)[0] = a;
+      reinterpret_cast<u32x4*>(p)[1] = b;
+    }
+  } else if (RAGGED) {
+#pragma unroll
+    for (int i = 0; i < 7; i++)
+      if (i < n) p[i] = f[i];
+  }
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+// Sum over the wave's 64 lanes, in every lane: partial sums run up each row of 16 lanes, then
+// across the rows, to lane 63.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0x111, 0xf>(v);   // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);   // row_bcast 15, 31
+  v = dpp_add<0x143, 0xc>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Sums of N values over the workgroup, in every thread.  The two halves of `part` are used in
+// turn, so one barrier a call suffices: a half is written again only after the barrier of the
+// call in between.
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float (*part)[16][N], int& turn) {
+#pragma unroll
+  for (int k = 0; k < N; k++) v[k] = wave_sum(v[k]);
+  const unsigned waves = blockDim.x >> 6;
+  if (waves == 1) return;
+  if ((threadIdx.x & 63u) == 0) {
+#pragma unroll
+    for (int k = 0; k < N; k++) part[turn][threadIdx.x >> 6][k] = v[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; k++) v[k] = part[turn][0][k];
+  for (unsigned w = 1; w < waves; w++)
+#pragma unroll
+    for (int k = 0; k < N; k++) v[k] += part[turn][w][k];
+  turn ^= 1;
+}
+
+}  // namespace glu

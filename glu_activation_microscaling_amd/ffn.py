@@ -1,0 +1,322 @@
+"""Binding of the operators around the GLU: block norms, linear products, expert routing.
+
+Argument marshalling only, as for the GLU entry points (C names and formulas in
+include/glu_mx.h); every function is also a name of the package:
+  glu_block_norm(x, y=None, ...)               -> (x_out, h, stats)
+  glu_block_norm_mxfp8(x, y=None, ...)         -> (x_out, q, s, stats), h quantized rowwise
+  glu_block_norm_bwd(x, y, stats, dx_out, dh, ...) -> (dx, dy, dgate, dw_post, dw_pre, db_pre)
+  glu_linear(x, w, bias, residual, ...)        -> y, or (y, pre) with save_pre
+  glu_linear_bwd(dy, x, w, ...)                -> (dx, dw, db)
+  glu_moe_sort(ids, experts)                   -> (rows, offsets)
+  glu_moe_permute(x, rows, offsets)            -> xs
+  glu_moe_combine(y, rows, weights, residual)  -> out
+  glu_moe_combine_bwd(dout, y, rows, weights, offsets) -> (dy, dweights)
+What is disabled comes back zero-sized (fixed arity).  Scratch memory is a torch allocation of
+the call, on the current stream.
+"""
+import torch
+
+from . import _call, _rowmajor, _stream, lib
+
+NORM_KIND = {"rms": 0, "layer": 1}
+LINEAR_ACT = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 2, "gelu_erf": 3}
+_PRE, _POST, _F32_STREAM, _F32_PARAMS, _GATE_GROUPED, _W_GROUPED, _B_GROUPED = 1, 2, 4, 8, 16, 32, 64
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None and t.numel() else None
+
+
+def _matrix(t, name, dtype, rows=None, cols=None):
+    """Row stride of a 2-D GPU tensor with unit column stride (of [rows, cols] where given).
+    The stride of a single row means nothing; a whole number of vectors is passed for it."""
+    M, N, ld = _rowmajor(t, name, dtype)
+    if (rows is not None and M != rows) or (cols is not None and N != cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got [{M}, {N}]")
+    return ld if M > 1 else (N + 7) // 8 * 8
+
+
+def _like(t, name, dtype, shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous GPU tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _same_device(ref, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+
+
+# ---- norms -----------------------------------------------------------------------------------
+
+def _norm_setup(x, y, gate, w_pre, b_pre, w_post, pre, post, kind):
+    """(kind code, flags, M, H, groups, ld_x, ld_y) of a norm call, its parameters checked."""
+    if kind not in NORM_KIND:
+        raise ValueError(f"kind must be one of {sorted(NORM_KIND)}")
+    if x.dtype not in (_BF16, _F32):
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    ld_x = _matrix(x, "x", x.dtype)
+    M, H = x.shape
+    ld_y = 0 if y is None else _matrix(y, "y", _BF16, M, H)
+    if y is None and (post or gate is not None):
+        raise ValueError("a gate and the norm after the block need y")
+    if not pre and (w_pre is not None or b_pre is not None):
+        raise ValueError("w_pre and b_pre belong to the norm before the next block (pre=True)")
+    if not post and w_post is not None:
+        raise ValueError("w_post belongs to the norm after the block (post=True)")
+    flags = (_PRE if pre else 0) | (_POST if post else 0) | (_F32_STREAM if x.dtype == _F32 else 0)
+    groups, dtype = 1, None
+    for p, name, grouped in ((gate, "gate", _GATE_GROUPED), (w_pre, "w_pre", _W_GROUPED),
+                             (b_pre, "b_pre", _B_GROUPED), (w_post, "w_post", 0)):
+        if p is None:
+            continue
+        dtype = dtype or p.dtype
+        if p.dtype != dtype or dtype not in (_BF16, _F32):
+            raise TypeError("the parameters must all be torch.bfloat16 or all torch.float32")
+        if not p.is_cuda or not p.is_contiguous() or p.dim() not in (1, 2) or p.shape[-1] != H:
+            raise ValueError(f"{name} must be a contiguous GPU tensor [H] or [groups, H]")
+        if p.dim() == 2 and p.shape[0] != 1:
+            if not grouped or (groups != 1 and groups != p.shape[0]):
+                raise ValueError(f"{name} must be [H] or share one number of groups with the other parameters")
+            groups = p.shape[0]
+            flags |= grouped
+    if groups == 0 or M % groups:
+        raise ValueError(f"{M} rows are not a whole number of rows for each of {groups} groups")
+    if dtype == _F32:
+        flags |= _F32_PARAMS
+    return NORM_KIND[kind], flags, M, H, groups, ld_x, ld_y
+
+
+def _norm_forward(fn, x, y, gate, w_pre, b_pre, w_post, pre, post, res_scale, kind, eps, outs, x_out):
+    k, flags, M, H, groups, ld_x, ld_y = _norm_setup(x, y, gate, w_pre, b_pre, w_post, pre, post, kind)
+    _same_device(x, y=y, gate=gate, w_pre=w_pre, b_pre=b_pre, w_post=w_post)
+    if y is None:
+        if x_out is not None or res_scale != 1.0:
+            raise ValueError("without y, x' is x itself: no x_out and res_scale 1")
+        ld_xo = 0
+    else:
+        if x_out is None:
+            x_out = torch.empty((M, H), dtype=x.dtype, device=x.device)
+        ld_xo = _matrix(x_out, "x_out", x.dtype, M, H)
+    stats = torch.empty((M, 4), dtype=_F32, device=x.device)
+    _call(fn, k, flags, M, H, groups, _ptr(x), ld_x, _ptr(y), ld_y, _ptr(gate), _ptr(w_pre), _ptr(b_pre),
+          _ptr(w_post), res_scale, eps, _ptr(x_out), ld_xo, *outs(M, H), _ptr(stats), _stream(x))
+    return x if y is None else x_out, stats
+
+
+def glu_block_norm(x, y=None, *, gate=None, w_pre=None, b_pre=None, w_post=None, pre=True, post=False,
+                   res_scale=1.0, kind="rms", eps=1e-6, x_out=None, out=None):
+    """x' = res_scale x + gate * N(y) w_post (post=True; else gate * y) and h = N(x') w_pre +
+    b_pre (pre=True), N the rms or layer norm of a row: (x', h, stats).  Without y, x' is x
+    itself.  gate, w_pre, b_pre: [H], or [groups, H] with one row per M / groups rows of x.
+    stats is what glu_block_norm_bwd needs."""
+    h = out
+    if pre and h is None:
+        h = torch.empty(x.shape, dtype=_BF16, device=x.device)
+    elif not pre:
+        if out is not None:
+            raise ValueError("out is the output of the norm before the next block (pre=True)")
+        h = torch.empty((0,), dtype=_BF16, device=x.device)
+
+    def outs(M, H):
+        return (_ptr(h), _matrix(h, "out", _BF16, M, H)) if pre else (None, 0)
+
+    x_out, stats = _norm_forward("glu_block_norm", x, y, gate, w_pre, b_pre, w_post, pre, post, res_scale, kind, eps,
+                                 outs, x_out)
+    return x_out, h, stats
+
+
+def glu_block_norm_mxfp8(x, y=None, *, gate=None, w_pre=None, b_pre=None, w_post=None, post=False, res_scale=1.0,
+                         kind="rms", eps=1e-6, x_out=None, out=None):
+    """glu_block_norm with h quantized MXFP8 rowwise: (x', q [M, H], s [M, H/32], stats); q and
+    s are the xq and xs of glu_gemm."""
+    from . import _byte_buffer
+    if x.dim() != 2:
+        raise ValueError("x must be a 2-D tensor with unit column stride (no silent copies)")
+    M, H = x.shape
+    if out is not None:
+        q, s = out
+        _byte_buffer(q, "q", M * H)
+        _byte_buffer(s, "s", M * (H // 32))
+    else:
+        q = torch.empty((M, H), dtype=torch.uint8, device=x.device)
+        s = torch.empty((M, H // 32), dtype=torch.uint8, device=x.device)
+    x_out, stats = _norm_forward("glu_block_norm_mxfp8", x, y, gate, w_pre, b_pre, w_post, True, post, res_scale,
+                                 kind, eps, lambda M, H: (_ptr(q), _ptr(s)), x_out)
+    return x_out, q, s, stats
+
+
+def glu_block_norm_bwd(x, y, stats, dx_out, dh, *, gate=None, w_pre=None, b_pre=None, w_post=None, pre=True,
+                       post=False, res_scale=1.0, kind="rms", eps=1e-6):
+    """Gradients of glu_block_norm from those of x' (dx_out, or None for zero) and of h (dh, None
+    when pre=False): (dx, dy, dgate, dw_post, dw_pre, db_pre), each in its operand's type and
+    shape and zero-sized where that operand is absent.  The other arguments are the
+    forward's (b_pre gives only its shape; eps is in stats)."""
+    k, flags, M, H, groups, ld_x, ld_y = _norm_setup(x, y, gate, w_pre, b_pre, w_post, pre, post, kind)
+    _like(stats, "stats", _F32, (M, 4))
+    if pre != (dh is not None):
+        raise ValueError("dh is the gradient of h: given exactly when pre=True")
+    if y is None and res_scale != 1.0:
+        raise ValueError("without y, x' is x itself: res_scale 1")
+    _same_device(x, y=y, stats=stats, dx_out=dx_out, dh=dh, gate=gate, w_pre=w_pre, b_pre=b_pre, w_post=w_post)
+    ld_dxo = 0 if dx_out is None else _matrix(dx_out, "dx_out", x.dtype, M, H)
+    ld_dh = 0 if dh is None else _matrix(dh, "dh", _BF16, M, H)
+    dev = x.device
+    dx = torch.empty((M, H), dtype=x.dtype, device=dev)
+    dy = torch.empty((M, H) if y is not None else (0,), dtype=_BF16, device=dev)
+
+    def grad_of(p):
+        return torch.empty((0,), dtype=_BF16, device=dev) if p is None else torch.empty_like(p)
+
+    dgate, dw_post, dw_pre, db_pre = grad_of(gate), grad_of(w_post), grad_of(w_pre), grad_of(b_pre)
+    nbytes = lib().glu_block_norm_bwd_work_bytes(M, H, groups)
+    work = torch.empty((max(nbytes, 0),), dtype=torch.uint8, device=dev)
+    _call("glu_block_norm_bwd", k, flags, M, H, groups, _ptr(x), ld_x, _ptr(y), ld_y, _ptr(stats), _ptr(dx_out),
+          ld_dxo, _ptr(dh), ld_dh, _ptr(gate), _ptr(w_pre), _ptr(w_post), res_scale, _ptr(dx), H if M > 1 else
+          (H + 7) // 8 * 8, _ptr(dy), H if M > 1 else (H + 7) // 8 * 8, _ptr(dgate), _ptr(dw_pre), _ptr(db_pre),
+          _ptr(dw_post), _ptr(work), nbytes, _stream(x))
+    return dx, dy, dgate, dw_post, dw_pre, db_pre
+
+
+# ---- linear products -------------------------------------------------------------------------
+
+def _linear_setup(x, w, offsets, act):
+    if act not in LINEAR_ACT:
+        raise ValueError(f"act must be one of {sorted(LINEAR_ACT)}")
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [N, K], or [groups, N, K] with offsets")
+    if (w.dim() == 3) != (offsets is not None):
+        raise ValueError("offsets go with w [groups, N, K], and only with it")
+    N, K = w.shape[-2:]
+    groups = w.shape[0] if w.dim() == 3 else 1
+    _like(w, "w", _BF16, w.shape)
+    ld_x = _matrix(x, "x", _BF16, None, K)
+    if offsets is not None:
+        _like(offsets, "offsets", _I32, (groups + 1,))
+    return x.shape[0], N, K, groups, ld_x
+
+
+def glu_linear(x, w, bias=None, residual=None, *, act="none", offsets=None, save_pre=False, out=None):
+    """y = act(x W^T + bias) + residual, [M, N].  w is [N, K], or [groups, N, K] with int32
+    offsets [groups + 1]: rows offsets[e] .. offsets[e + 1] - 1 of x go through w[e], bias[e].
+    save_pre=True returns (y, pre), pre the FP16 pre-activation that glu_linear_bwd takes."""
+    M, N, K, groups, ld_x = _linear_setup(x, w, offsets, act)
+    if bias is not None:
+        _like(bias, "bias", _BF16, w.shape[:-1])
+    _same_device(x, w=w, bias=bias, residual=residual, offsets=offsets, out=out)
+    ld_res = 0 if residual is None else _matrix(residual, "residual", _BF16, M, N)
+    y = out if out is not None else torch.empty((M, N), dtype=_BF16, device=x.device)
+    ld_y = _matrix(y, "out", _BF16, M, N)
+    pre = torch.empty((M, N), dtype=torch.float16, device=x.device) if save_pre else None
+    nbytes = lib().glu_linear_work_bytes(M, N, K, groups)
+    work = torch.empty((nbytes,), dtype=torch.uint8, device=x.device) if nbytes > 0 else None
+    _call("glu_linear", LINEAR_ACT[act], M, N, K, groups, _ptr(offsets), _ptr(x), ld_x, _ptr(w), _ptr(bias),
+          _ptr(residual), ld_res, _ptr(y), ld_y, _ptr(pre), _ptr(work), nbytes, _stream(x))
+    return (y, pre) if save_pre else y
+
+
+def glu_linear_bwd(dy, x, w, *, pre=None, act="none", offsets=None, bias=False, need_dx=True, need_dw=True):
+    """Gradients of glu_linear: (dx [M, K], dw like w, db [N] or [groups, N]).  pre is the
+    forward's (act other than "none"); bias=True asks for db.  What is not wanted comes back
+    zero-sized.  The residual's gradient is dy."""
+    M, N, K, groups, ld_x = _linear_setup(x, w, offsets, act)
+    ld_dy = _matrix(dy, "dy", _BF16, M, N)
+    a = LINEAR_ACT[act]
+    if (a != 0) != (pre is not None):
+        raise ValueError('pre goes with an act other than "none", and only with it')
+    if pre is not None:
+        _like(pre, "pre", torch.float16, (M, N))
+    _same_device(x, w=w, dy=dy, pre=pre, offsets=offsets)
+    dev, none = x.device, torch.empty((0,), dtype=_BF16, device=x.device)
+    dx = torch.empty((M, K), dtype=_BF16, device=dev) if need_dx else none
+    dw = torch.empty_like(w) if need_dw else none
+    db = torch.empty(w.shape[:-1], dtype=_BF16, device=dev) if bias else none
+    nbytes = lib().glu_linear_bwd_work_bytes(a, M, N, K, groups, int(bias))
+    work = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes > 0 else None
+    _call("glu_linear_bwd", a, M, N, K, groups, _ptr(offsets), _ptr(dy), ld_dy, _ptr(x), ld_x, _ptr(w), _ptr(pre),
+          _ptr(dx), K, _ptr(dw), _ptr(db), _ptr(work), nbytes, _stream(x))
+    return dx, dw, db
+
+
+# ---- expert routing --------------------------------------------------------------------------
+
+def glu_moe_sort(ids, experts):
+    """Places of a stable sort by expert: (rows int32 like ids, offsets int32 [experts + 1]).
+    ids [tokens, choices] is int32 or int64; a number outside 0 .. experts - 1 is a dropped
+    choice and gets row -1."""
+    if ids.dtype not in (_I32, torch.int64):
+        raise TypeError(f"ids must be torch.int32 or torch.int64, got {ids.dtype}")
+    if ids.dim() != 2:
+        raise ValueError("ids must be [tokens, choices]")
+    _like(ids, "ids", ids.dtype, ids.shape)
+    T, k = ids.shape
+    rows = torch.empty((T, k), dtype=_I32, device=ids.device)
+    offsets = torch.empty((experts + 1,), dtype=_I32, device=ids.device)
+    nbytes = lib().glu_moe_sort_work_bytes(T, k, experts)
+    work = torch.empty((nbytes,), dtype=torch.uint8, device=ids.device) if nbytes > 0 else None
+    _call("glu_moe_sort", T, k, experts, _ptr(ids), ids.element_size(), _ptr(rows), _ptr(offsets), _ptr(work), nbytes,
+          _stream(ids))
+    return rows, offsets
+
+
+def _routing(rows, offsets=None):
+    if rows.dim() != 2:
+        raise ValueError("rows must be [tokens, choices]")
+    _like(rows, "rows", _I32, rows.shape)
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.numel() < 2:
+            raise ValueError("offsets must be [experts + 1]")
+        _like(offsets, "offsets", _I32, offsets.shape)
+    return rows.shape
+
+
+def glu_moe_permute(x, rows, offsets, *, out=None):
+    """xs [tokens * choices, H] with xs[rows[t, j]] = x[t] and zero rows past offsets[-1]; x may
+    have any dtype (codes and scales of quantized tokens too)."""
+    T, k = _routing(rows, offsets)
+    M, H, ld = _rowmajor(x, "x", x.dtype)
+    if M != T:
+        raise ValueError(f"x must have {T} rows, got {M}")
+    _same_device(x, rows=rows, offsets=offsets, out=out)
+    xs = out if out is not None else torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+    ld_xs = _matrix(xs, "out", x.dtype, T * k, H)
+    e = x.element_size()
+    _call("glu_moe_permute", T, k, offsets.numel() - 1, H * e, _ptr(x), (ld if M > 1 else H) * e, _ptr(rows),
+          _ptr(offsets), _ptr(xs), ld_xs * e, _stream(x))
+    return xs
+
+
+def glu_moe_combine(y, rows, weights=None, residual=None, *, out=None):
+    """out[t] = residual[t] + sum over j of weights[t, j] y[rows[t, j]], dropped choices left out:
+    [tokens, H].  weights float32 like rows, or None for ones (the gradient of permute)."""
+    T, k = _routing(rows)
+    ld_y = _matrix(y, "y", _BF16, T * k)
+    H = y.shape[1]
+    if weights is not None:
+        _like(weights, "weights", _F32, (T, k))
+    _same_device(y, rows=rows, weights=weights, residual=residual, out=out)
+    ld_res = 0 if residual is None else _matrix(residual, "residual", _BF16, T, H)
+    o = out if out is not None else torch.empty((T, H), dtype=_BF16, device=y.device)
+    _call("glu_moe_combine", T, k, H, _ptr(y), ld_y, _ptr(rows), _ptr(weights), _ptr(residual), ld_res, _ptr(o),
+          _matrix(o, "out", _BF16, T, H), _stream(y))
+    return o
+
+
+def glu_moe_combine_bwd(dout, y, rows, weights, offsets):
+    """Gradients of glu_moe_combine: (dy like y, zero rows past offsets[-1]; dweights float32,
+    0 for dropped choices).  The residual's gradient is dout."""
+    T, k = _routing(rows, offsets)
+    ld_y = _matrix(y, "y", _BF16, T * k)
+    H = y.shape[1]
+    ld_d = _matrix(dout, "dout", _BF16, T, H)
+    _like(weights, "weights", _F32, (T, k))
+    _same_device(y, dout=dout, rows=rows, weights=weights, offsets=offsets)
+    dy = torch.empty((T * k, H), dtype=_BF16, device=y.device)
+    dw = torch.empty((T, k), dtype=_F32, device=y.device)
+    _call("glu_moe_combine_bwd", T, k, H, offsets.numel() - 1, _ptr(dout), ld_d, _ptr(y), ld_y, _ptr(rows),
+          _ptr(weights), _ptr(offsets), _ptr(dy), (H + 7) // 8 * 8 if T * k == 1 else H, _ptr(dw), _stream(y))
+    return dy, dw

@@ -350,6 +350,145 @@ int64_t glu_nvfp4_sf_bytes(int64_t M, int64_t H, int sf_layout);
  * scales: rows = N (2N), cols = M. */
 int64_t glu_mxfp8_sf_bytes(int64_t rows, int64_t cols, int swizzled);
 
+/* ==== Operators around the GLU =======================================================
+ * The norms on both sides of a block, the linear products beside the gate/up projection, and
+ * the routing of tokens to experts: what a feed-forward block needs next to act(gate) * up.
+ * The conventions above hold.  Data is BF16 unless said otherwise, arithmetic FP32.  Entry
+ * points that need scratch memory take `work` of at least *_work_bytes bytes (16-byte
+ * aligned; its contents need not be kept).  Results are deterministic. */
+
+/* ---- Block norms
+ *   x' = res_scale x + gate * z,  z = N(y) w_post (GLU_NORM_POST) or z = y
+ *   h  = N(x') w_pre + b_pre                      (GLU_NORM_PRE)
+ *   N(v) = v / sqrt(mean(v^2) + eps)              (GLU_NORM_RMS)
+ *        = (v - mean v) / sqrt(var v + eps)       (GLU_NORM_LAYER)
+ * x, x' are [M, H] BF16, or FP32 with GLU_NORM_F32_STREAM; y, h are BF16 [M, H]; h is formed
+ * from the unrounded x'.  gate, w_pre, b_pre, w_post are BF16, or FP32 with
+ * GLU_NORM_F32_PARAMS; a NULL one is left out of the formula.  The first three are [H], or
+ * with GLU_NORM_{GATE,W,B}_GROUPED [groups, H], one row per M / groups consecutive rows of x
+ * (a request's adaptive scale, shift and gate; groups = M gives one per row).
+ * y may be NULL (x' = x: no x_out, no gate, GLU_NORM_PRE only).  H <= 16384, any H and any
+ * row stride >= H; M < 2^31.  stats is FP32 [M, 4], kept for the backward: the mean and the
+ * reciprocal root of y's row, then of x's.
+ * glu_block_norm_mxfp8 writes h as MXFP8 rowwise instead (codes q [M, H], scales s [M, H/32],
+ * byte for byte the library's quantizer applied to the BF16 h): an operand of glu_gemm.
+ * H % 32 == 0 and row strides of x, y and x_out multiples of 8. */
+enum { GLU_NORM_RMS = 0, GLU_NORM_LAYER = 1 };
+enum {
+  GLU_NORM_PRE = 1, GLU_NORM_POST = 2, GLU_NORM_F32_STREAM = 4, GLU_NORM_F32_PARAMS = 8,
+  GLU_NORM_GATE_GROUPED = 16, GLU_NORM_W_GROUPED = 32, GLU_NORM_B_GROUPED = 64
+};
+glu_status glu_block_norm(int kind, int flags, int64_t M, int64_t H, int64_t groups, const void* x, int64_t ld_x,
+                          const uint16_t* y, int64_t ld_y, const void* gate, const void* w_pre,
+                          const void* b_pre, const void* w_post, float res_scale, float eps, void* x_out,
+                          int64_t ld_xo, uint16_t* h, int64_t ld_h, float* stats, void* stream);
+glu_status glu_block_norm_mxfp8(int kind, int flags, int64_t M, int64_t H, int64_t groups, const void* x,
+                                int64_t ld_x, const uint16_t* y, int64_t ld_y, const void* gate,
+                                const void* w_pre, const void* b_pre, const void* w_post, float res_scale,
+                                float eps, void* x_out, int64_t ld_xo, uint8_t* q, uint8_t* s, float* stats,
+                                void* stream);
+
+/* Gradients of x' and h with respect to everything.  dx_out (the stream's type; NULL: zero)
+ * and dh are the gradients of x' and h; dx has the stream's type, dy is BF16, and dgate,
+ * dw_pre, db_pre, dw_post have the parameters' type and shape (NULL: not wanted).  x, y and
+ * the parameters are the forward's.  With M == 0 the parameters' gradients are zero. */
+int64_t glu_block_norm_bwd_work_bytes(int64_t M, int64_t H, int64_t groups);
+glu_status glu_block_norm_bwd(int kind, int flags, int64_t M, int64_t H, int64_t groups, const void* x,
+                              int64_t ld_x, const uint16_t* y, int64_t ld_y, const float* stats,
+                              const void* dx_out, int64_t ld_dxo, const uint16_t* dh, int64_t ld_dh,
+                              const void* gate, const void* w_pre, const void* w_post, float res_scale,
+                              void* dx, int64_t ld_dx, uint16_t* dy, int64_t ld_dy, void* dgate, void* dw_pre,
+                              void* db_pre, void* dw_post, void* work, int64_t work_bytes, void* stream);
+
+/* ---- Linear products
+ *   p = x W^T + b,  y = act(p) + residual
+ * x [M, K], w [groups, N, K] contiguous, bias [groups, N] or NULL, residual [M, N] or NULL,
+ * y [M, N], all BF16; sums, bias, activation and residual in FP32, rounded once.  pre, if not
+ * NULL, receives p as FP16 [M, N] (clamped to the FP16 range) for the backward.
+ * offsets NULL: one W for all rows (groups == 1).  Otherwise int32 [groups + 1] on the device,
+ * non-decreasing, and rows offsets[e] .. offsets[e + 1] - 1 go through W and b number e; rows
+ * outside every group give zero rows of y (and pre), without bias or residual.  Offsets
+ * outside 0 .. M are taken as the nearer end.
+ * N and K are multiples of 8 up to 2^20, row strides multiples of 8, groups <= 1024. */
+enum { GLU_LINEAR_NONE = 0, GLU_LINEAR_SILU = 1, GLU_LINEAR_GELU = 2 /* tanh */, GLU_LINEAR_GELU_ERF = 3 };
+int64_t glu_linear_work_bytes(int64_t M, int64_t N, int64_t K, int64_t groups);
+glu_status glu_linear(int act, int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
+                      const uint16_t* x, int64_t ld_x, const uint16_t* w, const uint16_t* bias,
+                      const uint16_t* residual, int64_t ld_res, uint16_t* y, int64_t ld_y, uint16_t* pre,
+                      void* work, int64_t work_bytes, void* stream);
+
+/* dp = dy act'(p);  dx = dp W,  dw[e] = dp^T x and db[e] = sum of dp over the rows of group e.
+ * pre is the forward's (NULL when act is GLU_LINEAR_NONE).  dx [M, K], dw [groups, N, K],
+ * db [groups, N], BF16, each NULL when not wanted.  The residual's gradient is dy itself.
+ * Rows outside every group give zero rows of dx. */
+int64_t glu_linear_bwd_work_bytes(int act, int64_t M, int64_t N, int64_t K, int64_t groups, int with_bias);
+glu_status glu_linear_bwd(int act, int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
+                          const uint16_t* dy, int64_t ld_dy, const uint16_t* x, int64_t ld_x, const uint16_t* w,
+                          const uint16_t* pre, uint16_t* dx, int64_t ld_dx, uint16_t* dw, uint16_t* db,
+                          void* work, int64_t work_bytes, void* stream);
+
+/* ---- Expert routing
+ * glu_moe_sort: rows[t, j] = the place of choice (t, j) when all choices are sorted by expert,
+ * ties in reading order; -1 where ids[t, j] is no expert number (a dropped choice).  ids is
+ * int32 or int64 (id_bytes 4 or 8) [tokens, choices], rows int32 of that shape, offsets int32
+ * [experts + 1]: expert e has places offsets[e] .. offsets[e + 1] - 1.  experts <= 1024,
+ * tokens * choices < 2^31.
+ * glu_moe_permute: xs[rows[t, j]] = x[t], rows of row_bytes bytes of any type (strides in
+ * bytes); rows of xs [tokens * choices] past offsets[experts] are written as zero.
+ * glu_moe_combine: out[t] = residual[t] + sum over j of weights[t, j] y[rows[t, j]], dropped
+ * choices left out; weights FP32, NULL for ones (then it is the gradient of permute).
+ * glu_moe_combine_bwd: dy[rows[t, j]] = weights[t, j] dout[t], with the rows past
+ * offsets[experts] zero, and dweights[t, j] = <dout[t], y[rows[t, j]]> (0 where dropped). */
+int64_t glu_moe_sort_work_bytes(int64_t tokens, int64_t choices, int experts);
+glu_status glu_moe_sort(int64_t tokens, int64_t choices, int experts, const void* ids, int id_bytes, int32_t* rows,
+                        int32_t* offsets, void* work, int64_t work_bytes, void* stream);
+glu_status glu_moe_permute(int64_t tokens, int64_t choices, int experts, int64_t row_bytes, const void* x,
+                           int64_t ld_x, const int32_t* rows, const int32_t* offsets, void* xs, int64_t ld_xs,
+                           void* stream);
+glu_status glu_moe_combine(int64_t tokens, int64_t choices, int64_t H, const uint16_t* y, int64_t ld_y,
+                           const int32_t* rows, const float* weights, const uint16_t* residual, int64_t ld_res,
+                           uint16_t* out, int64_t ld_out, void* stream);
+glu_status glu_moe_combine_bwd(int64_t tokens, int64_t choices, int64_t H, int experts, const uint16_t* dout,
+                               int64_t ld_dout, const uint16_t* y, int64_t ld_y, const int32_t* rows,
+                               const float* weights, const int32_t* offsets, uint16_t* dy, int64_t ld_dy,
+                               float* dweights, void* stream);
+
+/* Argument checks of the entry points above, as for the others. */
+glu_status glu_check_block_norm(int kind, int flags, int64_t M, int64_t H, int64_t groups, const void* x,
+                                int64_t ld_x, const uint16_t* y, int64_t ld_y, const void* gate,
+                                const void* w_pre, const void* b_pre, const void* w_post, float res_scale,
+                                float eps, void* x_out, int64_t ld_xo, uint16_t* h, int64_t ld_h, float* stats);
+glu_status glu_check_block_norm_mxfp8(int kind, int flags, int64_t M, int64_t H, int64_t groups, const void* x,
+                                      int64_t ld_x, const uint16_t* y, int64_t ld_y, const void* gate,
+                                      const void* w_pre, const void* b_pre, const void* w_post, float res_scale,
+                                      float eps, void* x_out, int64_t ld_xo, uint8_t* q, uint8_t* s, float* stats);
+glu_status glu_check_block_norm_bwd(int kind, int flags, int64_t M, int64_t H, int64_t groups, const void* x,
+                                    int64_t ld_x, const uint16_t* y, int64_t ld_y, const float* stats,
+                                    const void* dx_out, int64_t ld_dxo, const uint16_t* dh, int64_t ld_dh,
+                                    const void* gate, const void* w_pre, const void* w_post, float res_scale,
+                                    void* dx, int64_t ld_dx, uint16_t* dy, int64_t ld_dy, void* dgate,
+                                    void* dw_pre, void* db_pre, void* dw_post, void* work, int64_t work_bytes);
+glu_status glu_check_linear(int act, int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
+                            const uint16_t* x, int64_t ld_x, const uint16_t* w, const uint16_t* bias,
+                            const uint16_t* residual, int64_t ld_res, uint16_t* y, int64_t ld_y, uint16_t* pre,
+                            void* work, int64_t work_bytes);
+glu_status glu_check_linear_bwd(int act, int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
+                                const uint16_t* dy, int64_t ld_dy, const uint16_t* x, int64_t ld_x,
+                                const uint16_t* w, const uint16_t* pre, uint16_t* dx, int64_t ld_dx,
+                                uint16_t* dw, uint16_t* db, void* work, int64_t work_bytes);
+glu_status glu_check_moe_sort(int64_t tokens, int64_t choices, int experts, const void* ids, int id_bytes,
+                              int32_t* rows, int32_t* offsets, void* work, int64_t work_bytes);
+glu_status glu_check_moe_permute(int64_t tokens, int64_t choices, int experts, int64_t row_bytes, const void* x,
+                                 int64_t ld_x, const int32_t* rows, const int32_t* offsets, void* xs,
+                                 int64_t ld_xs);
+glu_status glu_check_moe_combine(int64_t tokens, int64_t choices, int64_t H, const uint16_t* y, int64_t ld_y,
+                                 const int32_t* rows, const float* weights, const uint16_t* residual,
+                                 int64_t ld_res, uint16_t* out, int64_t ld_out);
+glu_status glu_check_moe_combine_bwd(int64_t tokens, int64_t choices, int64_t H, int experts, const uint16_t* dout,
+                                     int64_t ld_dout, const uint16_t* y, int64_t ld_y, const int32_t* rows,
+                                     const float* weights, const int32_t* offsets, uint16_t* dy, int64_t ld_dy,
+                                     float* dweights);
+
 /* Static text for a status code (never NULL). */
 const char* glu_status_string(glu_status status);
 
