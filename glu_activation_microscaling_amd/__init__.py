@@ -100,8 +100,8 @@ for _n, _args in _FFN_SIGNATURES.items():
     _SIGNATURES["glu_check_" + _n] = _args
 _SIZES = {   # functions that give a number of bytes
     "glu_nvfp4_sf_bytes": [_i64, _i64, _int], "glu_mxfp8_sf_bytes": [_i64, _i64, _int],
-    "glu_block_norm_bwd_work_bytes": [_i64, _i64, _i64], "glu_linear_work_bytes": [_i64, _i64, _i64, _i64],
-    "glu_linear_bwd_work_bytes": [_int, _i64, _i64, _i64, _i64, _int],
+    "glu_block_norm_bwd_work_bytes": [_i64, _i64, _i64], "glu_linear_work_bytes": [_i64, _i64, _i64, _i64, _int],
+    "glu_linear_bwd_work_bytes": [_int, _i64, _i64, _i64, _i64, _int, _int],
     "glu_moe_sort_work_bytes": [_i64, _i64, _int],
 }
 

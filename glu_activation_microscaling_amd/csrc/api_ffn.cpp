@@ -119,20 +119,18 @@ glu::NormArgs norm_args(int kind, int flags, int64_t M, int64_t H, int64_t group
 
 bool valid_linear_act(int act) { return act >= GLU_LINEAR_NONE && act <= GLU_LINEAR_GELU_ERF; }
 
-glu_status check_linear_shape(int act, int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets) {
+glu_status check_linear_shape(int act, int64_t M, int64_t N, int64_t K, int64_t groups, bool grouped) {
   if (!valid_linear_act(act)) return GLU_ERR_ARG;
   if (M < 0 || N < 0 || K < 0 || groups < 1 || M > kMaxRows || groups > glu::kMaxExperts) return GLU_ERR_SHAPE;
   if (N % 8 != 0 || K % 8 != 0 || N > kMaxLinearWidth || K > kMaxLinearWidth) return GLU_ERR_SHAPE;
-  if (offsets == nullptr && groups != 1) return GLU_ERR_NULL;
-  if (!aligned4(offsets)) return GLU_ERR_ALIGN;
-  return GLU_OK;
+  return grouped || groups == 1 ? GLU_OK : GLU_ERR_NULL;
 }
 
 // A BF16 matrix operand of the products: 16-byte rows.
 glu_status check_linear_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld) {
   if (rows == 0 || cols == 0) return GLU_OK;
   if (p == nullptr) return GLU_ERR_NULL;
-  if (ld < cols || ld % 8 != 0) return GLU_ERR_STRIDE;
+  if (ld < cols || ld % 8 != 0 || ld > glu::kMaxLinearStride) return GLU_ERR_STRIDE;
   return aligned16(p) ? GLU_OK : GLU_ERR_ALIGN;
 }
 
@@ -264,23 +262,24 @@ glu_status glu_block_norm_bwd(int kind, int flags, int64_t M, int64_t H, int64_t
 
 // ---- linear products -------------------------------------------------------------------------
 
-int64_t glu_linear_work_bytes(int64_t M, int64_t N, int64_t K, int64_t groups) {
-  if (M < 0 || N < 0 || K < 0 || groups < 1) return -1;
-  return glu::linear_work_bytes(M, N, K, groups);
+int64_t glu_linear_work_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, int grouped) {
+  if (check_linear_shape(GLU_LINEAR_NONE, M, N, K, groups, grouped != 0) != GLU_OK) return -1;
+  return glu::linear_work_bytes(M, N, K, groups, grouped != 0);
 }
 
 glu_status glu_check_linear(int act, int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
                             const uint16_t* x, int64_t ld_x, const uint16_t* w, const uint16_t* bias,
                             const uint16_t* residual, int64_t ld_res, uint16_t* y, int64_t ld_y, uint16_t* pre,
                             void* work, int64_t work_bytes) {
-  glu_status st = check_linear_shape(act, M, N, K, groups, offsets);
+  glu_status st = check_linear_shape(act, M, N, K, groups, offsets != nullptr);
   if (st != GLU_OK || M == 0 || N == 0) return st;
+  if (!aligned4(offsets)) return GLU_ERR_ALIGN;
   if ((st = check_linear_matrix(x, M, K, ld_x)) != GLU_OK) return st;
   if ((st = check_linear_matrix(w, groups * N, K, K)) != GLU_OK) return st;
   if ((st = check_linear_matrix(y, M, N, ld_y)) != GLU_OK) return st;
   if (residual != nullptr && (st = check_linear_matrix(residual, M, N, ld_res)) != GLU_OK) return st;
   if (!aligned16(bias) || !aligned16(pre) || !aligned16(work)) return GLU_ERR_ALIGN;
-  const int64_t need = glu_linear_work_bytes(M, N, K, groups);
+  const int64_t need = glu::linear_work_bytes(M, N, K, groups, offsets != nullptr);
   if (need > 0 && work == nullptr) return GLU_ERR_NULL;
   if (need > work_bytes) return GLU_ERR_SHAPE;
   const Operand X = mat(x, M, K, ld_x, 2), W = mat(w, groups * N, K, K, 2), B = mat(bias, groups, N, N, 2),
@@ -302,17 +301,19 @@ glu_status glu_linear(int act, int64_t M, int64_t N, int64_t K, int64_t groups, 
   return status_of(glu::launch_linear(a, (hipStream_t)stream));
 }
 
-int64_t glu_linear_bwd_work_bytes(int act, int64_t M, int64_t N, int64_t K, int64_t groups, int with_bias) {
-  if (!valid_linear_act(act) || M < 0 || N < 0 || K < 0 || groups < 1) return -1;
-  return glu::linear_bwd_work_bytes(act, M, N, K, groups, with_bias != 0);
+int64_t glu_linear_bwd_work_bytes(int act, int64_t M, int64_t N, int64_t K, int64_t groups, int grouped,
+                                  int with_bias) {
+  if (check_linear_shape(act, M, N, K, groups, grouped != 0) != GLU_OK) return -1;
+  return glu::linear_bwd_work_bytes(act, M, N, K, groups, grouped != 0, with_bias != 0);
 }
 
 glu_status glu_check_linear_bwd(int act, int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
                                 const uint16_t* dy, int64_t ld_dy, const uint16_t* x, int64_t ld_x,
                                 const uint16_t* w, const uint16_t* pre, uint16_t* dx, int64_t ld_dx,
                                 uint16_t* dw, uint16_t* db, void* work, int64_t work_bytes) {
-  glu_status st = check_linear_shape(act, M, N, K, groups, offsets);
+  glu_status st = check_linear_shape(act, M, N, K, groups, offsets != nullptr);
   if (st != GLU_OK) return st;
+  if (!aligned4(offsets)) return GLU_ERR_ALIGN;
   if ((st = check_linear_matrix(dy, M, N, ld_dy)) != GLU_OK) return st;
   if (act != GLU_LINEAR_NONE && M > 0 && N > 0 && pre == nullptr) return GLU_ERR_NULL;
   if (act == GLU_LINEAR_NONE && pre != nullptr) return GLU_ERR_ARG;
@@ -322,7 +323,7 @@ glu_status glu_check_linear_bwd(int act, int64_t M, int64_t N, int64_t K, int64_
   }
   if (dw != nullptr && (st = check_linear_matrix(x, M, K, ld_x)) != GLU_OK) return st;
   if (!aligned16(pre) || !aligned16(dw) || !aligned16(db) || !aligned16(work)) return GLU_ERR_ALIGN;
-  const int64_t need = glu::linear_bwd_work_bytes(act, M, N, K, groups, db != nullptr);
+  const int64_t need = glu::linear_bwd_work_bytes(act, M, N, K, groups, offsets != nullptr, db != nullptr);
   if (need > 0 && work == nullptr) return GLU_ERR_NULL;
   if (need > work_bytes) return GLU_ERR_SHAPE;
   const Operand DY = mat(dy, M, N, ld_dy, 2), X = mat(dw ? x : nullptr, M, K, ld_x, 2),

@@ -77,6 +77,7 @@ constexpr int64_t kMaxNormWidth = 16384;
 // ---- expert routing ----------------------------------------------------------------------
 
 constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxLinearStride = (int64_t)1 << 21;   // 256 rows stay within 32-bit offsets
 
 struct MoeSortArgs {
   int64_t n;                 // choices, tokens x choices per token
@@ -164,8 +165,8 @@ struct LinearBwdArgs {
   uint16_t* db;              // [groups, N], or null
   uint8_t* work;
 };
-int64_t linear_work_bytes(int64_t M, int64_t N, int64_t K, int64_t groups);
-int64_t linear_bwd_work_bytes(int act, int64_t M, int64_t N, int64_t K, int64_t groups, bool bias);
+int64_t linear_work_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, bool grouped);
+int64_t linear_bwd_work_bytes(int act, int64_t M, int64_t N, int64_t K, int64_t groups, bool grouped, bool bias);
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t s);

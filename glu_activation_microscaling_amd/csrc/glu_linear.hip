@@ -75,128 +75,528 @@ struct ProductArgs {
   const uint16_t* residual;
   int64_t ld_res;
   uint16_t* pre;             // [I, J]
+  float* work;               // split sums: [parts, rows of C, J]
 };
 
-constexpr int BI = 128, BJ = 128, BK = 32, PAD = 8, PROD_THREADS = 256;
-
-// Finds the group and the row tile of tile number t when groups are cut into tiles of BI rows
-// one by one; past the last group, the rows after it are tiled as group `groups`.
+// Finds the group and the rows of row tile t when each group's rows are cut into tiles of
+// `size`, group after group; the rows after the last group count as group `groups`.  group is
+// -1 past the last tile.  64 groups are looked at together, one a lane.
 struct RowTile {
   int64_t group, i0, i1;
 };
+// The value of lane `at` (a wave-uniform lane), as a wave-uniform value.
+__device__ __forceinline__ int64_t lane_value(int64_t v, int at) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)v, at), hi = __builtin_amdgcn_readlane((int)(v >> 32), at);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ RowTile find_tile(const int32_t* off, int64_t groups, int64_t I, int64_t t, int64_t size) {
-  if (off == nullptr) return {0, t * size, min((t + 1) * size, I)};
-  for (int64_t e = 0; e <= groups; e++) {
-    const int64_t a = e == 0 ? 0 : min((int64_t)max(off[e], 0), I);
-    const int64_t b = e == groups ? I : max(a, min((int64_t)off[e + 1], I));
-    const int64_t n = (b - a + size - 1) / size;
-    if (t < n) return {e, a + t * size, min(a + (t + 1) * size, b)};
-    t -= n;
+  if (off == nullptr) return {t * size < I ? 0 : -1, t * size, min((t + 1) * size, I)};
+  const int lane = threadIdx.x & 63;
+  int64_t first = 0;   // tiles of the groups before this batch
+  for (int64_t e0 = 0; e0 <= groups; e0 += 64) {
+    const int64_t e = e0 + lane;
+    int64_t a = 0, b = 0;
+    if (e <= groups) {
+      a = e == 0 ? 0 : min((int64_t)max(off[e], 0), I);
+      b = e == groups ? I : max(a, min((int64_t)off[e + 1], I));
+    }
+    int64_t n = (b - a + size - 1) / size;
+    const int64_t own = n;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t v = __shfl_up(n, d);
+      if (lane >= d) n += v;
+    }
+    const uint64_t hit = __ballot(t < first + n && t >= first + n - own);
+    if (hit != 0) {
+      const int at = __builtin_ctzll(hit);
+      const int64_t i0 = a + (t - (first + n - own)) * size;
+      return {e0 + at, lane_value(i0, at), lane_value(min(i0 + size, b), at)};
+    }
+    first += lane_value(n, 63);
   }
   return {-1, 0, 0};
 }
 
-// Loads a BI x BK tile of an operand into LDS rows of BK elements (k contiguous): 8 elements
-// a thread and step along the operand's contiguous dimension.  Rows i0 .. i1 - 1 and k below
-// k1 exist; the rest reads zero.
-template <bool T>
-__device__ __forceinline__ void load_tile(uint16_t (*lds)[BK + PAD], const uint16_t* p, int64_t ld, int64_t i0,
-                                          int64_t i1, int64_t k0, int64_t k1) {
-  for (int c = threadIdx.x; c < BI * BK / 8; c += PROD_THREADS) {
-    u32x4 v = (u32x4)0u;
+// s_waitcnt on the vector-memory counter alone (gfx9 encoding: vmcnt in bits 3:0 and 15:14).
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+// s_waitcnt lgkmcnt(0) alone.
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// A pointer that is the same in every lane, held in scalar registers.
+__device__ __forceinline__ const uint16_t* uniform(const uint16_t* p) {
+  const uint64_t v = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (const uint16_t*)((uint64_t)hi << 32 | lo);
+}
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+
+constexpr uint32_t BK = 64;   // elements of the sum per step: one 128-byte line of a row
+
+// One operand of a tile: B_ rows of the operand by BK elements of the sum per step, copied
+// straight into LDS in blocks of 1 KiB (16 bytes a lane) and read back as 16 x 32 fragments
+// (lane r + 16 g: row r, elements 8 g .. 8 g + 7).
+//   k along rows (T = false): a row's 128 bytes hold its BK elements; 16-byte chunk c of row R
+//     lies at chunk c ^ (R / 2 % 8), so a fragment read touches every LDS bank once.
+//   transposed (T = true): an LDS row holds one element of the sum for all B_ rows; its
+//     32-byte segment s of element k lies at segment s ^ (k % 8), and the fragment is
+//     gathered by two transposing reads of 4 elements each (16 lanes take a 4 x 16 block).
+template <bool T, int B_, int WAVES>
+struct Operand {
+  static constexpr int LOADS = B_ * BK * 2 / 1024 / WAVES;     // 1 KiB blocks per wave and step
+  static constexpr uint32_t BYTES = B_ * BK * 2;
+  static_assert(LOADS >= 1 && LOADS * WAVES * 1024 == (int)BYTES);
+  uint32_t off[LOADS];       // byte offset of the lane's 16 bytes from the tile's base
+  uint32_t kk;               // T: the lane's element of the sum in block 0; else its first one
+  const uint16_t* base;
+  int64_t ld;
+
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld_, int64_t i0, int64_t i1, uint32_t wave,
+                                       uint32_t lane) {
+    ld = ld_;
     if constexpr (!T) {
-      const int i = c / (BK / 8), k = c % (BK / 8) * 8;
-      if (i0 + i < i1 && k0 + k < k1) v = *reinterpret_cast<const u32x4*>(p + (i0 + i) * ld + k0 + k);
-      *reinterpret_cast<u32x4*>(&lds[i][k]) = v;
-    } else {
-      const int k = c / (BI / 8), i = c % (BI / 8) * 8;
-      if (i0 + i < i1 && k0 + k < k1) v = *reinterpret_cast<const u32x4*>(p + (k0 + k) * ld + i0 + i);
+      base = uniform(p + i0 * ld);
+      const uint32_t lrow = lane >> 3;
 #pragma unroll
-      for (int j = 0; j < 8; j++) lds[i + j][k] = (uint16_t)(v[j / 2] >> (16 * (j & 1)));
+      for (int q = 0; q < LOADS; q++) {
+        const uint32_t row = 8u * (wave * LOADS + q) + lrow;
+        const uint32_t chunk = (lane & 7u) ^ ((row >> 1) & 7u);
+        off[q] = i0 + row < i1 ? 2u * (row * (uint32_t)ld + 8u * chunk) : kOob;
+      }
+      // the chunk depends on the row through (row / 2) % 8 = 4 (block % 2) + lrow / 2
+      kk = 0;
+    } else {
+      base = uniform(p + i0);
+      constexpr uint32_t CH = B_ / 8;                             // chunks per LDS row
+#pragma unroll
+      for (int q = 0; q < LOADS; q++) {
+        const uint32_t k = (wave * LOADS + q) * (64u / CH) + lane / CH;
+        const uint32_t chunk = (lane % CH) ^ (2u * (k & 7u));
+        off[q] = i0 + 8u * chunk < i1 ? 2u * (k * (uint32_t)ld + 8u * chunk) : kOob;
+      }
+      kk = wave * LOADS * (64u / CH) + lane / CH;
+    }
+  }
+  // Starts load q of the step at element k of the sum; elements at and past k1 read zero.
+  __device__ __forceinline__ void issue(int q, uint32_t k, uint32_t k1, uint8_t* lds, uint32_t wave, uint32_t lane) const {
+    uint32_t o = off[q];
+    if (k + BK > k1) {       // the last step of a sum that is no multiple of BK
+      uint32_t mine;
+      if constexpr (!T) {
+        const uint32_t row = 8u * (wave * LOADS + q) + (lane >> 3);
+        mine = 8u * ((lane & 7u) ^ ((row >> 1) & 7u));
+      } else {
+        mine = kk + q * (64u / (B_ / 8));
+      }
+      if (k + mine >= k1) o = kOob;
+    }
+    const auto r = rsrc(T ? base + k * ld : base + k);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(lds + (wave * LOADS + q) * 1024u), 16, o, 0, 0, 0);
+  }
+};
+
+// Four elements of a 4 x 16 block (per 16 lanes) of 16-bit values in LDS, transposed.  The
+// restricted pointer tells the compiler that no copy into LDS that is under way writes here;
+// without it every such read would wait for all of them.
+__device__ __forceinline__ v4s transposed(const uint8_t* __restrict__ p) {
+  typedef __attribute__((address_space(3))) v4s* tr_ptr;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr)p);
+}
+
+// A lane's fragment addresses of an operand in LDS.  Wave w of W along this operand owns TILES
+// tiles of 16 rows: consecutive ones, or, transposed, every W-th one (tile i of the wave is tile
+// i W + w).  With that, the segment of tile i and element 8 g + 4 u + q is
+//   (i W + w) ^ (4 u + q) = 4 (i / (4 / W) ^ u) + ((i % (4 / W)) W + w) ^ q,
+// whose first part is a constant of the unrolled code and whose second takes 4 / W values.
+template <bool T, int B_, int W, int TILES>
+struct Fragments {
+  static constexpr int BASES = 4 / W;
+  uint32_t at[2];
+  static __device__ __forceinline__ uint32_t tile(uint32_t w, int i) { return T ? i * W + w : w * TILES + i; }
+  __device__ __forceinline__ void init(uint32_t w, uint32_t lane) {
+    const uint32_t g = lane >> 4, r = lane & 15u;
+    if constexpr (!T) {
+#pragma unroll
+      for (uint32_t h = 0; h < 2; h++) at[h] = 128u * (16u * TILES * w + r) + 16u * ((4u * h + g) ^ ((r >> 1) & 7u));
+    } else {
+      const uint32_t q = r >> 2;
+#pragma unroll
+      for (uint32_t m = 0; m < BASES; m++)
+        at[m] = (8u * g + q) * (2u * B_) + 32u * ((m * W + w) ^ q) + 8u * (r & 3u);
+    }
+  }
+  __device__ __forceinline__ v8bf read(const uint8_t* lds, int i, int h) const {
+    if constexpr (!T) {
+      return *reinterpret_cast<const v8bf*>(lds + at[h] + 2048u * i);
+    } else {
+      const uint8_t* p = lds + at[i % BASES] + 2u * B_ * 32u * h;
+      const v4s lo = transposed(p + 128 * (i / BASES));
+      const v4s hi = transposed(p + 8 * B_ + 128 * ((i / BASES) ^ 1));
+      return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+
+// Workgroup b of n: those of one XCD (b mod 8) get a contiguous run.
+__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n) {
+  const uint32_t per = n / 8u;
+  return b < 8u * per ? (b % 8u) * per + b / 8u : b;
+}
+
+constexpr uint32_t GROUP_I = 8;   // row tiles per group of the tile order
+
+// Epilogue of four consecutive columns of one row.
+template <int MODE, int ACT>
+__device__ __forceinline__ void finish(const ProductArgs& a, int64_t group, int64_t row, int64_t col, float (&v)[4]) {
+  if constexpr (MODE == FWD) {
+    if (group < a.groups) {
+      if (a.bias != nullptr) {
+        const u32x2 b = *reinterpret_cast<const u32x2*>(a.bias + group * a.J + col);
+        v[0] += bf_lo(b.x);
+        v[1] += bf_hi(b.x);
+        v[2] += bf_lo(b.y);
+        v[3] += bf_hi(b.y);
+      }
+      if (a.pre != nullptr) {
+        uint32_t p[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          p[e] = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_fmed3f(v[e], -65504.0f, 65504.0f));
+        *reinterpret_cast<u32x2*>(a.pre + row * a.J + col) = (u32x2){p[0] | p[1] << 16, p[2] | p[3] << 16};
+      }
+#pragma unroll
+      for (int e = 0; e < 4; e++) v[e] = act_of<ACT>(v[e]);
+      if (a.residual != nullptr) {
+        const u32x2 b = *reinterpret_cast<const u32x2*>(a.residual + row * a.ld_res + col);
+        v[0] += bf_lo(b.x);
+        v[1] += bf_hi(b.x);
+        v[2] += bf_lo(b.y);
+        v[3] += bf_hi(b.y);
+      }
+    } else if (a.pre != nullptr) {
+      *reinterpret_cast<u32x2*>(a.pre + row * a.J + col) = (u32x2){0u, 0u};
+    }
+  }
+  uint16_t* c = a.c + (MODE == WGRAD ? group * a.c_group : 0) + row * a.ld_c + col;
+  *reinterpret_cast<u32x2*>(c) = (u32x2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+}
+
+// WI x WJ waves of TI x TJ tiles of 16 x 16 each: a tile of 16 WI TI rows by 16 WJ TJ columns.
+//
+// Two LDS stages, each a step of BK elements.  A step's matrix work runs in two halves of 32
+// elements.  While the first half multiplies, the second half's fragments are read; then one
+// barrier says both that every wave has read the stage and that the next stage has landed;
+// the loads of the step after next go into the stage just freed and the next stage's first
+// fragments are read while the second half multiplies.  A load so has a whole step to arrive.
+template <int MODE, int ACT, int WI, int WJ, int TI, int TJ>
+__global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_t tiles_i, uint32_t tiles_j,
+                                                          uint32_t splits) {
+  constexpr bool TA = MODE == WGRAD, TB = MODE != FWD;
+  constexpr int BI = 16 * WI * TI, BJ = 16 * WJ * TJ, WAVES = WI * WJ;
+  using OpA = Operand<TA, BI, WAVES>;
+  using OpB = Operand<TB, BJ, WAVES>;
+  // both stages of A, then both of B: every fragment read's place is within the 16-bit offset
+  // of a read instruction from the lane's base
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * (OpA::BYTES + OpB::BYTES)];
+  const uint32_t lane = threadIdx.x & 63u;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // this workgroup's tile: contiguous runs per XCD; a run goes down GROUP_I row tiles before the
+  // next column tile, so that the workgroups of one XCD share operands in its L2
+  const uint32_t per = tiles_i * tiles_j;
+  uint32_t b = xcd_run(blockIdx.x, gridDim.x);
+  const uint32_t outer = b / per;          // WGRAD: group; with splits: part of the sum
+  b -= outer * per;
+  const uint32_t in_group = GROUP_I * tiles_j, first_i = b / in_group * GROUP_I;
+  const uint32_t gi = min(tiles_i - first_i, GROUP_I);
+  const uint32_t ti = first_i + b % in_group % gi, tj = b % in_group / gi;
+
+  RowTile t;
+  int64_t group;
+  uint32_t k0 = 0, k1 = (uint32_t)a.K, part = 0;
+  if constexpr (MODE == WGRAD) {
+    group = outer / splits;
+    part = outer % splits;
+    if (a.offsets != nullptr) {
+      k0 = min((uint32_t)max(a.offsets[group], 0), k1);
+      k1 = max(k0, min((uint32_t)max(a.offsets[group + 1], 0), k1));
+    }
+    t = {group, (int64_t)ti * BI, min((int64_t)(ti + 1) * BI, a.I)};
+  } else {
+    t = find_tile(a.offsets, a.groups, a.I, ti, BI);
+    if (t.group < 0) return;
+    group = t.group;
+    part = outer;
+    if (group == a.groups) k1 = 0;   // rows of no group
+  }
+  if (splits > 1) {                  // whole steps to each part
+    const uint32_t steps = (k1 - k0 + BK - 1) / BK;
+    const uint32_t s0 = steps * part / splits, s1 = steps * (part + 1) / splits;
+    k1 = min(k1, k0 + s1 * BK);
+    k0 += s0 * BK;
+  }
+  const int64_t j0 = (int64_t)tj * BJ, j1 = min(j0 + BJ, a.J);
+  const uint32_t wi = wave / WJ, wj = wave % WJ;
+
+  OpA oa;
+  OpB ob;
+  oa.init(a.a, a.ld_a, t.i0, t.i1, wave, lane);
+  ob.init(a.b + group * a.b_group, a.ld_b, j0, j1, wave, lane);
+  if (MODE != WGRAD && group == a.groups) ob.base = a.b;
+  using FrA = Fragments<TA, BI, WI, TI>;
+  using FrB = Fragments<TB, BJ, WJ, TJ>;
+  FrA fa;
+  FrB fb;
+  fa.init(wi, lane);
+  fb.init(wj, lane);
+
+  v4f acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; i++)
+#pragma unroll
+    for (int j = 0; j < TJ; j++) acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+
+  uint8_t *const sa = smem, *const sb = smem + 2 * OpA::BYTES;
+  auto issue = [&](uint32_t k, int stage) {
+#pragma unroll
+    for (int q = 0; q < OpA::LOADS; q++) oa.issue(q, k, k1, sa + stage * OpA::BYTES, wave, lane);
+#pragma unroll
+    for (int q = 0; q < OpB::LOADS; q++) ob.issue(q, k, k1, sb + stage * OpB::BYTES, wave, lane);
+  };
+  v8bf xa[2][TI], xb[2][TJ];
+  auto read = [&](int stage, int h) {
+#pragma unroll
+    for (int i = 0; i < TI; i++) xa[h][i] = fa.read(sa + stage * OpA::BYTES, i, h);
+#pragma unroll
+    for (int j = 0; j < TJ; j++) xb[h][j] = fb.read(sb + stage * OpB::BYTES, j, h);
+  };
+  auto multiply = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < TI; i++)
+#pragma unroll
+      for (int j = 0; j < TJ; j++)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[h][j], xa[h][i], acc[i][j], 0, 0, 0);
+  };
+  auto step = [&](uint32_t k, int stage) {
+    read(stage, 1);
+    multiply(0);
+    __builtin_amdgcn_sched_barrier(0);   // the products above are not to sink below the wait
+    wait_vm<0>();
+    lds_barrier();
+    if (k + 2 * BK < k1) issue(k + 2 * BK, stage);
+    if (k + BK < k1) read(1 - stage, 0);
+    multiply(1);
+    __builtin_amdgcn_sched_barrier(0);
+    wait_lds();   // long since arrived; said here so that the loop's head waits for no more
+  };
+
+  if (k0 < k1) {
+    issue(k0, 0);
+    wait_vm<0>();
+    lds_barrier();
+    if (k0 + BK < k1) issue(k0 + BK, 1);
+    read(0, 0);
+    for (uint32_t k = k0; k < k1; k += 2 * BK) {
+      step(k, 0);
+      if (k + BK < k1) step(k + BK, 1);
+    }
+  }
+
+  // acc[i][j][e] is C at row r of its row tile and column 4 g + e of its column tile
+  const uint32_t g = lane >> 4, r = lane & 15u;
+#pragma unroll
+  for (int i = 0; i < TI; i++) {
+    const int64_t row = t.i0 + 16u * FrA::tile(wi, i) + r;
+    if (row >= t.i1) continue;
+#pragma unroll
+    for (int j = 0; j < TJ; j++) {
+      const int64_t col = j0 + 16u * FrB::tile(wj, j) + 4u * g;
+      if (col >= j1) continue;
+      if (splits > 1) {
+        const int64_t gr = MODE == WGRAD ? group * a.I + row : row;
+        const int64_t rows = MODE == WGRAD ? a.groups * a.I : a.I;
+        *reinterpret_cast<v4f*>(a.work + (part * rows + gr) * a.J + col) = acc[i][j];
+      } else {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] = acc[i][j][e];
+        finish<MODE, ACT>(a, group, row, col, v);
+      }
     }
   }
 }
 
-// grid: (row tiles, column tiles, groups for WGRAD).  Four waves, 64 x 64 of C each.
+// Joins the parts of split sums and finishes them: four columns a thread.
 template <int MODE, int ACT>
-__global__ __launch_bounds__(PROD_THREADS) void k_product(ProductArgs a) {
-  constexpr bool TA = MODE == WGRAD, TB = MODE != FWD;
-  __shared__ __attribute__((aligned(16))) uint16_t sa[BI][BK + PAD], sb[BJ][BK + PAD];
-  RowTile t;
-  int64_t group, k0 = 0, k1 = a.K;
-  if constexpr (MODE == WGRAD) {
-    group = blockIdx.z;
-    if (a.offsets != nullptr) {
-      k0 = min((int64_t)max(a.offsets[group], 0), a.K);
-      k1 = max(k0, min((int64_t)a.offsets[group + 1], a.K));
-    }
-    t = {group, (int64_t)blockIdx.x * BI, min((int64_t)(blockIdx.x + 1) * BI, a.I)};
-  } else {
-    t = find_tile(a.offsets, a.groups, a.I, blockIdx.x, BI);
-    if (t.group < 0) return;
-    group = t.group;
-    if (group == a.groups) k1 = 0;   // rows of no group
+__global__ __launch_bounds__(256) void k_product_join(ProductArgs a, uint32_t splits) {
+  const int64_t rows = MODE == WGRAD ? a.groups * a.I : a.I, n = rows * a.J / 4;
+  for (int64_t q = 256 * (int64_t)blockIdx.x + threadIdx.x; q < n; q += 256 * (int64_t)gridDim.x) {
+    const int64_t row = q / (a.J / 4), col = 4 * (q % (a.J / 4));
+    v4f s = *reinterpret_cast<const v4f*>(a.work + row * a.J + col);
+    for (uint32_t p = 1; p < splits; p++) s += *reinterpret_cast<const v4f*>(a.work + (p * rows + row) * a.J + col);
+    float v[4] = {s[0], s[1], s[2], s[3]};
+    finish<MODE, ACT>(a, MODE == WGRAD ? row / a.I : 0, MODE == WGRAD ? row % a.I : row, col, v);
   }
-  const int64_t j0 = (int64_t)blockIdx.y * BJ, j1 = min(j0 + BJ, a.J);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, r = lane & 15;
-  const int wi = 64 * (wave >> 1), wj = 64 * (wave & 1);
-  const uint16_t* B = a.b + group * a.b_group;
-  v4f acc[4][4];
+}
+
+// ---- few rows --------------------------------------------------------------------------------
+
+// The forward for a few rows (up to 64 of one group): a pass over W at memory speed.  A
+// workgroup takes 16 rows of W (columns of C); its waves take chunks of 128 elements of the sum
+// in turn, straight from memory into registers, multiply them as 16 x 16 x 32 tiles against 16,
+// 32, 48 or 64 rows of x, and join their sums through LDS.
+constexpr int FEW_WAVES = 8, FEW_ROWS = 64, FEW_CHUNK = 128;
+
+template <int RT>
+__device__ __forceinline__ void few_rows_sum(const ProductArgs& a, const RowTile& t, int64_t n0, int64_t k0, int64_t k1,
+                                             uint32_t lane, uint32_t wave, v4f (&acc)[4]) {
+  constexpr int UNROLL = RT <= 1 ? 4 : 2;   // chunks in flight
+  const uint32_t g = lane >> 4, r = lane & 15u;
+  const uint32_t wo = n0 + r < a.J ? 2u * (r * (uint32_t)a.ld_b + 8u * g) : kOob;
+  uint32_t xo[RT];
+#pragma unroll
+  for (int i = 0; i < RT; i++)
+    xo[i] = t.i0 + 16 * i + r < t.i1 ? 2u * ((16u * i + r) * (uint32_t)a.ld_a + 8u * g) : kOob;
+  const auto rw = rsrc(a.b + t.group * a.b_group + n0 * a.ld_b), rx = rsrc(a.a + t.i0 * a.ld_a);
+  for (int64_t k = k0 + FEW_CHUNK * wave; k < k1; k += FEW_CHUNK * FEW_WAVES * UNROLL) {
+    v8bf w[UNROLL][4], x[UNROLL][4][RT];
+#pragma unroll
+    for (int c = 0; c < UNROLL; c++) {
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        const int64_t kk = k + FEW_CHUNK * FEW_WAVES * c + 32 * u;
+        const bool in = kk + 8 * g < k1;
+        w[c][u] = __builtin_bit_cast(v8bf, __builtin_amdgcn_raw_buffer_load_b128(rw, in ? wo : kOob, (int)(2 * kk), 0));
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+          x[c][u][i] =
+              __builtin_bit_cast(v8bf, __builtin_amdgcn_raw_buffer_load_b128(rx, in ? xo[i] : kOob, (int)(2 * kk), 0));
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < UNROLL; c++)
+#pragma unroll
+      for (int u = 0; u < 4; u++)
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[c][u], x[c][u][i], acc[i], 0, 0, 0);
+  }
+}
+
+// grid: (16-column tiles, row tiles, parts of the sum)
+template <int ACT>
+__global__ __launch_bounds__(64 * FEW_WAVES) void k_few_rows(ProductArgs a) {
+  __shared__ v4f sums[FEW_WAVES][FEW_ROWS / 16][64];
+  const uint32_t lane = threadIdx.x & 63u;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const RowTile t = find_tile(a.offsets, a.groups, a.I, blockIdx.y, FEW_ROWS);
+  if (t.group < 0) return;
+  const int64_t n0 = 16 * (int64_t)blockIdx.x;
+  int64_t k0 = 0, k1 = t.group < a.groups ? a.K : 0;
+  if (gridDim.z > 1) {
+    const int64_t chunks = (k1 + FEW_CHUNK - 1) / FEW_CHUNK;
+    k0 = chunks * blockIdx.z / gridDim.z * FEW_CHUNK;
+    k1 = min(k1, chunks * (blockIdx.z + 1) / gridDim.z * FEW_CHUNK);
+  }
+  const int rt = (int)((t.i1 - t.i0 + 15) / 16);
+  v4f acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) acc[i] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+  if (k0 < k1) {
+    if (rt == 1) few_rows_sum<1>(a, t, n0, k0, k1, lane, wave, acc);
+    else if (rt == 2) few_rows_sum<2>(a, t, n0, k0, k1, lane, wave, acc);
+    else if (rt == 3) few_rows_sum<3>(a, t, n0, k0, k1, lane, wave, acc);
+    else few_rows_sum<4>(a, t, n0, k0, k1, lane, wave, acc);
+  }
 #pragma unroll
   for (int i = 0; i < 4; i++)
+    if (i < rt) sums[wave][i][lane] = acc[i];
+  __syncthreads();
+  const int i = threadIdx.x >> 6;
+  if (i >= rt) return;
+  v4f s = sums[0][i][lane];
 #pragma unroll
-    for (int j = 0; j < 4; j++) acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t k = k0; k < k1; k += BK) {
-    load_tile<TA>(sa, a.a, a.ld_a, t.i0, t.i1, k, k1);
-    load_tile<TB>(sb, B, a.ld_b, j0, j1, k, k1);
-    __syncthreads();
-    v8bf fa[4], fb[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) fa[i] = *reinterpret_cast<const v8bf*>(&sa[wi + 16 * i + r][8 * g]);
-#pragma unroll
-    for (int j = 0; j < 4; j++) fb[j] = *reinterpret_cast<const v8bf*>(&sb[wj + 16 * j + r][8 * g]);
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-      for (int j = 0; j < 4; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
-    __syncthreads();
+  for (int w = 1; w < FEW_WAVES; w++) s += sums[w][i][lane];
+  const int64_t row = t.i0 + 16 * i + (lane & 15u), col = n0 + 4 * (lane >> 4);
+  if (row >= t.i1 || col >= a.J) return;
+  if (gridDim.z > 1) {
+    *reinterpret_cast<v4f*>(a.work + ((int64_t)blockIdx.z * a.I + row) * a.J + col) = s;
+  } else {
+    float v[4] = {s[0], s[1], s[2], s[3]};
+    finish<FWD, ACT>(a, t.group, row, col, v);
   }
-  // acc[i][j][e] is C at row wi + 16 i + r, column wj + 16 j + 4 g + e of the tile
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int64_t row = t.i0 + wi + 16 * i + r;
-    if (row >= t.i1) continue;
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const int64_t col = j0 + wj + 16 * j + 4 * g;
-      if (col >= j1) continue;
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; e++) v[e] = acc[i][j][e];
-      if constexpr (MODE == FWD) {
-        if (group < a.groups) {
-          if (a.bias != nullptr)
-#pragma unroll
-            for (int e = 0; e < 4; e++) v[e] += bf_lo(a.bias[group * a.J + col + e]);
-          if (a.pre != nullptr)
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-              a.pre[row * a.J + col + e] =
-                  __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_fmed3f(v[e], -65504.0f, 65504.0f));
-#pragma unroll
-          for (int e = 0; e < 4; e++) v[e] = act_of<ACT>(v[e]);
-          if (a.residual != nullptr)
-#pragma unroll
-            for (int e = 0; e < 4; e++) v[e] += bf_lo(a.residual[row * a.ld_res + col + e]);
-        } else if (a.pre != nullptr) {
-#pragma unroll
-          for (int e = 0; e < 4; e++) a.pre[row * a.J + col + e] = 0;
-        }
-      }
-      uint16_t* c = a.c + (MODE == WGRAD ? group * a.c_group : 0) + row * a.ld_c + col;
-      *reinterpret_cast<u32x2*>(c) = (u32x2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+}
+
+// ---- which kernel ----------------------------------------------------------------------------
+
+enum { TILE_256, TILE_128, FEW };
+struct ProductPlan {
+  int kind;
+  int64_t tiles_i, tiles_j, splits;
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A rule on extents alone, so that the scratch memory of split sums can be sized before the
+// launch.
+ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped) {
+  ProductPlan p{};
+  p.splits = 1;
+  if (mode == FWD && I <= (grouped ? FEW_ROWS / 2 * groups : FEW_ROWS)) {
+    p.kind = FEW;
+    p.tiles_i = ceil_div(I, FEW_ROWS) + (grouped ? groups : 0);
+    p.tiles_j = ceil_div(J, 16);
+    if (!grouped && p.tiles_j < 256) {
+      const int64_t most = K / (2 * FEW_WAVES * FEW_CHUNK), want = ceil_div(256, p.tiles_j);
+      p.splits = want < most ? want : most;
+    }
+  } else {
+    const int64_t extra = grouped && mode != WGRAD ? groups : 0, outer = mode == WGRAD ? groups : 1;
+    auto tiles = [&](int64_t b) { return (ceil_div(I, b) + extra) * ceil_div(J, b) * outer; };
+    p.kind = tiles(256) >= 192 ? TILE_256 : TILE_128;
+    const int64_t b = p.kind == TILE_256 ? 256 : 128;
+    p.tiles_i = ceil_div(I, b) + extra;
+    p.tiles_j = ceil_div(J, b);
+    if (!grouped && p.kind == TILE_128) {
+      const int64_t most = K / 512, want = 512 / tiles(128);
+      p.splits = want < most ? want : most;
     }
   }
+  if (p.splits < 1) p.splits = 1;
+  return p;
+}
+
+int64_t product_work_bytes(int mode, int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped) {
+  const ProductPlan p = plan_product(mode, I, J, K, groups, grouped);
+  return p.splits > 1 ? 4 * p.splits * (mode == WGRAD ? groups : 1) * I * J : 0;
+}
+
+template <int MODE, int ACT>
+hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
+  const ProductPlan p = plan_product(MODE, a.I, a.J, a.K, a.groups, a.offsets != nullptr);
+  hipError_t e;
+  if (p.kind == FEW) {
+    e = launch_kernel(k_few_rows<ACT>, dim3((unsigned)p.tiles_j, (unsigned)p.tiles_i, (unsigned)p.splits),
+                      dim3(64 * FEW_WAVES), s, a);
+  } else {
+    const unsigned n = (unsigned)(p.tiles_i * p.tiles_j * p.splits * (MODE == WGRAD ? a.groups : 1));
+    e = p.kind == TILE_256
+            ? launch_kernel(k_product<MODE, ACT, 2, 4, 8, 4>, dim3(n), dim3(512), s, a, (uint32_t)p.tiles_i,
+                            (uint32_t)p.tiles_j, (uint32_t)p.splits)
+            : launch_kernel(k_product<MODE, ACT, 2, 2, 4, 4>, dim3(n), dim3(256), s, a, (uint32_t)p.tiles_i,
+                            (uint32_t)p.tiles_j, (uint32_t)p.splits);
+  }
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t quads = (MODE == WGRAD ? a.groups : 1) * a.I * a.J / 4;
+  return launch_kernel(k_product_join<MODE, ACT>, dim3(grid_for(ceil_div(quads, 256), 4096)), dim3(256), s, a,
+                       (uint32_t)p.splits);
 }
 
 // ---- dp = dy act'(p) and its column sums -----------------------------------------------------
@@ -275,32 +675,47 @@ int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
 
 }  // namespace
 
-int64_t linear_work_bytes(int64_t, int64_t, int64_t, int64_t) { return 0; }
+int64_t linear_work_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, bool grouped) {
+  return product_work_bytes(FWD, M, N, K, groups, grouped);
+}
 
-int64_t linear_bwd_work_bytes(int act, int64_t M, int64_t N, int64_t, int64_t groups, bool bias) {
-  int64_t b = act == LIN_NONE ? 0 : round16(2 * M * N);
-  if (bias) b += 4 * grad_parts(M, N, groups) * groups * N;
-  return b;
+namespace {
+// Scratch memory of the backward: dp, the partial column sums, then the split sums of the two
+// products (one after the other in the same place).
+struct BwdWork {
+  int64_t dp, sums, split;   // bytes
+};
+BwdWork bwd_work(int act, int64_t M, int64_t N, int64_t K, int64_t groups, bool grouped, bool bias) {
+  BwdWork w{};
+  w.dp = act == LIN_NONE ? 0 : round16(2 * M * N);
+  w.sums = bias ? round16(4 * grad_parts(M, N, groups) * groups * N) : 0;
+  const int64_t d = product_work_bytes(DGRAD, M, K, N, groups, grouped);
+  const int64_t g = product_work_bytes(WGRAD, N, K, M, groups, grouped);
+  w.split = d > g ? d : g;
+  return w;
+}
+}  // namespace
+
+int64_t linear_bwd_work_bytes(int act, int64_t M, int64_t N, int64_t K, int64_t groups, bool grouped, bool bias) {
+  const BwdWork w = bwd_work(act, M, N, K, groups, grouped, bias);
+  return w.dp + w.sums + w.split;
 }
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
-  ProductArgs p{a.M, a.N, a.K, a.groups, a.offsets, a.x, a.ld_x, a.w, a.K, a.N * a.K, a.y, a.ld_y, 0,
-                a.bias, a.residual, a.ld_res, a.pre};
-  const int64_t ti = (a.M + BI - 1) / BI + (a.offsets != nullptr ? a.groups : 0);
-  const dim3 grid((unsigned)ti, (unsigned)((a.N + BJ - 1) / BJ));
-  return with_linear_act(a.act, [&](auto A) {
-    return launch_kernel(k_product<FWD, decltype(A)::value>, grid, dim3(PROD_THREADS), s, p);
-  });
+  const ProductArgs p{a.M, a.N, a.K, a.groups, a.offsets, a.x, a.ld_x, a.w, a.K, a.N * a.K, a.y, a.ld_y, 0,
+                      a.bias, a.residual, a.ld_res, a.pre, a.work};
+  return with_linear_act(a.act, [&](auto A) { return launch_product<FWD, decltype(A)::value>(p, s); });
 }
 
 hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t s) {
+  const BwdWork w = bwd_work(a.act, a.M, a.N, a.K, a.groups, a.offsets != nullptr, a.db != nullptr);
   const uint16_t* dp = a.dy;
   int64_t ld_dp = a.ld_dy;
   hipError_t st = hipSuccess;
   if (a.act != LIN_NONE || a.db != nullptr) {
     const int64_t parts = grad_parts(a.M, a.N, a.groups);
     uint16_t* out = a.act == LIN_NONE ? nullptr : (uint16_t*)a.work;
-    float* sums = a.db == nullptr ? nullptr : (float*)(a.work + (out ? round16(2 * a.M * a.N) : 0));
+    float* sums = a.db == nullptr ? nullptr : (float*)(a.work + w.dp);
     const GradArgs g{a.M, a.N, a.groups, a.offsets, a.dy, a.ld_dy, a.pre, out, sums};
     const dim3 grid((unsigned)((a.N + 255) / 256), (unsigned)a.groups, (unsigned)parts);
     st = with_linear_act(a.act, [&](auto A) {
@@ -314,19 +729,16 @@ hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t s) {
       ld_dp = a.N;
     }
   }
+  float* split = (float*)(a.work + w.dp + w.sums);
   if (st == hipSuccess && a.dx != nullptr) {
-    ProductArgs p{a.M, a.K, a.N, a.groups, a.offsets, dp, ld_dp, a.w, a.K, a.N * a.K, a.dx, a.ld_dx, 0,
-                  nullptr, nullptr, 0, nullptr};
-    const int64_t ti = (a.M + BI - 1) / BI + (a.offsets != nullptr ? a.groups : 0);
-    st = launch_kernel(k_product<DGRAD, LIN_NONE>, dim3((unsigned)ti, (unsigned)((a.K + BJ - 1) / BJ)),
-                       dim3(PROD_THREADS), s, p);
+    const ProductArgs p{a.M, a.K, a.N, a.groups, a.offsets, dp, ld_dp, a.w, a.K, a.N * a.K, a.dx, a.ld_dx, 0,
+                        nullptr, nullptr, 0, nullptr, split};
+    st = launch_product<DGRAD, LIN_NONE>(p, s);
   }
   if (st == hipSuccess && a.dw != nullptr) {
-    ProductArgs p{a.N, a.K, a.M, a.groups, a.offsets, dp, ld_dp, a.x, a.ld_x, 0, a.dw, a.K, a.N * a.K,
-                  nullptr, nullptr, 0, nullptr};
-    st = launch_kernel(k_product<WGRAD, LIN_NONE>,
-                       dim3((unsigned)((a.N + BI - 1) / BI), (unsigned)((a.K + BJ - 1) / BJ), (unsigned)a.groups),
-                       dim3(PROD_THREADS), s, p);
+    const ProductArgs p{a.N, a.K, a.M, a.groups, a.offsets, dp, ld_dp, a.x, a.ld_x, 0, a.dw, a.K, a.N * a.K,
+                        nullptr, nullptr, 0, nullptr, split};
+    st = launch_product<WGRAD, LIN_NONE>(p, s);
   }
   return st;
 }

@@ -212,7 +212,7 @@ def glu_linear(x, w, bias=None, residual=None, *, act="none", offsets=None, save
     y = out if out is not None else torch.empty((M, N), dtype=_BF16, device=x.device)
     ld_y = _matrix(y, "out", _BF16, M, N)
     pre = torch.empty((M, N), dtype=torch.float16, device=x.device) if save_pre else None
-    nbytes = lib().glu_linear_work_bytes(M, N, K, groups)
+    nbytes = lib().glu_linear_work_bytes(M, N, K, groups, int(offsets is not None))
     work = torch.empty((nbytes,), dtype=torch.uint8, device=x.device) if nbytes > 0 else None
     _call("glu_linear", LINEAR_ACT[act], M, N, K, groups, _ptr(offsets), _ptr(x), ld_x, _ptr(w), _ptr(bias),
           _ptr(residual), ld_res, _ptr(y), ld_y, _ptr(pre), _ptr(work), nbytes, _stream(x))
@@ -235,7 +235,7 @@ def glu_linear_bwd(dy, x, w, *, pre=None, act="none", offsets=None, bias=False, 
     dx = torch.empty((M, K), dtype=_BF16, device=dev) if need_dx else none
     dw = torch.empty_like(w) if need_dw else none
     db = torch.empty(w.shape[:-1], dtype=_BF16, device=dev) if bias else none
-    nbytes = lib().glu_linear_bwd_work_bytes(a, M, N, K, groups, int(bias))
+    nbytes = lib().glu_linear_bwd_work_bytes(a, M, N, K, groups, int(offsets is not None), int(bias))
     work = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes > 0 else None
     _call("glu_linear_bwd", a, M, N, K, groups, _ptr(offsets), _ptr(dy), ld_dy, _ptr(x), ld_x, _ptr(w), _ptr(pre),
           _ptr(dx), K, _ptr(dw), _ptr(db), _ptr(work), nbytes, _stream(x))

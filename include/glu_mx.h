@@ -409,9 +409,10 @@ glu_status glu_block_norm_bwd(int kind, int flags, int64_t M, int64_t H, int64_t
  * non-decreasing, and rows offsets[e] .. offsets[e + 1] - 1 go through W and b number e; rows
  * outside every group give zero rows of y (and pre), without bias or residual.  Offsets
  * outside 0 .. M are taken as the nearer end.
- * N and K are multiples of 8 up to 2^20, row strides multiples of 8, groups <= 1024. */
+ * N and K are multiples of 8 up to 2^20, row strides multiples of 8 up to 2^21, groups <= 1024.
+ * glu_linear_work_bytes: grouped is 1 when offsets are given. */
 enum { GLU_LINEAR_NONE = 0, GLU_LINEAR_SILU = 1, GLU_LINEAR_GELU = 2 /* tanh */, GLU_LINEAR_GELU_ERF = 3 };
-int64_t glu_linear_work_bytes(int64_t M, int64_t N, int64_t K, int64_t groups);
+int64_t glu_linear_work_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, int grouped);
 glu_status glu_linear(int act, int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
                       const uint16_t* x, int64_t ld_x, const uint16_t* w, const uint16_t* bias,
                       const uint16_t* residual, int64_t ld_res, uint16_t* y, int64_t ld_y, uint16_t* pre,
@@ -421,7 +422,8 @@ glu_status glu_linear(int act, int64_t M, int64_t N, int64_t K, int64_t groups, 
  * pre is the forward's (NULL when act is GLU_LINEAR_NONE).  dx [M, K], dw [groups, N, K],
  * db [groups, N], BF16, each NULL when not wanted.  The residual's gradient is dy itself.
  * Rows outside every group give zero rows of dx. */
-int64_t glu_linear_bwd_work_bytes(int act, int64_t M, int64_t N, int64_t K, int64_t groups, int with_bias);
+int64_t glu_linear_bwd_work_bytes(int act, int64_t M, int64_t N, int64_t K, int64_t groups, int grouped,
+                                  int with_bias);
 glu_status glu_linear_bwd(int act, int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
                           const uint16_t* dy, int64_t ld_dy, const uint16_t* x, int64_t ld_x, const uint16_t* w,
                           const uint16_t* pre, uint16_t* dx, int64_t ld_dx, uint16_t* dw, uint16_t* db,
