@@ -25,8 +25,8 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 template <int ACT>
 __device__ __forceinline__ float act_of(float p) {
   if constexpr (ACT == LIN_NONE) return p;
-  if constexpr (ACT == LIN_SILU) return p * (1.0f / (1.0f + __builtin_amdgcn_exp2f(-zl2<SWIGLU>(p))));
-  if constexpr (ACT == LIN_GELU) return p * (1.0f / (1.0f + __builtin_amdgcn_exp2f(-zl2<GEGLU_TANH>(p))));
+  if constexpr (ACT == LIN_SILU) return p * sigmoid_from(exp_neg(zl2<SWIGLU>(p)));
+  if constexpr (ACT == LIN_GELU) return p * sigmoid_from(exp_neg(zl2<GEGLU_TANH>(p)));
   if constexpr (ACT == LIN_GELU_ERF) return p < ERF_TAIL_X ? 0.0f : p * phi_cdf(p);
 }
 template <int ACT>
@@ -41,7 +41,7 @@ __device__ __forceinline__ float act_grad(float p) {
   if constexpr (ACT == LIN_SILU || ACT == LIN_GELU) {
     constexpr int A = ACT == LIN_SILU ? SWIGLU : GEGLU_TANH;
     const float z = zl2<A>(p), e = __builtin_amdgcn_exp2f(-__builtin_fabsf(z));
-    const float s = 1.0f / (1.0f + e), sp = z >= 0.0f ? s : e * s, sn = z >= 0.0f ? e * s : s;
+    const float s = __builtin_amdgcn_rcpf(1.0f + e), sp = z >= 0.0f ? s : e * s, sn = z >= 0.0f ? e * s : s;
     return sp * __builtin_fmaf(p * sn, dz<A>(p), 1.0f);
   }
 }
@@ -117,6 +117,19 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* off, int64_t groups,
   return {-1, 0, 0};
 }
 
+// Row tiles of all groups, the rows after the last one included.
+__device__ __forceinline__ uint32_t count_tiles(const int32_t* off, int64_t groups, int64_t I, int64_t size) {
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+  for (int64_t e = lane; e <= groups; e += 64) {
+    const int64_t a = e == 0 ? 0 : min((int64_t)max(off[e], 0), I);
+    const int64_t b = e == groups ? I : max(a, min((int64_t)off[e + 1], I));
+    n += (int)((b - a + size - 1) / size);
+  }
+  for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
 // s_waitcnt on the vector-memory counter alone (gfx9 encoding: vmcnt in bits 3:0 and 15:14).
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -184,10 +197,12 @@ struct Operand {
       kk = wave * LOADS * (64u / CH) + lane / CH;
     }
   }
-  // Starts load q of the step at element k of the sum; elements at and past k1 read zero.
+  // Starts load q of the step at element k of the sum.  TAIL: elements at and past k1, which are
+  // less than a step away, read zero.
+  template <bool TAIL>
   __device__ __forceinline__ void issue(int q, uint32_t k, uint32_t k1, uint8_t* lds, uint32_t wave, uint32_t lane) const {
     uint32_t o = off[q];
-    if (k + BK > k1) {       // the last step of a sum that is no multiple of BK
+    if constexpr (TAIL) {
       uint32_t mine;
       if constexpr (!T) {
         const uint32_t row = 8u * (wave * LOADS + q) + (lane >> 3);
@@ -252,40 +267,54 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n) {
 
 constexpr uint32_t GROUP_I = 8;   // row tiles per group of the tile order
 
-// Epilogue of four consecutive columns of one row.
-template <int MODE, int ACT>
-__device__ __forceinline__ void finish(const ProductArgs& a, int64_t group, int64_t row, int64_t col, float (&v)[4]) {
-  if constexpr (MODE == FWD) {
-    if (group < a.groups) {
-      if (a.bias != nullptr) {
-        const u32x2 b = *reinterpret_cast<const u32x2*>(a.bias + group * a.J + col);
-        v[0] += bf_lo(b.x);
-        v[1] += bf_hi(b.x);
-        v[2] += bf_lo(b.y);
-        v[3] += bf_hi(b.y);
-      }
-      if (a.pre != nullptr) {
-        uint32_t p[4];
+// N consecutive BF16 values, widened (zeros for a null pointer).
+template <int N>
+__device__ __forceinline__ void load_bf16(float (&f)[N], const uint16_t* p) {
+  typedef unsigned int vec __attribute__((ext_vector_type(N / 2)));
+  vec v = (vec)0u;
+  if (p != nullptr) v = *reinterpret_cast<const vec*>(p);
 #pragma unroll
-        for (int e = 0; e < 4; e++)
-          p[e] = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_fmed3f(v[e], -65504.0f, 65504.0f));
-        *reinterpret_cast<u32x2*>(a.pre + row * a.J + col) = (u32x2){p[0] | p[1] << 16, p[2] | p[3] << 16};
-      }
-#pragma unroll
-      for (int e = 0; e < 4; e++) v[e] = act_of<ACT>(v[e]);
-      if (a.residual != nullptr) {
-        const u32x2 b = *reinterpret_cast<const u32x2*>(a.residual + row * a.ld_res + col);
-        v[0] += bf_lo(b.x);
-        v[1] += bf_hi(b.x);
-        v[2] += bf_lo(b.y);
-        v[3] += bf_hi(b.y);
-      }
-    } else if (a.pre != nullptr) {
-      *reinterpret_cast<u32x2*>(a.pre + row * a.J + col) = (u32x2){0u, 0u};
-    }
+  for (int i = 0; i < N / 2; i++) {
+    f[2 * i] = bf_lo(v[i]);
+    f[2 * i + 1] = bf_hi(v[i]);
   }
-  uint16_t* c = a.c + (MODE == WGRAD ? group * a.c_group : 0) + row * a.ld_c + col;
-  *reinterpret_cast<u32x2*>(c) = (u32x2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+}
+
+// Epilogue of N consecutive columns of one row, in place: v holds the sums, then what is stored.
+template <int MODE, int ACT, int N>
+__device__ __forceinline__ void finish(const ProductArgs& a, int64_t group, int64_t row, int64_t col, float (&v)[N],
+                                       const float (&bias)[N], const float (&res)[N]) {
+  typedef unsigned int vec __attribute__((ext_vector_type(N / 2)));
+  vec o;
+  if constexpr (MODE == FWD) {
+    const bool live = group < a.groups;
+#pragma unroll
+    for (int e = 0; e < N; e++) v[e] += bias[e];
+    if (a.pre != nullptr) {
+#pragma unroll
+      for (int e = 0; e < N / 2; e++) {
+        const uint16_t lo = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_fmed3f(v[2 * e], -65504.0f, 65504.0f));
+        const uint16_t hi =
+            __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_fmed3f(v[2 * e + 1], -65504.0f, 65504.0f));
+        o[e] = live ? lo | (uint32_t)hi << 16 : 0u;
+      }
+      *reinterpret_cast<vec*>(a.pre + row * a.J + col) = o;
+    }
+#pragma unroll
+    for (int e = 0; e < N; e++) v[e] = live ? act_of<ACT>(v[e]) + res[e] : 0.0f;
+  }
+#pragma unroll
+  for (int e = 0; e < N / 2; e++) o[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+  *reinterpret_cast<vec*>(a.c + (MODE == WGRAD ? group * a.c_group : 0) + row * a.ld_c + col) = o;
+}
+// The same with bias and residual loaded here.
+template <int MODE, int ACT, int N>
+__device__ __forceinline__ void finish(const ProductArgs& a, int64_t group, int64_t row, int64_t col, float (&v)[N]) {
+  float bias[N], res[N];
+  const bool live = MODE == FWD && group < a.groups;
+  load_bf16(bias, live && a.bias != nullptr ? a.bias + group * a.J + col : nullptr);
+  load_bf16(res, live && a.residual != nullptr ? a.residual + row * a.ld_res + col : nullptr);
+  finish<MODE, ACT, N>(a, group, row, col, v, bias, res);
 }
 
 // WI x WJ waves of TI x TJ tiles of 16 x 16 each: a tile of 16 WI TI rows by 16 WJ TJ columns.
@@ -310,8 +339,12 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
 
   // this workgroup's tile: contiguous runs per XCD; a run goes down GROUP_I row tiles before the
   // next column tile, so that the workgroups of one XCD share operands in its L2
+  if (MODE != WGRAD && a.offsets != nullptr) {   // the grid allows for more row tiles than there are
+    tiles_i = count_tiles(a.offsets, a.groups, a.I, BI);
+    if (blockIdx.x >= tiles_i * tiles_j) return;
+  }
   const uint32_t per = tiles_i * tiles_j;
-  uint32_t b = xcd_run(blockIdx.x, gridDim.x);
+  uint32_t b = xcd_run(blockIdx.x, MODE != WGRAD && a.offsets != nullptr ? per : gridDim.x);
   const uint32_t outer = b / per;          // WGRAD: group; with splits: part of the sum
   b -= outer * per;
   const uint32_t in_group = GROUP_I * tiles_j, first_i = b / in_group * GROUP_I;
@@ -366,9 +399,19 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
   uint8_t *const sa = smem, *const sb = smem + 2 * OpA::BYTES;
   auto issue = [&](uint32_t k, int stage) {
 #pragma unroll
-    for (int q = 0; q < OpA::LOADS; q++) oa.issue(q, k, k1, sa + stage * OpA::BYTES, wave, lane);
+    for (int q = 0; q < OpA::LOADS; q++) oa.template issue<false>(q, k, k1, sa + stage * OpA::BYTES, wave, lane);
 #pragma unroll
-    for (int q = 0; q < OpB::LOADS; q++) ob.issue(q, k, k1, sb + stage * OpB::BYTES, wave, lane);
+    for (int q = 0; q < OpB::LOADS; q++) ob.template issue<false>(q, k, k1, sb + stage * OpB::BYTES, wave, lane);
+  };
+  auto issue_tail = [&](uint32_t k, int stage) {
+#pragma unroll
+    for (int q = 0; q < OpA::LOADS; q++) oa.template issue<true>(q, k, k1, sa + stage * OpA::BYTES, wave, lane);
+#pragma unroll
+    for (int q = 0; q < OpB::LOADS; q++) ob.template issue<true>(q, k, k1, sb + stage * OpB::BYTES, wave, lane);
+  };
+  auto start = [&](uint32_t k, int stage) {   // the loads of the step at k, if there is one
+    if (k + BK <= k1) issue(k, stage);
+    else if (k < k1) issue_tail(k, stage);
   };
   v8bf xa[2][TI], xb[2][TJ];
   auto read = [&](int stage, int h) {
@@ -390,7 +433,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
     __builtin_amdgcn_sched_barrier(0);   // the products above are not to sink below the wait
     wait_vm<0>();
     lds_barrier();
-    if (k + 2 * BK < k1) issue(k + 2 * BK, stage);
+    start(k + 2 * BK, stage);
     if (k + BK < k1) read(1 - stage, 0);
     multiply(1);
     __builtin_amdgcn_sched_barrier(0);
@@ -398,11 +441,12 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
   };
 
   if (k0 < k1) {
-    issue(k0, 0);
+    start(k0, 0);
     wait_vm<0>();
     lds_barrier();
-    if (k0 + BK < k1) issue(k0 + BK, 1);
+    start(k0 + BK, 1);
     read(0, 0);
+    wait_lds();
     for (uint32_t k = k0; k < k1; k += 2 * BK) {
       step(k, 0);
       if (k + BK < k1) step(k + BK, 1);
@@ -411,38 +455,76 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
 
   // acc[i][j][e] is C at row r of its row tile and column 4 g + e of its column tile
   const uint32_t g = lane >> 4, r = lane & 15u;
+  if (splits > 1) {
+#pragma unroll
+    for (int i = 0; i < TI; i++) {
+      const int64_t row = t.i0 + 16u * FrA::tile(wi, i) + r;
+      const int64_t at = MODE == WGRAD ? (part * a.groups + group) * a.I + row : part * a.I + row;
+#pragma unroll
+      for (int j = 0; j < TJ; j++) {
+        const int64_t col = j0 + 16u * FrB::tile(wj, j) + 4u * g;
+        if (row < t.i1 && col < j1) *reinterpret_cast<v4f*>(a.work + at * a.J + col) = acc[i][j];
+      }
+    }
+    return;
+  }
+  // A row tile's 16 x (16 TJ) sums go through the wave's own piece of LDS, so that a lane gets 8
+  // consecutive columns of a row: 16-byte loads and stores.  (No wave reads the stages any
+  // more: the last step's barrier comes after its last read.)
+  constexpr uint32_t PITCH = 16 * TJ + 4, CH = 2 * TJ, ROWS = 64 / CH;   // floats; lanes a row; rows a pass
+  static_assert(WAVES * 16 * PITCH * 4 <= sizeof(smem));
+  float* const mine = reinterpret_cast<float*>(smem) + wave * (16 * PITCH);
+  const uint32_t cc = 8u * (lane % CH), lrow = lane / CH;
+  const int64_t col = j0 + 16u * FrB::tile(wj, cc / 16) + cc % 16u;
+  const bool live = MODE == FWD && group < a.groups, in = col < j1;
+  float bias[8];
+  load_bf16(bias, live && in && a.bias != nullptr ? a.bias + group * a.J + col : nullptr);
+  u32x4 res[TI][16 / ROWS];
+  if constexpr (MODE == FWD) {
+#pragma unroll
+    for (int i = 0; i < TI; i++)
+#pragma unroll
+      for (uint32_t p = 0; p < 16 / ROWS; p++) {
+        const int64_t row = t.i0 + 16u * FrA::tile(wi, i) + ROWS * p + lrow;
+        res[i][p] = (u32x4)0u;
+        if (live && a.residual != nullptr && in && row < t.i1)
+          res[i][p] = *reinterpret_cast<const u32x4*>(a.residual + row * a.ld_res + col);
+      }
+  }
 #pragma unroll
   for (int i = 0; i < TI; i++) {
-    const int64_t row = t.i0 + 16u * FrA::tile(wi, i) + r;
-    if (row >= t.i1) continue;
 #pragma unroll
-    for (int j = 0; j < TJ; j++) {
-      const int64_t col = j0 + 16u * FrB::tile(wj, j) + 4u * g;
-      if (col >= j1) continue;
-      if (splits > 1) {
-        const int64_t gr = MODE == WGRAD ? group * a.I + row : row;
-        const int64_t rows = MODE == WGRAD ? a.groups * a.I : a.I;
-        *reinterpret_cast<v4f*>(a.work + (part * rows + gr) * a.J + col) = acc[i][j];
-      } else {
-        float v[4];
+    for (int j = 0; j < TJ; j++) *reinterpret_cast<v4f*>(mine + r * PITCH + 16 * j + 4 * g) = acc[i][j];
 #pragma unroll
-        for (int e = 0; e < 4; e++) v[e] = acc[i][j][e];
-        finish<MODE, ACT>(a, group, row, col, v);
+    for (uint32_t p = 0; p < 16 / ROWS; p++) {
+      const int64_t row = t.i0 + 16u * FrA::tile(wi, i) + ROWS * p + lrow;
+      const float* q = mine + (ROWS * p + lrow) * PITCH + cc;
+      const v4f lo = *reinterpret_cast<const v4f*>(q), hi = *reinterpret_cast<const v4f*>(q + 4);
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}, rs[8];
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        rs[2 * e] = MODE == FWD ? bf_lo(res[i][p][e]) : 0.0f;
+        rs[2 * e + 1] = MODE == FWD ? bf_hi(res[i][p][e]) : 0.0f;
       }
+      if (in && row < t.i1) finish<MODE, ACT, 8>(a, group, row, col, v, bias, rs);
     }
   }
 }
 
-// Joins the parts of split sums and finishes them: four columns a thread.
+// Joins the parts of split sums and finishes them: eight columns a thread.
 template <int MODE, int ACT>
 __global__ __launch_bounds__(256) void k_product_join(ProductArgs a, uint32_t splits) {
-  const int64_t rows = MODE == WGRAD ? a.groups * a.I : a.I, n = rows * a.J / 4;
+  const int64_t rows = MODE == WGRAD ? a.groups * a.I : a.I, n = rows * a.J / 8;
   for (int64_t q = 256 * (int64_t)blockIdx.x + threadIdx.x; q < n; q += 256 * (int64_t)gridDim.x) {
-    const int64_t row = q / (a.J / 4), col = 4 * (q % (a.J / 4));
-    v4f s = *reinterpret_cast<const v4f*>(a.work + row * a.J + col);
-    for (uint32_t p = 1; p < splits; p++) s += *reinterpret_cast<const v4f*>(a.work + (p * rows + row) * a.J + col);
-    float v[4] = {s[0], s[1], s[2], s[3]};
-    finish<MODE, ACT>(a, MODE == WGRAD ? row / a.I : 0, MODE == WGRAD ? row % a.I : row, col, v);
+    const int64_t row = q / (a.J / 8), col = 8 * (q % (a.J / 8));
+    v4f lo = (v4f)0.0f, hi = (v4f)0.0f;
+    for (uint32_t p = 0; p < splits; p++) {
+      const v4f* src = reinterpret_cast<const v4f*>(a.work + (p * rows + row) * a.J + col);
+      lo += src[0];
+      hi += src[1];
+    }
+    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    finish<MODE, ACT, 8>(a, MODE == WGRAD ? row / a.I : 0, MODE == WGRAD ? row % a.I : row, col, v);
   }
 }
 
@@ -530,7 +612,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few_rows(ProductArgs a) {
     *reinterpret_cast<v4f*>(a.work + ((int64_t)blockIdx.z * a.I + row) * a.J + col) = s;
   } else {
     float v[4] = {s[0], s[1], s[2], s[3]};
-    finish<FWD, ACT>(a, t.group, row, col, v);
+    finish<FWD, ACT, 4>(a, t.group, row, col, v);
   }
 }
 
@@ -594,8 +676,8 @@ hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
                             (uint32_t)p.tiles_j, (uint32_t)p.splits);
   }
   if (e != hipSuccess || p.splits == 1) return e;
-  const int64_t quads = (MODE == WGRAD ? a.groups : 1) * a.I * a.J / 4;
-  return launch_kernel(k_product_join<MODE, ACT>, dim3(grid_for(ceil_div(quads, 256), 4096)), dim3(256), s, a,
+  const int64_t octets = (MODE == WGRAD ? a.groups : 1) * a.I * a.J / 8;
+  return launch_kernel(k_product_join<MODE, ACT>, dim3(grid_for(ceil_div(octets, 256), 4096)), dim3(256), s, a,
                        (uint32_t)p.splits);
 }
 

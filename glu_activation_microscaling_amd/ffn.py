@@ -16,7 +16,7 @@ the call, on the current stream.
 """
 import torch
 
-from . import _call, _rowmajor, _stream, lib
+from . import GluError, _rowmajor, lib
 
 NORM_KIND = {"rms": 0, "layer": 1}
 LINEAR_ACT = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 2, "gelu_erf": 3}
@@ -25,8 +25,38 @@ _PRE, _POST, _F32_STREAM, _F32_PARAMS, _GATE_GROUPED, _W_GROUPED, _B_GROUPED = 1
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
+_fns = {}   # C entry points by name, looked up once
+
+
+def _call(name, *args):
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    status = fn(*args)
+    if status != 0:
+        raise GluError(name, status)
+
+
+def _size(name, *args):
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    return fn(*args)
+
+
+# The current stream's handle by device index: what torch.cuda.current_stream(device).cuda_stream
+# is, without the stream object in between (0.2 us instead of 2.3).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(t):
+    if _raw_stream is not None:
+        return _raw_stream(t.device.index)
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
 def _ptr(t):
-    return t.data_ptr() if t is not None and t.numel() else None
+    return None if t is None else t.data_ptr() or None   # an empty tensor's pointer is 0
 
 
 def _matrix(t, name, dtype, rows=None, cols=None):
@@ -38,6 +68,13 @@ def _matrix(t, name, dtype, rows=None, cols=None):
     return ld if M > 1 else (N + 7) // 8 * 8
 
 
+def _empty(t, shape, dtype):
+    """An uninitialised tensor on t's device; shaped like a contiguous t it is the quicker call."""
+    if dtype is t.dtype and t.shape == shape and t.is_contiguous():
+        return torch.empty_like(t)
+    return t.new_empty(shape, dtype=dtype)
+
+
 def _like(t, name, dtype, shape):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -45,10 +82,11 @@ def _like(t, name, dtype, shape):
         raise ValueError(f"{name} must be a contiguous GPU tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _same_device(ref, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+def _same_device(ref, *tensors):
+    dev = ref.device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"the operands are on different devices: {t.device} and {dev}")
 
 
 # ---- norms -----------------------------------------------------------------------------------
@@ -93,16 +131,16 @@ def _norm_setup(x, y, gate, w_pre, b_pre, w_post, pre, post, kind):
 
 def _norm_forward(fn, x, y, gate, w_pre, b_pre, w_post, pre, post, res_scale, kind, eps, outs, x_out):
     k, flags, M, H, groups, ld_x, ld_y = _norm_setup(x, y, gate, w_pre, b_pre, w_post, pre, post, kind)
-    _same_device(x, y=y, gate=gate, w_pre=w_pre, b_pre=b_pre, w_post=w_post)
+    _same_device(x, y, gate, w_pre, b_pre, w_post)
     if y is None:
         if x_out is not None or res_scale != 1.0:
             raise ValueError("without y, x' is x itself: no x_out and res_scale 1")
         ld_xo = 0
     else:
         if x_out is None:
-            x_out = torch.empty((M, H), dtype=x.dtype, device=x.device)
+            x_out = _empty(x, (M, H), x.dtype)
         ld_xo = _matrix(x_out, "x_out", x.dtype, M, H)
-    stats = torch.empty((M, 4), dtype=_F32, device=x.device)
+    stats = x.new_empty((M, 4), dtype=_F32)
     _call(fn, k, flags, M, H, groups, _ptr(x), ld_x, _ptr(y), ld_y, _ptr(gate), _ptr(w_pre), _ptr(b_pre),
           _ptr(w_post), res_scale, eps, _ptr(x_out), ld_xo, *outs(M, H), _ptr(stats), _stream(x))
     return x if y is None else x_out, stats
@@ -116,11 +154,11 @@ def glu_block_norm(x, y=None, *, gate=None, w_pre=None, b_pre=None, w_post=None,
     stats is what glu_block_norm_bwd needs."""
     h = out
     if pre and h is None:
-        h = torch.empty(x.shape, dtype=_BF16, device=x.device)
+        h = _empty(x, x.shape, _BF16)
     elif not pre:
         if out is not None:
             raise ValueError("out is the output of the norm before the next block (pre=True)")
-        h = torch.empty((0,), dtype=_BF16, device=x.device)
+        h = x.new_empty((0,), dtype=_BF16)
 
     def outs(M, H):
         return (_ptr(h), _matrix(h, "out", _BF16, M, H)) if pre else (None, 0)
@@ -143,8 +181,8 @@ def glu_block_norm_mxfp8(x, y=None, *, gate=None, w_pre=None, b_pre=None, w_post
         _byte_buffer(q, "q", M * H)
         _byte_buffer(s, "s", M * (H // 32))
     else:
-        q = torch.empty((M, H), dtype=torch.uint8, device=x.device)
-        s = torch.empty((M, H // 32), dtype=torch.uint8, device=x.device)
+        q = x.new_empty((M, H), dtype=torch.uint8)
+        s = x.new_empty((M, H // 32), dtype=torch.uint8)
     x_out, stats = _norm_forward("glu_block_norm_mxfp8", x, y, gate, w_pre, b_pre, w_post, True, post, res_scale,
                                  kind, eps, lambda M, H: (_ptr(q), _ptr(s)), x_out)
     return x_out, q, s, stats
@@ -162,19 +200,18 @@ def glu_block_norm_bwd(x, y, stats, dx_out, dh, *, gate=None, w_pre=None, b_pre=
         raise ValueError("dh is the gradient of h: given exactly when pre=True")
     if y is None and res_scale != 1.0:
         raise ValueError("without y, x' is x itself: res_scale 1")
-    _same_device(x, y=y, stats=stats, dx_out=dx_out, dh=dh, gate=gate, w_pre=w_pre, b_pre=b_pre, w_post=w_post)
+    _same_device(x, y, stats, dx_out, dh, gate, w_pre, b_pre, w_post)
     ld_dxo = 0 if dx_out is None else _matrix(dx_out, "dx_out", x.dtype, M, H)
     ld_dh = 0 if dh is None else _matrix(dh, "dh", _BF16, M, H)
-    dev = x.device
-    dx = torch.empty((M, H), dtype=x.dtype, device=dev)
-    dy = torch.empty((M, H) if y is not None else (0,), dtype=_BF16, device=dev)
+    dx = _empty(x, (M, H), x.dtype)
+    dy = x.new_empty((0,), dtype=_BF16) if y is None else _empty(y, (M, H), _BF16)
 
     def grad_of(p):
-        return torch.empty((0,), dtype=_BF16, device=dev) if p is None else torch.empty_like(p)
+        return x.new_empty((0,), dtype=_BF16) if p is None else torch.empty_like(p)
 
     dgate, dw_post, dw_pre, db_pre = grad_of(gate), grad_of(w_post), grad_of(w_pre), grad_of(b_pre)
-    nbytes = lib().glu_block_norm_bwd_work_bytes(M, H, groups)
-    work = torch.empty((max(nbytes, 0),), dtype=torch.uint8, device=dev)
+    nbytes = _size("glu_block_norm_bwd_work_bytes", M, H, groups)
+    work = x.new_empty((max(nbytes, 0),), dtype=torch.uint8)
     _call("glu_block_norm_bwd", k, flags, M, H, groups, _ptr(x), ld_x, _ptr(y), ld_y, _ptr(stats), _ptr(dx_out),
           ld_dxo, _ptr(dh), ld_dh, _ptr(gate), _ptr(w_pre), _ptr(w_post), res_scale, _ptr(dx), H if M > 1 else
           (H + 7) // 8 * 8, _ptr(dy), H if M > 1 else (H + 7) // 8 * 8, _ptr(dgate), _ptr(dw_pre), _ptr(db_pre),
@@ -207,13 +244,13 @@ def glu_linear(x, w, bias=None, residual=None, *, act="none", offsets=None, save
     M, N, K, groups, ld_x = _linear_setup(x, w, offsets, act)
     if bias is not None:
         _like(bias, "bias", _BF16, w.shape[:-1])
-    _same_device(x, w=w, bias=bias, residual=residual, offsets=offsets, out=out)
+    _same_device(x, w, bias, residual, offsets, out)
     ld_res = 0 if residual is None else _matrix(residual, "residual", _BF16, M, N)
-    y = out if out is not None else torch.empty((M, N), dtype=_BF16, device=x.device)
+    y = out if out is not None else x.new_empty((M, N))
     ld_y = _matrix(y, "out", _BF16, M, N)
-    pre = torch.empty((M, N), dtype=torch.float16, device=x.device) if save_pre else None
-    nbytes = lib().glu_linear_work_bytes(M, N, K, groups, int(offsets is not None))
-    work = torch.empty((nbytes,), dtype=torch.uint8, device=x.device) if nbytes > 0 else None
+    pre = x.new_empty((M, N), dtype=torch.float16) if save_pre else None
+    nbytes = _size("glu_linear_work_bytes", M, N, K, groups, int(offsets is not None))
+    work = x.new_empty((nbytes,), dtype=torch.uint8) if nbytes > 0 else None
     _call("glu_linear", LINEAR_ACT[act], M, N, K, groups, _ptr(offsets), _ptr(x), ld_x, _ptr(w), _ptr(bias),
           _ptr(residual), ld_res, _ptr(y), ld_y, _ptr(pre), _ptr(work), nbytes, _stream(x))
     return (y, pre) if save_pre else y
@@ -230,13 +267,13 @@ def glu_linear_bwd(dy, x, w, *, pre=None, act="none", offsets=None, bias=False, 
         raise ValueError('pre goes with an act other than "none", and only with it')
     if pre is not None:
         _like(pre, "pre", torch.float16, (M, N))
-    _same_device(x, w=w, dy=dy, pre=pre, offsets=offsets)
-    dev, none = x.device, torch.empty((0,), dtype=_BF16, device=x.device)
-    dx = torch.empty((M, K), dtype=_BF16, device=dev) if need_dx else none
+    _same_device(x, w, dy, pre, offsets)
+    none = x.new_empty((0,)) if not (need_dx and need_dw and bias) else None
+    dx = _empty(x, (M, K), _BF16) if need_dx else none
     dw = torch.empty_like(w) if need_dw else none
-    db = torch.empty(w.shape[:-1], dtype=_BF16, device=dev) if bias else none
-    nbytes = lib().glu_linear_bwd_work_bytes(a, M, N, K, groups, int(offsets is not None), int(bias))
-    work = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes > 0 else None
+    db = x.new_empty(w.shape[:-1]) if bias else none
+    nbytes = _size("glu_linear_bwd_work_bytes", a, M, N, K, groups, int(offsets is not None), int(bias))
+    work = x.new_empty((nbytes,), dtype=torch.uint8) if nbytes > 0 else None
     _call("glu_linear_bwd", a, M, N, K, groups, _ptr(offsets), _ptr(dy), ld_dy, _ptr(x), ld_x, _ptr(w), _ptr(pre),
           _ptr(dx), K, _ptr(dw), _ptr(db), _ptr(work), nbytes, _stream(x))
     return dx, dw, db
@@ -254,10 +291,10 @@ def glu_moe_sort(ids, experts):
         raise ValueError("ids must be [tokens, choices]")
     _like(ids, "ids", ids.dtype, ids.shape)
     T, k = ids.shape
-    rows = torch.empty((T, k), dtype=_I32, device=ids.device)
-    offsets = torch.empty((experts + 1,), dtype=_I32, device=ids.device)
-    nbytes = lib().glu_moe_sort_work_bytes(T, k, experts)
-    work = torch.empty((nbytes,), dtype=torch.uint8, device=ids.device) if nbytes > 0 else None
+    rows = _empty(ids, (T, k), _I32)
+    offsets = ids.new_empty((experts + 1,), dtype=_I32)
+    nbytes = _size("glu_moe_sort_work_bytes", T, k, experts)
+    work = ids.new_empty((nbytes,), dtype=torch.uint8) if nbytes > 0 else None
     _call("glu_moe_sort", T, k, experts, _ptr(ids), ids.element_size(), _ptr(rows), _ptr(offsets), _ptr(work), nbytes,
           _stream(ids))
     return rows, offsets
@@ -281,8 +318,8 @@ def glu_moe_permute(x, rows, offsets, *, out=None):
     M, H, ld = _rowmajor(x, "x", x.dtype)
     if M != T:
         raise ValueError(f"x must have {T} rows, got {M}")
-    _same_device(x, rows=rows, offsets=offsets, out=out)
-    xs = out if out is not None else torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+    _same_device(x, rows, offsets, out)
+    xs = out if out is not None else x.new_empty((T * k, H))
     ld_xs = _matrix(xs, "out", x.dtype, T * k, H)
     e = x.element_size()
     _call("glu_moe_permute", T, k, offsets.numel() - 1, H * e, _ptr(x), (ld if M > 1 else H) * e, _ptr(rows),
@@ -298,9 +335,9 @@ def glu_moe_combine(y, rows, weights=None, residual=None, *, out=None):
     H = y.shape[1]
     if weights is not None:
         _like(weights, "weights", _F32, (T, k))
-    _same_device(y, rows=rows, weights=weights, residual=residual, out=out)
+    _same_device(y, rows, weights, residual, out)
     ld_res = 0 if residual is None else _matrix(residual, "residual", _BF16, T, H)
-    o = out if out is not None else torch.empty((T, H), dtype=_BF16, device=y.device)
+    o = out if out is not None else y.new_empty((T, H))
     _call("glu_moe_combine", T, k, H, _ptr(y), ld_y, _ptr(rows), _ptr(weights), _ptr(residual), ld_res, _ptr(o),
           _matrix(o, "out", _BF16, T, H), _stream(y))
     return o
@@ -314,9 +351,9 @@ def glu_moe_combine_bwd(dout, y, rows, weights, offsets):
     H = y.shape[1]
     ld_d = _matrix(dout, "dout", _BF16, T, H)
     _like(weights, "weights", _F32, (T, k))
-    _same_device(y, dout=dout, rows=rows, weights=weights, offsets=offsets)
-    dy = torch.empty((T * k, H), dtype=_BF16, device=y.device)
-    dw = torch.empty((T, k), dtype=_F32, device=y.device)
+    _same_device(y, dout, rows, weights, offsets)
+    dy = _empty(y, (T * k, H), _BF16)
+    dw = torch.empty_like(weights)
     _call("glu_moe_combine_bwd", T, k, H, offsets.numel() - 1, _ptr(dout), ld_d, _ptr(y), ld_y, _ptr(rows),
           _ptr(weights), _ptr(offsets), _ptr(dy), (H + 7) // 8 * 8 if T * k == 1 else H, _ptr(dw), _stream(y))
     return dy, dw
