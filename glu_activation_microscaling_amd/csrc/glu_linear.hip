@@ -631,6 +631,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped) {
   ProductPlan p{};
   p.splits = 1;
+  if (I == 0 || J == 0) return p;   // nothing to launch
   if (mode == FWD && I <= (grouped ? FEW_ROWS / 2 * groups : FEW_ROWS)) {
     p.kind = FEW;
     p.tiles_i = ceil_div(I, FEW_ROWS) + (grouped ? groups : 0);
@@ -747,6 +748,7 @@ __global__ __launch_bounds__(256) void k_linear_join(const float* sums, int64_t 
 // Parts each group's rows are cut into for the column sums: enough workgroups to fill the chip,
 // with 64 rows or more of an average group each.
 int64_t grad_parts(int64_t M, int64_t N, int64_t groups) {
+  if (N == 0) return 1;
   const int64_t tiles = (N + 255) / 256 * groups, want = (1024 + tiles - 1) / tiles;
   const int64_t most = (M / groups + 63) / 64;
   const int64_t p = want < most ? want : most;

@@ -51,7 +51,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(t):
     if _raw_stream is not None:
-        return _raw_stream(t.device.index)
+        return _raw_stream(t.get_device())
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
@@ -62,10 +62,17 @@ def _ptr(t):
 def _matrix(t, name, dtype, rows=None, cols=None):
     """Row stride of a 2-D GPU tensor with unit column stride (of [rows, cols] where given).
     The stride of a single row means nothing; a whole number of vectors is passed for it."""
-    M, N, ld = _rowmajor(t, name, dtype)
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not dtype or not t.is_cuda or len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
+        _rowmajor(t, name, dtype)   # says what is wrong
+    M, N = shape
     if (rows is not None and M != rows) or (cols is not None and N != cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got [{M}, {N}]")
-    return ld if M > 1 else (N + 7) // 8 * 8
+    return stride[0] if M > 1 else _one_row(N)
+
+
+def _one_row(N):
+    return (N + 7) // 8 * 8
 
 
 def _empty(t, shape, dtype):
@@ -83,10 +90,10 @@ def _like(t, name, dtype, shape):
 
 
 def _same_device(ref, *tensors):
-    dev = ref.device
+    dev = ref.get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"the operands are on different devices: {t.device} and {dev}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"the operands are on different devices: {t.device} and {ref.device}")
 
 
 # ---- norms -----------------------------------------------------------------------------------
@@ -106,25 +113,26 @@ def _norm_setup(x, y, gate, w_pre, b_pre, w_post, pre, post, kind):
         raise ValueError("w_pre and b_pre belong to the norm before the next block (pre=True)")
     if not post and w_post is not None:
         raise ValueError("w_post belongs to the norm after the block (post=True)")
-    flags = (_PRE if pre else 0) | (_POST if post else 0) | (_F32_STREAM if x.dtype == _F32 else 0)
+    flags = (_PRE if pre else 0) | (_POST if post else 0) | (_F32_STREAM if x.dtype is _F32 else 0)
     groups, dtype = 1, None
-    for p, name, grouped in ((gate, "gate", _GATE_GROUPED), (w_pre, "w_pre", _W_GROUPED),
-                             (b_pre, "b_pre", _B_GROUPED), (w_post, "w_post", 0)):
+    for p, grouped in ((gate, _GATE_GROUPED), (w_pre, _W_GROUPED), (b_pre, _B_GROUPED), (w_post, 0)):
         if p is None:
             continue
-        dtype = dtype or p.dtype
-        if p.dtype != dtype or dtype not in (_BF16, _F32):
-            raise TypeError("the parameters must all be torch.bfloat16 or all torch.float32")
-        if not p.is_cuda or not p.is_contiguous() or p.dim() not in (1, 2) or p.shape[-1] != H:
-            raise ValueError(f"{name} must be a contiguous GPU tensor [H] or [groups, H]")
-        if p.dim() == 2 and p.shape[0] != 1:
-            if not grouped or (groups != 1 and groups != p.shape[0]):
-                raise ValueError(f"{name} must be [H] or share one number of groups with the other parameters")
-            groups = p.shape[0]
+        if p.dtype is not dtype:
+            if dtype is not None or (p.dtype is not _BF16 and p.dtype is not _F32):
+                raise TypeError("the parameters must all be torch.bfloat16 or all torch.float32")
+            dtype = p.dtype
+        shape = p.shape
+        if not p.is_cuda or not p.is_contiguous() or len(shape) not in (1, 2) or shape[-1] != H:
+            raise ValueError(f"a parameter must be a contiguous GPU tensor [{H}] or [groups, {H}], got {tuple(shape)}")
+        if len(shape) == 2 and shape[0] != 1:
+            if not grouped or (groups != 1 and groups != shape[0]):
+                raise ValueError("w_post is [H]; gate, w_pre and b_pre are [H] or share one number of groups")
+            groups = shape[0]
             flags |= grouped
     if groups == 0 or M % groups:
         raise ValueError(f"{M} rows are not a whole number of rows for each of {groups} groups")
-    if dtype == _F32:
+    if dtype is _F32:
         flags |= _F32_PARAMS
     return NORM_KIND[kind], flags, M, H, groups, ld_x, ld_y
 
@@ -136,13 +144,14 @@ def _norm_forward(fn, x, y, gate, w_pre, b_pre, w_post, pre, post, res_scale, ki
         if x_out is not None or res_scale != 1.0:
             raise ValueError("without y, x' is x itself: no x_out and res_scale 1")
         ld_xo = 0
+    elif x_out is None:
+        x_out, ld_xo = _empty(x, (M, H), x.dtype), H if M > 1 else _one_row(H)
     else:
-        if x_out is None:
-            x_out = _empty(x, (M, H), x.dtype)
+        _same_device(x, x_out)
         ld_xo = _matrix(x_out, "x_out", x.dtype, M, H)
     stats = x.new_empty((M, 4), dtype=_F32)
     _call(fn, k, flags, M, H, groups, _ptr(x), ld_x, _ptr(y), ld_y, _ptr(gate), _ptr(w_pre), _ptr(b_pre),
-          _ptr(w_post), res_scale, eps, _ptr(x_out), ld_xo, *outs(M, H), _ptr(stats), _stream(x))
+          _ptr(w_post), res_scale, eps, _ptr(x_out), ld_xo, *outs, _ptr(stats), _stream(x))
     return x if y is None else x_out, stats
 
 
@@ -152,19 +161,19 @@ def glu_block_norm(x, y=None, *, gate=None, w_pre=None, b_pre=None, w_post=None,
     b_pre (pre=True), N the rms or layer norm of a row: (x', h, stats).  Without y, x' is x
     itself.  gate, w_pre, b_pre: [H], or [groups, H] with one row per M / groups rows of x.
     stats is what glu_block_norm_bwd needs."""
-    h = out
-    if pre and h is None:
-        h = _empty(x, x.shape, _BF16)
-    elif not pre:
+    h, ld_h = out, 0
+    if not pre:
         if out is not None:
             raise ValueError("out is the output of the norm before the next block (pre=True)")
         h = x.new_empty((0,), dtype=_BF16)
-
-    def outs(M, H):
-        return (_ptr(h), _matrix(h, "out", _BF16, M, H)) if pre else (None, 0)
-
+    elif out is None:
+        h = _empty(x, x.shape, _BF16)
+        ld_h = x.shape[-1] if x.shape[0] > 1 else _one_row(x.shape[-1])
+    else:
+        _same_device(x, out)
+        ld_h = _matrix(out, "out", _BF16, *x.shape)
     x_out, stats = _norm_forward("glu_block_norm", x, y, gate, w_pre, b_pre, w_post, pre, post, res_scale, kind, eps,
-                                 outs, x_out)
+                                 (_ptr(h), ld_h), x_out)
     return x_out, h, stats
 
 
@@ -184,7 +193,7 @@ def glu_block_norm_mxfp8(x, y=None, *, gate=None, w_pre=None, b_pre=None, w_post
         q = x.new_empty((M, H), dtype=torch.uint8)
         s = x.new_empty((M, H // 32), dtype=torch.uint8)
     x_out, stats = _norm_forward("glu_block_norm_mxfp8", x, y, gate, w_pre, b_pre, w_post, True, post, res_scale,
-                                 kind, eps, lambda M, H: (_ptr(q), _ptr(s)), x_out)
+                                 kind, eps, (_ptr(q), _ptr(s)), x_out)
     return x_out, q, s, stats
 
 
@@ -211,10 +220,10 @@ def glu_block_norm_bwd(x, y, stats, dx_out, dh, *, gate=None, w_pre=None, b_pre=
 
     dgate, dw_post, dw_pre, db_pre = grad_of(gate), grad_of(w_post), grad_of(w_pre), grad_of(b_pre)
     nbytes = _size("glu_block_norm_bwd_work_bytes", M, H, groups)
-    work = x.new_empty((max(nbytes, 0),), dtype=torch.uint8)
+    work, ld = x.new_empty((max(nbytes, 0),), dtype=torch.uint8), H if M > 1 else _one_row(H)
     _call("glu_block_norm_bwd", k, flags, M, H, groups, _ptr(x), ld_x, _ptr(y), ld_y, _ptr(stats), _ptr(dx_out),
-          ld_dxo, _ptr(dh), ld_dh, _ptr(gate), _ptr(w_pre), _ptr(w_post), res_scale, _ptr(dx), H if M > 1 else
-          (H + 7) // 8 * 8, _ptr(dy), H if M > 1 else (H + 7) // 8 * 8, _ptr(dgate), _ptr(dw_pre), _ptr(db_pre),
+          ld_dxo, _ptr(dh), ld_dh, _ptr(gate), _ptr(w_pre), _ptr(w_post), res_scale, _ptr(dx), ld, _ptr(dy),
+          ld, _ptr(dgate), _ptr(dw_pre), _ptr(db_pre),
           _ptr(dw_post), _ptr(work), nbytes, _stream(x))
     return dx, dy, dgate, dw_post, dw_pre, db_pre
 
@@ -246,8 +255,10 @@ def glu_linear(x, w, bias=None, residual=None, *, act="none", offsets=None, save
         _like(bias, "bias", _BF16, w.shape[:-1])
     _same_device(x, w, bias, residual, offsets, out)
     ld_res = 0 if residual is None else _matrix(residual, "residual", _BF16, M, N)
-    y = out if out is not None else x.new_empty((M, N))
-    ld_y = _matrix(y, "out", _BF16, M, N)
+    if out is None:
+        y, ld_y = x.new_empty((M, N)), N
+    else:
+        y, ld_y = out, _matrix(out, "out", _BF16, M, N)
     pre = x.new_empty((M, N), dtype=torch.float16) if save_pre else None
     nbytes = _size("glu_linear_work_bytes", M, N, K, groups, int(offsets is not None))
     work = x.new_empty((nbytes,), dtype=torch.uint8) if nbytes > 0 else None
@@ -355,5 +366,5 @@ def glu_moe_combine_bwd(dout, y, rows, weights, offsets):
     dy = _empty(y, (T * k, H), _BF16)
     dw = torch.empty_like(weights)
     _call("glu_moe_combine_bwd", T, k, H, offsets.numel() - 1, _ptr(dout), ld_d, _ptr(y), ld_y, _ptr(rows),
-          _ptr(weights), _ptr(offsets), _ptr(dy), (H + 7) // 8 * 8 if T * k == 1 else H, _ptr(dw), _stream(y))
+          _ptr(weights), _ptr(offsets), _ptr(dy), _one_row(H) if T * k == 1 else H, _ptr(dw), _stream(y))
     return dy, dw
