@@ -6,6 +6,9 @@
 
 namespace glu {
 
+// A value that is the same in every lane, moved to a scalar register.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane((int)v); }
+
 struct __attribute__((packed, aligned(2))) Vec16 {
   u32x4 v;
 };
@@ -36,9 +39,18 @@ struct Raw<float> {
   }
 };
 
-// Loads elements 0..n-1 of p (n <= 0: none, n >= 8: all eight); the others read zero.
+// A lane offset that the compiler forgets the origin of: the address stays a scalar base plus
+// this offset, instead of a 64-bit lane pointer per operand kept across a loop over rows.
+__device__ __forceinline__ uint32_t lane_offset(uint32_t o) {
+  asm volatile("" : "+v"(o));
+  return o;
+}
+
+// Loads elements o .. o + n - 1 of p (n <= 0: none, n >= 8: all eight); the others read zero.  With a
+// wave-uniform p the address is a scalar base and a 32-bit lane offset.
 template <bool RAGGED>
-__device__ __forceinline__ void load(Raw<uint16_t>& r, const uint16_t* p, int n) {
+__device__ __forceinline__ void load(Raw<uint16_t>& r, const uint16_t* base, uint32_t o, int n) {
+  const uint16_t* p = reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(base) + lane_offset(2u * o));
   r.a = (u32x4)0u;
   if (n >= 8) {
     r.a = RAGGED ? reinterpret_cast<const Vec16*>(p)->v : *reinterpret_cast<const u32x4*>(p);
@@ -49,7 +61,8 @@ __device__ __forceinline__ void load(Raw<uint16_t>& r, const uint16_t* p, int n)
   }
 }
 template <bool RAGGED>
-__device__ __forceinline__ void load(Raw<float>& r, const float* p, int n) {
+__device__ __forceinline__ void load(Raw<float>& r, const float* base, uint32_t o, int n) {
+  const float* p = reinterpret_cast<const float*>(reinterpret_cast<const char*>(base) + lane_offset(4u * o));
   r.a = (u32x4)0u;
   r.b = (u32x4)0u;
   if (n >= 8) {
@@ -71,7 +84,8 @@ __device__ __forceinline__ void load(Raw<float>& r, const float* p, int n) {
 }
 
 template <bool RAGGED>
-__device__ __forceinline__ void store(uint16_t* p, const float (&f)[8], int n) {
+__device__ __forceinline__ void store(uint16_t* base, uint32_t o, const float (&f)[8], int n) {
+  uint16_t* p = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(base) + lane_offset(2u * o));
   u32x4 v;
 #pragma unroll
   for (int i = 0; i < 4; i++) v[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
@@ -85,7 +99,8 @@ __device__ __forceinline__ void store(uint16_t* p, const float (&f)[8], int n) {
   }
 }
 template <bool RAGGED>
-__device__ __forceinline__ void store(float* p, const float (&f)[8], int n) {
+__device__ __forceinline__ void store(float* base, uint32_t o, const float (&f)[8], int n) {
+  float* p = reinterpret_cast<float*>(reinterpret_cast<char*>(base) + lane_offset(4u * o));
   const u32x4 a = {__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
   const u32x4 b = {__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])};
   if (n >= 8) {
@@ -119,25 +134,37 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// Sums of N values over the workgroup, in every thread.  The two halves of `part` are used in
-// turn, so one barrier a call suffices: a half is written again only after the barrier of the
-// call in between.
+// Sums of N values over the workgroup (up to 16 waves), in every thread.  The two halves of `part`
+// are used in turn, so one barrier a call suffices: a half is written again only after the
+// barrier of the call in between.  Call clear_parts once before the first sum.
 template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float (*part)[16][N], int& turn) {
+struct BlockParts {
+  float v[2][16][N];
+};
+template <int N>
+__device__ __forceinline__ void clear_parts(BlockParts<N>& part) {
+  for (unsigned i = threadIdx.x; i < 2 * 16 * N; i += blockDim.x) (&part.v[0][0][0])[i] = 0.0f;
+  __syncthreads();
+}
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], BlockParts<N>& part, int& turn) {
 #pragma unroll
   for (int k = 0; k < N; k++) v[k] = wave_sum(v[k]);
-  const unsigned waves = blockDim.x >> 6;
-  if (waves == 1) return;
+  if (blockDim.x == 64) return;
   if ((threadIdx.x & 63u) == 0) {
 #pragma unroll
-    for (int k = 0; k < N; k++) part[turn][threadIdx.x >> 6][k] = v[k];
+    for (int k = 0; k < N; k++) part.v[turn][threadIdx.x >> 6][k] = v[k];
   }
   __syncthreads();
+  // absent waves hold zero; four waves' sums at a time, to hold few registers
 #pragma unroll
-  for (int k = 0; k < N; k++) v[k] = part[turn][0][k];
-  for (unsigned w = 1; w < waves; w++)
+  for (int k = 0; k < N; k++) v[k] = 0.0f;
+#pragma unroll 1
+  for (int w = 0; w < 16; w += 4)
 #pragma unroll
-    for (int k = 0; k < N; k++) v[k] += part[turn][w][k];
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int k = 0; k < N; k++) v[k] += part.v[turn][w + i][k];
   turn ^= 1;
 }
 

@@ -64,9 +64,11 @@ struct NormBwdArgs {
 // How the backward splits its rows over workgroups (a rule on shapes alone, so that the
 // workspace can be sized before the launch).
 struct NormBwdPlan {
-  int64_t groups;            // parameter groups
-  int64_t per_group;         // workgroups per group, or 1 with several groups per workgroup
-  int64_t blocks;            // workgroups = rows of partial sums
+  uint32_t groups;           // parameter groups
+  uint32_t per_group;        // split: workgroups per group
+  uint32_t part_rows;        // split: rows a workgroup; else whole groups a workgroup
+  uint32_t blocks;           // workgroups = rows of partial sums
+  bool split;                // a workgroup takes a part of one group
   unsigned threads;
   int vecs;                  // 8-column chunks per thread
 };

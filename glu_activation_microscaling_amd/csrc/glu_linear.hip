@@ -530,87 +530,119 @@ __global__ __launch_bounds__(256) void k_product_join(ProductArgs a, uint32_t sp
 
 // ---- few rows --------------------------------------------------------------------------------
 
-// The forward for a few rows (up to 64 of one group): a pass over W at memory speed.  A
-// workgroup takes 16 rows of W (columns of C); its waves take chunks of 128 elements of the sum
-// in turn, straight from memory into registers, multiply them as 16 x 16 x 32 tiles against 16,
-// 32, 48 or 64 rows of x, and join their sums through LDS.
+// The forward for a few rows (up to 64 of one group): a pass over W at memory speed.  A wave takes
+// 16 rows of W (columns of C) and multiplies them, straight from memory, as 16 x 16 x 32 tiles
+// against 16, 32, 48 or 64 rows of x; KW waves share the sum, taking chunks of 128 elements in
+// turn, and join through LDS, so a call is one launch whatever its extents.  The next chunks of
+// W are in flight while the present ones are multiplied.
+//   HALF, for up to 8 rows in all: a wave takes 8 rows of W, and a tile's other 8 rows (and
+//   columns, of x) are the same ones 32 elements on: the products of matching halves add up to
+//   the result, the others are dropped.  Twice the workgroups, and 128 bytes of a row a load.
 constexpr int FEW_WAVES = 8, FEW_ROWS = 64, FEW_CHUNK = 128;
 
-template <int RT>
-__device__ __forceinline__ void few_rows_sum(const ProductArgs& a, const RowTile& t, int64_t n0, int64_t k0, int64_t k1,
-                                             uint32_t lane, uint32_t wave, v4f (&acc)[4]) {
-  constexpr int UNROLL = RT <= 1 ? 4 : 2;   // chunks in flight
-  const uint32_t g = lane >> 4, r = lane & 15u;
-  const uint32_t wo = n0 + r < a.J ? 2u * (r * (uint32_t)a.ld_b + 8u * g) : kOob;
+template <int RT, bool HALF>
+__device__ __forceinline__ void few_rows_sum(const ProductArgs& a, const RowTile& t, int64_t n0, uint32_t first,
+                                             uint32_t stride, uint32_t k1, uint32_t lane, v4f (&acc)[4]) {
+  constexpr int U = HALF ? 4 : RT == 1 ? 2 : 1;   // chunks per stage
+  constexpr int STEPS = HALF ? 2 : 4;             // tiles per chunk
+  const uint32_t g = lane >> 4, r = HALF ? lane & 7u : lane & 15u;
+  const uint32_t mine = 8u * g + (HALF ? 32u * (lane >> 3 & 1u) : 0u);   // the lane's elements in a tile
+  const uint32_t wo = n0 + r < a.J ? 2u * (r * (uint32_t)a.ld_b + mine) : kOob;
   uint32_t xo[RT];
 #pragma unroll
   for (int i = 0; i < RT; i++)
-    xo[i] = t.i0 + 16 * i + r < t.i1 ? 2u * ((16u * i + r) * (uint32_t)a.ld_a + 8u * g) : kOob;
-  const auto rw = rsrc(a.b + t.group * a.b_group + n0 * a.ld_b), rx = rsrc(a.a + t.i0 * a.ld_a);
-  for (int64_t k = k0 + FEW_CHUNK * wave; k < k1; k += FEW_CHUNK * FEW_WAVES * UNROLL) {
-    v8bf w[UNROLL][4], x[UNROLL][4][RT];
+    xo[i] = t.i0 + 16 * i + r < t.i1 ? 2u * ((16u * i + r) * (uint32_t)a.ld_a + mine) : kOob;
+  const auto rw = rsrc(uniform(a.b + t.group * a.b_group + n0 * a.ld_b)), rx = rsrc(uniform(a.a + t.i0 * a.ld_a));
+  v8bf w[2][U][STEPS];
+  auto load_w = [&](uint32_t k, int s) {
 #pragma unroll
-    for (int c = 0; c < UNROLL; c++) {
+    for (int c = 0; c < U; c++)
 #pragma unroll
-      for (int u = 0; u < 4; u++) {
-        const int64_t kk = k + FEW_CHUNK * FEW_WAVES * c + 32 * u;
-        const bool in = kk + 8 * g < k1;
-        w[c][u] = __builtin_bit_cast(v8bf, __builtin_amdgcn_raw_buffer_load_b128(rw, in ? wo : kOob, (int)(2 * kk), 0));
-#pragma unroll
-        for (int i = 0; i < RT; i++)
-          x[c][u][i] =
-              __builtin_bit_cast(v8bf, __builtin_amdgcn_raw_buffer_load_b128(rx, in ? xo[i] : kOob, (int)(2 * kk), 0));
+      for (int u = 0; u < STEPS; u++) {
+        const uint32_t kk = k + stride * c + FEW_CHUNK / STEPS * u;
+        w[s][c][u] = __builtin_bit_cast(
+            v8bf, __builtin_amdgcn_raw_buffer_load_b128(rw, kk + mine < k1 ? wo : kOob, (int)(2u * kk), 0));
       }
-    }
+  };
+  // x of this stage before W of the next: loads return in order, and the products wait for x
+  auto step = [&](uint32_t k, int s) {
+    v8bf x[U][STEPS][RT];
 #pragma unroll
-    for (int c = 0; c < UNROLL; c++)
+    for (int c = 0; c < U; c++)
 #pragma unroll
-      for (int u = 0; u < 4; u++)
+      for (int u = 0; u < STEPS; u++) {
+        const uint32_t kk = k + stride * c + FEW_CHUNK / STEPS * u;
 #pragma unroll
         for (int i = 0; i < RT; i++)
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[c][u], x[c][u][i], acc[i], 0, 0, 0);
+          x[c][u][i] = __builtin_bit_cast(
+              v8bf, __builtin_amdgcn_raw_buffer_load_b128(rx, kk + mine < k1 ? xo[i] : kOob, (int)(2u * kk), 0));
+      }
+    __builtin_amdgcn_sched_barrier(0);
+    if (k + stride * U < k1) load_w(k + stride * U, 1 - s);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int c = 0; c < U; c++)
+#pragma unroll
+      for (int u = 0; u < STEPS; u++)
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[s][c][u], x[c][u][i], acc[i], 0, 0, 0);
+  };
+  if (first >= k1) return;
+  load_w(first, 0);
+  for (uint32_t k = first; k < k1; k += 2 * stride * U) {
+    step(k, 0);
+    if (k + stride * U < k1) step(k + stride * U, 1);
   }
 }
 
-// grid: (16-column tiles, row tiles, parts of the sum)
-template <int ACT>
-__global__ __launch_bounds__(64 * FEW_WAVES) void k_few_rows(ProductArgs a) {
-  __shared__ v4f sums[FEW_WAVES][FEW_ROWS / 16][64];
+// grid: (column tiles of 16 FEW_WAVES / KW, or half that; row tiles)
+template <int ACT, int KW, bool HALF>
+__global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_few_rows(ProductArgs a) {
+  __shared__ v4f sums[FEW_WAVES][HALF ? 1 : FEW_ROWS / 16][64];
+  constexpr int COLS = HALF ? 8 : 16;
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const RowTile t = find_tile(a.offsets, a.groups, a.I, blockIdx.y, FEW_ROWS);
   if (t.group < 0) return;
-  const int64_t n0 = 16 * (int64_t)blockIdx.x;
-  int64_t k0 = 0, k1 = t.group < a.groups ? a.K : 0;
-  if (gridDim.z > 1) {
-    const int64_t chunks = (k1 + FEW_CHUNK - 1) / FEW_CHUNK;
-    k0 = chunks * blockIdx.z / gridDim.z * FEW_CHUNK;
-    k1 = min(k1, chunks * (blockIdx.z + 1) / gridDim.z * FEW_CHUNK);
-  }
-  const int rt = (int)((t.i1 - t.i0 + 15) / 16);
+  const int64_t n0 = COLS * ((int64_t)blockIdx.x * (FEW_WAVES / KW) + wave / KW);
+  const int rt = HALF ? 1 : (int)((t.i1 - t.i0 + 15) / 16);
   v4f acc[4];
 #pragma unroll
   for (int i = 0; i < 4; i++) acc[i] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  if (k0 < k1) {
-    if (rt == 1) few_rows_sum<1>(a, t, n0, k0, k1, lane, wave, acc);
-    else if (rt == 2) few_rows_sum<2>(a, t, n0, k0, k1, lane, wave, acc);
-    else if (rt == 3) few_rows_sum<3>(a, t, n0, k0, k1, lane, wave, acc);
-    else few_rows_sum<4>(a, t, n0, k0, k1, lane, wave, acc);
+  if (t.group < a.groups && n0 < a.J) {
+    const uint32_t first = FEW_CHUNK * (wave % KW), stride = FEW_CHUNK * KW, k1 = (uint32_t)a.K;
+    if constexpr (HALF) {
+      few_rows_sum<1, true>(a, t, n0, first, stride, k1, lane, acc);
+    } else {
+      if (rt == 1) few_rows_sum<1, false>(a, t, n0, first, stride, k1, lane, acc);
+      else if (rt == 2) few_rows_sum<2, false>(a, t, n0, first, stride, k1, lane, acc);
+      else if (rt == 3) few_rows_sum<3, false>(a, t, n0, first, stride, k1, lane, acc);
+      else few_rows_sum<4, false>(a, t, n0, first, stride, k1, lane, acc);
+    }
   }
+  if constexpr (KW > 1 || HALF) {
 #pragma unroll
-  for (int i = 0; i < 4; i++)
-    if (i < rt) sums[wave][i][lane] = acc[i];
-  __syncthreads();
-  const int i = threadIdx.x >> 6;
-  if (i >= rt) return;
-  v4f s = sums[0][i][lane];
+    for (int i = 0; i < (HALF ? 1 : 4); i++)
+      if (i < rt) sums[wave][i][lane] = acc[i];
+    __syncthreads();
+  }
+  if (HALF && (lane & 40u) != 0) return;   // results are in rows and columns 0 .. 7 of the tile
+  // row tile i of a column tile is finished by wave i % KW of those that share it
 #pragma unroll
-  for (int w = 1; w < FEW_WAVES; w++) s += sums[w][i][lane];
-  const int64_t row = t.i0 + 16 * i + (lane & 15u), col = n0 + 4 * (lane >> 4);
-  if (row >= t.i1 || col >= a.J) return;
-  if (gridDim.z > 1) {
-    *reinterpret_cast<v4f*>(a.work + ((int64_t)blockIdx.z * a.I + row) * a.J + col) = s;
-  } else {
+  for (int i = 0; i < (HALF ? 1 : 4); i++) {
+    if (i >= rt || wave % KW != i % KW) continue;
+    v4f s = acc[i];
+    if constexpr (KW > 1 || HALF) {
+      s = (v4f)0.0f;
+#pragma unroll
+      for (int w = 0; w < KW; w++) {
+        s += sums[wave / KW * KW + w][i][lane];
+        if constexpr (HALF) s += sums[wave / KW * KW + w][i][lane + 40];   // rows and columns 8 .. 15
+      }
+    }
+    const int64_t row = t.i0 + 16 * i + (lane & 15u), col = n0 + 4 * (lane >> 4);
+    if (row >= t.i1 || col >= a.J) continue;
     float v[4] = {s[0], s[1], s[2], s[3]};
     finish<FWD, ACT, 4>(a, t.group, row, col, v);
   }
@@ -620,7 +652,8 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void k_few_rows(ProductArgs a) {
 
 enum { TILE_256, TILE_128, FEW };
 struct ProductPlan {
-  int kind;
+  int kind, share;
+  bool half;
   int64_t tiles_i, tiles_j, splits;
 };
 
@@ -635,11 +668,13 @@ ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t grou
   if (mode == FWD && I <= (grouped ? FEW_ROWS / 2 * groups : FEW_ROWS)) {
     p.kind = FEW;
     p.tiles_i = ceil_div(I, FEW_ROWS) + (grouped ? groups : 0);
-    p.tiles_j = ceil_div(J, 16);
-    if (!grouped && p.tiles_j < 256) {
-      const int64_t most = K / (2 * FEW_WAVES * FEW_CHUNK), want = ceil_div(256, p.tiles_j);
-      p.splits = want < most ? want : most;
-    }
+    // waves sharing a sum: as few as give 16 waves a compute unit, with four chunks or more each
+    p.half = !grouped && I <= 8;
+    const int64_t cols = p.half ? 8 : 16;
+    p.share = 1;
+    while (p.share < FEW_WAVES && ceil_div(J, cols) * p.tiles_i * p.share < 4096 && K >= 8 * p.share * FEW_CHUNK)
+      p.share *= 2;
+    p.tiles_j = ceil_div(J, cols * FEW_WAVES / p.share);
   } else {
     const int64_t extra = grouped && mode != WGRAD ? groups : 0, outer = mode == WGRAD ? groups : 1;
     auto tiles = [&](int64_t b) { return (ceil_div(I, b) + extra) * ceil_div(J, b) * outer; };
@@ -666,8 +701,15 @@ hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
   const ProductPlan p = plan_product(MODE, a.I, a.J, a.K, a.groups, a.offsets != nullptr);
   hipError_t e;
   if (p.kind == FEW) {
-    e = launch_kernel(k_few_rows<ACT>, dim3((unsigned)p.tiles_j, (unsigned)p.tiles_i, (unsigned)p.splits),
-                      dim3(64 * FEW_WAVES), s, a);
+    const dim3 grid((unsigned)p.tiles_j, (unsigned)p.tiles_i), block(64 * FEW_WAVES);
+    auto go = [&](auto KW) {
+      return p.half ? launch_kernel(k_few_rows<ACT, decltype(KW)::value, true>, grid, block, s, a)
+                    : launch_kernel(k_few_rows<ACT, decltype(KW)::value, false>, grid, block, s, a);
+    };
+    return p.share == 1   ? go(std::integral_constant<int, 1>{})
+           : p.share == 2 ? go(std::integral_constant<int, 2>{})
+           : p.share == 4 ? go(std::integral_constant<int, 4>{})
+                          : go(std::integral_constant<int, 8>{});
   } else {
     const unsigned n = (unsigned)(p.tiles_i * p.tiles_j * p.splits * (MODE == WGRAD ? a.groups : 1));
     e = p.kind == TILE_256
@@ -711,16 +753,16 @@ __global__ __launch_bounds__(256) void k_linear_grad(GradArgs a) {
   if (col < a.N) {
     for (int64_t row = r0 + lr; row < r1; row += 8) {
       Raw<uint16_t> q;
-      load<false>(q, a.dy + row * a.ld_dy + col, 8);
+      load<false>(q, a.dy + row * a.ld_dy, (uint32_t)col, 8);
       float d[8];
       q.get(d);
       if constexpr (ACT != LIN_NONE) {
-        load<false>(q, a.pre + row * a.N + col, 8);
+        load<false>(q, a.pre + row * a.N, (uint32_t)col, 8);
 #pragma unroll
         for (int i = 0; i < 8; i++)
           d[i] *= act_grad<ACT>((float)__builtin_bit_cast(_Float16, (uint16_t)(q.a[i / 2] >> (16 * (i & 1)))));
       }
-      if (a.dp != nullptr) store<false>(a.dp + row * a.N + col, d, 8);
+      if (a.dp != nullptr) store<false>(a.dp + row * a.N, (uint32_t)col, d, 8);
 #pragma unroll
       for (int i = 0; i < 8; i++) s[i] += d[i];
     }

@@ -48,34 +48,47 @@ __global__ __launch_bounds__(SORT_THREADS) void k_moe_count(MoeSortArgs a) {
 // share it).
 __global__ __launch_bounds__(SORT_THREADS) void k_moe_place(MoeSortArgs a) {
   __shared__ int next[SORT_WAVES][kMaxExperts];   // counts, then the next place, per wave
-  __shared__ int wave_total[SORT_WAVES];
+  __shared__ int wave_total[SORT_WAVES], sum_all[kMaxExperts], sum_early[kMaxExperts];
   const int E = a.experts;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t b0 = sort_begin(a.n, gridDim.x, blockIdx.x), b1 = sort_begin(a.n, gridDim.x, blockIdx.x + 1);
   const int64_t i0 = b0 + sort_begin(b1 - b0, SORT_WAVES, wave), i1 = b0 + sort_begin(b1 - b0, SORT_WAVES, wave + 1);
-  for (int e = threadIdx.x; e < E; e += SORT_THREADS)
-    for (int w = 0; w < SORT_WAVES; w++) next[w][e] = 0;
+  for (int x = threadIdx.x; x < E; x += SORT_THREADS) {
+    for (int w = 0; w < SORT_WAVES; w++) next[w][x] = 0;
+    sum_all[x] = sum_early[x] = 0;
+  }
   __syncthreads();
   for (int64_t i = i0 + lane; i < i1; i += 64) {
     const int e = expert_at(a.ids, i, a.id_bytes, E);
     if (e >= 0) atomicAdd(&next[wave][e], 1);
   }
   __syncthreads();
-  // thread e: this workgroup's counts become places relative to the expert's start; the
-  // expert's total is scanned over the threads
+  // totals of the experts, and of them what earlier workgroups have; 1024 / E threads an expert
+  // share the other workgroups' counts
   const int e = threadIdx.x;
   int total = 0, before = 0;
-  if (e < E) {
-    if (gridDim.x > 1) {
-      for (unsigned b = 0; b < gridDim.x; b++) {
-        const int c = a.work[(int64_t)b * E + e];
-        total += c;
-        if (b < blockIdx.x) before += c;
+  if (gridDim.x > 1) {
+    const int share = SORT_THREADS / E, part = threadIdx.x / E, x = threadIdx.x % E;
+    if (part < share) {
+      int all = 0, early = 0;
+#pragma unroll 4
+      for (unsigned b = part; b < gridDim.x; b += share) {
+        const int c = a.work[(int64_t)b * E + x];
+        all += c;
+        early += b < blockIdx.x ? c : 0;
       }
-    } else {
-      for (int w = 0; w < SORT_WAVES; w++) total += next[w][e];
+      atomicAdd(&sum_all[x], all);
+      atomicAdd(&sum_early[x], early);
     }
+    __syncthreads();
+    if (e < E) {
+      total = sum_all[e];
+      before = sum_early[e];
+    }
+  } else if (e < E) {
+    for (int w = 0; w < SORT_WAVES; w++) total += next[w][e];
   }
+  // thread e: the expert's start is the scan of the totals; this workgroup's counts become places
   int scan = total;
   for (int d = 1; d < 64; d <<= 1) {
     const int v = __shfl_up(scan, d);
@@ -169,6 +182,7 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_moe_permute(MoePermuteArgs a) 
 
 // grid: (parts of 2048 columns, tokens)
 constexpr int64_t SUM_PART = 8 * MOVE_THREADS;
+constexpr int SUM_CHOICES = 8;
 template <bool RAGGED>
 __global__ __launch_bounds__(MOVE_THREADS) void k_moe_combine(MoeCombineArgs a) {
   const int64_t c = SUM_PART * blockIdx.x + 8 * (int64_t)threadIdx.x;
@@ -179,21 +193,33 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_moe_combine(MoeCombineArgs a) 
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (a.residual != nullptr) {
       Raw<uint16_t> r;
-      load<RAGGED>(r, a.residual + t * a.ld_res + c, n);
+      load<RAGGED>(r, a.residual + t * a.ld_res, (uint32_t)c, n);
       r.get(s);
     }
-    for (int64_t j = 0; j < a.choices; j++) {
-      const int64_t r = a.rows[t * a.choices + j];
-      if (r < 0 || r >= rows) continue;
-      const float w = a.weights != nullptr ? a.weights[t * a.choices + j] : 1.0f;
-      Raw<uint16_t> q;
-      float f[8];
-      load<RAGGED>(q, a.y + r * a.ld_y + c, n);
-      q.get(f);
+    for (int64_t j0 = 0; j0 < a.choices; j0 += SUM_CHOICES) {
+      // all rows of the batch are in flight before the first is added
+      Raw<uint16_t> q[SUM_CHOICES];
+      float w[SUM_CHOICES];
 #pragma unroll
-      for (int i = 0; i < 8; i++) s[i] = __builtin_fmaf(w, f[i], s[i]);
+      for (int j = 0; j < SUM_CHOICES; j++) {
+        const int64_t i = t * a.choices + j0 + j;
+        const int64_t r = j0 + j < a.choices ? a.rows[i] : -1;
+        w[j] = 0.0f;
+        q[j].a = (u32x4)0u;
+        if (r >= 0 && r < rows) {
+          load<RAGGED>(q[j], a.y + r * a.ld_y, (uint32_t)c, n);
+          w[j] = a.weights != nullptr ? a.weights[i] : 1.0f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < SUM_CHOICES; j++) {
+        float f[8];
+        q[j].get(f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) s[i] = __builtin_fmaf(w[j], f[i], s[i]);
+      }
     }
-    store<RAGGED>(a.out + t * a.ld_out + c, s, n);
+    store<RAGGED>(a.out + t * a.ld_out, (uint32_t)c, s, n);
   }
 }
 
@@ -201,8 +227,9 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_moe_combine(MoeCombineArgs a) 
 constexpr int GRAD_CHOICES = 8;
 template <bool RAGGED>
 __global__ __launch_bounds__(MOVE_THREADS) void k_moe_combine_bwd(MoeCombineBwdArgs a) {
-  __shared__ float part[2][16][GRAD_CHOICES];
+  __shared__ BlockParts<GRAD_CHOICES> part;
   int turn = 0;
+  clear_parts(part);
   const int64_t used = max(a.offsets[a.experts], 0), rows = a.tokens * a.choices;
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
     for (int64_t j0 = 0; j0 < a.choices; j0 += GRAD_CHOICES) {
@@ -220,20 +247,20 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_moe_combine_bwd(MoeCombineBwdA
         const int n = (int)min((int64_t)8, a.H - c);
         Raw<uint16_t> q;
         float g[8];
-        load<RAGGED>(q, a.dout + t * a.ld_dout + c, n);
+        load<RAGGED>(q, a.dout + t * a.ld_dout, (uint32_t)c, n);
         q.get(g);
 #pragma unroll
         for (int j = 0; j < GRAD_CHOICES; j++) {
           if (r[j] < 0) continue;
           float f[8], d[8];
-          load<RAGGED>(q, a.y + r[j] * a.ld_y + c, n);
+          load<RAGGED>(q, a.y + r[j] * a.ld_y, (uint32_t)c, n);
           q.get(f);
 #pragma unroll
           for (int i = 0; i < 8; i++) {
             dot[j] = __builtin_fmaf(g[i], f[i], dot[j]);
             d[i] = w[j] * g[i];
           }
-          store<RAGGED>(a.dy + r[j] * a.ld_dy + c, d, n);
+          store<RAGGED>(a.dy + r[j] * a.ld_dy, (uint32_t)c, d, n);
         }
       }
       block_sum(dot, part, turn);
@@ -249,11 +276,12 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_moe_combine_bwd(MoeCombineBwdA
 
 }  // namespace
 
-// Workgroups of the sort: parts of 1024 choices or more, at most 64 (each reads the others'
-// counts).
+// Workgroups of the sort: one up to 4096 choices (one launch), else parts of 1024 choices or more,
+// at most 64 (each reads the others' counts).
 int64_t moe_sort_blocks(int64_t n) {
+  if (n <= 4 * SORT_THREADS) return 1;
   const int64_t b = (n + SORT_THREADS - 1) / SORT_THREADS;
-  return b < 1 ? 1 : b < 64 ? b : 64;
+  return b < 64 ? b : 64;
 }
 
 hipError_t launch_moe_sort(const MoeSortArgs& a, hipStream_t s) {
