@@ -159,8 +159,11 @@ constexpr uint32_t BK = 64;   // elements of the sum per step: one 128-byte line
 //   k along rows (T = false): a row's 128 bytes hold its BK elements; 16-byte chunk c of row R
 //     lies at chunk c ^ (R / 2 % 8), so a fragment read touches every LDS bank once.
 //   transposed (T = true): an LDS row holds one element of the sum for all B_ rows; its
-//     32-byte segment s of element k lies at segment s ^ (k % 8), and the fragment is
-//     gathered by two transposing reads of 4 elements each (16 lanes take a 4 x 16 block).
+//     32-byte segment s of element k lies at segment s ^ turn(k), and the fragment is gathered by
+//     two transposing reads of 4 elements each.  Such a read takes 256 bytes at a time: two
+//     4 x 16 blocks, 8 elements apart, whose rows turn() spreads over all banks.
+__device__ __forceinline__ uint32_t turn(uint32_t k) { return (k & 3u) | (k >> 1 & 4u); }
+
 template <bool T, int B_, int WAVES>
 struct Operand {
   static constexpr int LOADS = B_ * BK * 2 / 1024 / WAVES;     // 1 KiB blocks per wave and step
@@ -191,7 +194,7 @@ struct Operand {
 #pragma unroll
       for (int q = 0; q < LOADS; q++) {
         const uint32_t k = (wave * LOADS + q) * (64u / CH) + lane / CH;
-        const uint32_t chunk = (lane % CH) ^ (2u * (k & 7u));
+        const uint32_t chunk = (lane % CH) ^ (2u * turn(k));
         off[q] = i0 + 8u * chunk < i1 ? 2u * (k * (uint32_t)ld + 8u * chunk) : kOob;
       }
       kk = wave * LOADS * (64u / CH) + lane / CH;
@@ -227,13 +230,13 @@ __device__ __forceinline__ v4s transposed(const uint8_t* __restrict__ p) {
 
 // A lane's fragment addresses of an operand in LDS.  Wave w of W along this operand owns TILES
 // tiles of 16 rows: consecutive ones, or, transposed, every W-th one (tile i of the wave is tile
-// i W + w).  With that, the segment of tile i and element 8 g + 4 u + q is
-//   (i W + w) ^ (4 u + q) = 4 (i / (4 / W) ^ u) + ((i % (4 / W)) W + w) ^ q,
-// whose first part is a constant of the unrolled code and whose second takes 4 / W values.
+// i W + w).  The lane reads elements k = 8 g + 4 u + q of tile i at segment
+//   (i W + w) ^ turn(k) = 8 (i / (8 / W)) + ((i % (8 / W)) W + w) ^ (q + 4 (g % 2)),
+// whose first part is a constant of the unrolled code and whose second takes 8 / W values.
 template <bool T, int B_, int W, int TILES>
 struct Fragments {
-  static constexpr int BASES = 4 / W;
-  uint32_t at[2];
+  static constexpr int BASES = T ? (8 / W < TILES ? 8 / W : TILES) : 2;
+  uint32_t at[BASES];
   static __device__ __forceinline__ uint32_t tile(uint32_t w, int i) { return T ? i * W + w : w * TILES + i; }
   __device__ __forceinline__ void init(uint32_t w, uint32_t lane) {
     const uint32_t g = lane >> 4, r = lane & 15u;
@@ -244,16 +247,15 @@ struct Fragments {
       const uint32_t q = r >> 2;
 #pragma unroll
       for (uint32_t m = 0; m < BASES; m++)
-        at[m] = (8u * g + q) * (2u * B_) + 32u * ((m * W + w) ^ q) + 8u * (r & 3u);
+        at[m] = (8u * g + q) * (2u * B_) + 32u * ((m * W + w) ^ (q + 4u * (g & 1u))) + 8u * (r & 3u);
     }
   }
   __device__ __forceinline__ v8bf read(const uint8_t* lds, int i, int h) const {
     if constexpr (!T) {
       return *reinterpret_cast<const v8bf*>(lds + at[h] + 2048u * i);
     } else {
-      const uint8_t* p = lds + at[i % BASES] + 2u * B_ * 32u * h;
-      const v4s lo = transposed(p + 128 * (i / BASES));
-      const v4s hi = transposed(p + 8 * B_ + 128 * ((i / BASES) ^ 1));
+      const uint8_t* p = lds + at[i % BASES] + 2u * B_ * 32u * h + 256 * (i / (8 / W));
+      const v4s lo = transposed(p), hi = transposed(p + 8 * B_);
       return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
@@ -427,15 +429,41 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
       for (int j = 0; j < TJ; j++)
         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[h][j], xa[h][i], acc[i][j], 0, 0, 0);
   };
-  auto step = [&](uint32_t k, int stage) {
+  // The scheduler's groups: a fragment read to every few products, so that neither the matrix
+  // cores nor LDS wait for a burst of the other.
+  constexpr int READS = TI * (TA ? 2 : 1) + TJ * (TB ? 2 : 1), PRODUCTS = TI * TJ;
+  constexpr int LOADS = OpA::LOADS + OpB::LOADS;
+  enum { G_MFMA = 0x8, G_VMEM = 0x10, G_DS_READ = 0x100 };
+  auto step = [&](uint32_t k, int stage, auto FULL) {
     read(stage, 1);
     multiply(0);
+#pragma unroll
+    for (int q = 0; q < READS; q++) {
+      __builtin_amdgcn_sched_group_barrier(G_DS_READ, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(G_MFMA, PRODUCTS / READS, 0);
+    }
     __builtin_amdgcn_sched_barrier(0);   // the products above are not to sink below the wait
     wait_vm<0>();
     lds_barrier();
-    start(k + 2 * BK, stage);
-    if (k + BK < k1) read(1 - stage, 0);
-    multiply(1);
+    if constexpr (decltype(FULL)::value) {   // at least two whole steps follow: no branches
+      issue(k + 2 * BK, stage);
+      read(1 - stage, 0);
+      multiply(1);
+#pragma unroll
+      for (int q = 0; q < LOADS; q++) {
+        __builtin_amdgcn_sched_group_barrier(G_VMEM, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(G_MFMA, 1, 0);
+      }
+#pragma unroll
+      for (int q = 0; q < READS; q++) {
+        __builtin_amdgcn_sched_group_barrier(G_DS_READ, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(G_MFMA, (PRODUCTS - LOADS) / READS > 1 ? (PRODUCTS - LOADS) / READS : 1, 0);
+      }
+    } else {
+      start(k + 2 * BK, stage);
+      if (k + BK < k1) read(1 - stage, 0);
+      multiply(1);
+    }
     __builtin_amdgcn_sched_barrier(0);
     wait_lds();   // long since arrived; said here so that the loop's head waits for no more
   };
@@ -447,9 +475,14 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
     start(k0 + BK, 1);
     read(0, 0);
     wait_lds();
-    for (uint32_t k = k0; k < k1; k += 2 * BK) {
-      step(k, 0);
-      if (k + BK < k1) step(k + BK, 1);
+    uint32_t k = k0;
+    for (; k + 4 * BK <= k1; k += 2 * BK) {
+      step(k, 0, std::true_type{});
+      step(k + BK, 1, std::true_type{});
+    }
+    for (; k < k1; k += 2 * BK) {
+      step(k, 0, std::false_type{});
+      if (k + BK < k1) step(k + BK, 1, std::false_type{});
     }
   }
 
