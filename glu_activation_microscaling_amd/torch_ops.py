@@ -17,17 +17,28 @@ that torch.compile keeps whole; these ops do the same for the MI355X kernels:
   torch.ops.glu_mx.glu_gemm_mxfp8(xq, xs, wq, ws, act, fmt, w_layout)  -> (q_row, s_row)
   torch.ops.glu_mx.glu_gemm_nvfp4(xq, xs, wq, ws, act, sf_layout, fmt, w_layout) -> (q, sf)
   torch.ops.glu_mx.glu_gemm_nvfp4_gs(xq, xs, wq, ws, amax, act, sf_layout, fmt, w_layout) -> (q, sf)
+  torch.ops.glu_mx.block_norm(x, y, gate, w_pre, b_pre, w_post, post, res_scale, kind, eps)
+                                                                       -> (x_out, h, stats)
+  torch.ops.glu_mx.block_norm_backward(x, y, stats, dx_out, dh, gate, w_pre, b_pre, w_post, post,
+                                       res_scale, kind)  -> (dx, dy, dgate, dw_post, dw_pre, db_pre)
+  torch.ops.glu_mx.linear(x, w, bias, residual, offsets, act, save_pre) -> (y, pre)
+  torch.ops.glu_mx.linear_backward(dy, x, w, pre, offsets, act, bias)  -> (dx, dw, db)
+  torch.ops.glu_mx.moe_sort(ids, experts)                              -> (rows, offsets)
+  torch.ops.glu_mx.moe_permute(x, rows, offsets)                       -> xs
+  torch.ops.glu_mx.moe_combine(y, rows, offsets, weights, residual)    -> out
+  torch.ops.glu_mx.moe_combine_backward(dout, y, rows, weights, offsets) -> (dy, dweights)
 
 Each real implementation is the binding function of the same name (argument marshalling;
 the HIP kernels compute everything).  Each fake implementation gives the output shapes and
 dtypes without touching a GPU, so FakeTensor tracing and torch.compile(fullgraph=True)
 capture the ops as single graph nodes.  `glu` is differentiable: its backward is the
-`glu_backward` op (the fused BF16 backward kernel).  The quantized ops are not
+`glu_backward` op (the fused BF16 backward kernel); so are block_norm, linear, moe_permute and
+moe_combine, through the backward ops beside them.  The quantized ops are not
 differentiable.  In the split layout `up` is the second operand; in the paired layout pass
 an empty `up` (a 0-element tensor), since a custom op cannot take None for a tensor that
 other layouts need.
 """
-from typing import Tuple
+from typing import Optional, Tuple
 
 import torch
 from torch import Tensor
@@ -37,6 +48,9 @@ from . import (glu_amax as _amax, glu_bwd as _bwd, glu_bwd_mxfp8 as _bwd_mx,
                glu_fwd_nvfp4 as _fwd_nv, glu_fwd_nvfp4_gs as _fwd_nv_gs, glu_gemm as _gemm,
                glu_gemm_mxfp8 as _gemm_mx, glu_gemm_nvfp4 as _gemm_nv,
                glu_gemm_nvfp4_gs as _gemm_nv_gs)
+from . import (glu_block_norm as _norm, glu_block_norm_bwd as _norm_bwd, glu_linear as _linear,
+               glu_linear_bwd as _linear_bwd, glu_moe_combine as _combine,
+               glu_moe_combine_bwd as _combine_bwd, glu_moe_permute as _permute, glu_moe_sort as _sort)
 
 _LIB = "glu_mx"
 
@@ -249,3 +263,178 @@ def _(xq, xs, wq, ws, amax, act="geglu", sf_layout="rowmajor", fmt="mxfp8", w_la
     M, N = xq.shape[0], wq.shape[0] // 2
     return (xq.new_empty((M, N // 2), dtype=torch.uint8),
             xq.new_empty(_nv_scale_shape(M, N, sf_layout), dtype=torch.uint8))
+
+
+# ---- block norms, differentiable ------------------------------------------------------
+# Without y, x' is x itself and x_out comes back zero-sized (an op may not return its input).
+
+@torch.library.custom_op(f"{_LIB}::block_norm", mutates_args=())
+def block_norm(x: Tensor, y: Optional[Tensor] = None, gate: Optional[Tensor] = None,
+               w_pre: Optional[Tensor] = None, b_pre: Optional[Tensor] = None, w_post: Optional[Tensor] = None,
+               post: bool = False, res_scale: float = 1.0, kind: str = "rms",
+               eps: float = 1e-6) -> Tuple[Tensor, Tensor, Tensor]:
+    x_out, h, stats = _norm(x, y, gate=gate, w_pre=w_pre, b_pre=b_pre, w_post=w_post, post=post,
+                            res_scale=res_scale, kind=kind, eps=eps)
+    return x.new_empty((0,)) if y is None else x_out, h, stats
+
+
+@block_norm.register_fake
+def _(x, y=None, gate=None, w_pre=None, b_pre=None, w_post=None, post=False, res_scale=1.0, kind="rms", eps=1e-6):
+    return (x.new_empty((0,) if y is None else x.shape), x.new_empty(x.shape, dtype=torch.bfloat16),
+            x.new_empty((x.shape[0], 4), dtype=torch.float32))
+
+
+@torch.library.custom_op(f"{_LIB}::block_norm_backward", mutates_args=())
+def block_norm_backward(x: Tensor, y: Optional[Tensor], stats: Tensor, dx_out: Optional[Tensor], dh: Tensor,
+                        gate: Optional[Tensor], w_pre: Optional[Tensor], b_pre: Optional[Tensor],
+                        w_post: Optional[Tensor], post: bool, res_scale: float,
+                        kind: str) -> Tuple[Tensor, Tensor, Tensor, Tensor, Tensor, Tensor]:
+    return _norm_bwd(x, y, stats, dx_out, dh, gate=gate, w_pre=w_pre, b_pre=b_pre, w_post=w_post, post=post,
+                     res_scale=res_scale, kind=kind)
+
+
+@block_norm_backward.register_fake
+def _(x, y, stats, dx_out, dh, gate, w_pre, b_pre, w_post, post, res_scale, kind):
+    def like(t):
+        return x.new_empty((0,), dtype=torch.bfloat16) if t is None else t.new_empty(t.shape)
+    return x.new_empty(x.shape), like(y), like(gate), like(w_post), like(w_pre), like(b_pre)
+
+
+def _norm_setup(ctx, inputs, output):
+    x, y, gate, w_pre, b_pre, w_post, ctx.post, ctx.res_scale, ctx.kind, _ = inputs
+    ctx.save_for_backward(x, y, output[2], gate, w_pre, b_pre, w_post)
+
+
+def _norm_grad(ctx, dx_out, dh, _):
+    x, y, stats, gate, w_pre, b_pre, w_post = ctx.saved_tensors
+    dx, dy, dgate, dw_post, dw_pre, db_pre = block_norm_backward(
+        x, y, stats, None if y is None else dx_out.contiguous(), dh.contiguous(), gate, w_pre, b_pre, w_post,
+        ctx.post, ctx.res_scale, ctx.kind)
+    grads = [g if t is not None else None for g, t in ((dy, y), (dgate, gate), (dw_pre, w_pre), (db_pre, b_pre),
+                                                      (dw_post, w_post))]
+    return (dx, *grads, None, None, None, None)
+
+
+block_norm.register_autograd(_norm_grad, setup_context=_norm_setup)
+
+
+# ---- linear products, differentiable ----------------------------------------------------
+# pre is the pre-activation the backward needs, zero-sized when act is "none" or save_pre is off
+# (then only y's residual has a gradient with an act).
+
+@torch.library.custom_op(f"{_LIB}::linear", mutates_args=())
+def linear(x: Tensor, w: Tensor, bias: Optional[Tensor] = None, residual: Optional[Tensor] = None,
+           offsets: Optional[Tensor] = None, act: str = "none", save_pre: bool = True) -> Tuple[Tensor, Tensor]:
+    if act != "none" and save_pre:
+        return _linear(x, w, bias, residual, act=act, offsets=offsets, save_pre=True)
+    return _linear(x, w, bias, residual, act=act, offsets=offsets), x.new_empty((0,), dtype=torch.float16)
+
+
+@linear.register_fake
+def _(x, w, bias=None, residual=None, offsets=None, act="none", save_pre=True):
+    shape = (x.shape[0], w.shape[-2])
+    return x.new_empty(shape), x.new_empty(shape if act != "none" and save_pre else (0,), dtype=torch.float16)
+
+
+@torch.library.custom_op(f"{_LIB}::linear_backward", mutates_args=())
+def linear_backward(dy: Tensor, x: Tensor, w: Tensor, pre: Optional[Tensor], offsets: Optional[Tensor], act: str,
+                    bias: bool) -> Tuple[Tensor, Tensor, Tensor]:
+    return _linear_bwd(dy, x, w, pre=pre, act=act, offsets=offsets, bias=bias)
+
+
+@linear_backward.register_fake
+def _(dy, x, w, pre, offsets, act, bias):
+    return x.new_empty(x.shape), w.new_empty(w.shape), w.new_empty(w.shape[:-1] if bias else (0,))
+
+
+def _linear_setup(ctx, inputs, output):
+    x, w, bias, residual, offsets, ctx.act, save_pre = inputs
+    ctx.has_bias, ctx.has_residual = bias is not None, residual is not None
+    ctx.no_pre = ctx.act != "none" and not save_pre
+    ctx.save_for_backward(x, w, None if ctx.act == "none" else output[1], offsets)
+
+
+def _linear_grad(ctx, dy, _):
+    if ctx.no_pre:
+        raise RuntimeError("linear was called with save_pre=False: its activation has no gradient")
+    x, w, pre, offsets = ctx.saved_tensors
+    dy = dy.contiguous()
+    dx, dw, db = linear_backward(dy, x, w, pre, offsets, ctx.act, ctx.has_bias)
+    return dx, dw, db if ctx.has_bias else None, dy if ctx.has_residual else None, None, None, None
+
+
+linear.register_autograd(_linear_grad, setup_context=_linear_setup)
+
+
+# ---- expert routing, differentiable -----------------------------------------------------
+
+@torch.library.custom_op(f"{_LIB}::moe_sort", mutates_args=())
+def moe_sort(ids: Tensor, experts: int) -> Tuple[Tensor, Tensor]:
+    return _sort(ids, experts)
+
+
+@moe_sort.register_fake
+def _(ids, experts):
+    return ids.new_empty(ids.shape, dtype=torch.int32), ids.new_empty((experts + 1,), dtype=torch.int32)
+
+
+@torch.library.custom_op(f"{_LIB}::moe_permute", mutates_args=())
+def moe_permute(x: Tensor, rows: Tensor, offsets: Tensor) -> Tensor:
+    return _permute(x, rows, offsets)
+
+
+@moe_permute.register_fake
+def _(x, rows, offsets):
+    return x.new_empty((rows.shape[0] * rows.shape[1], x.shape[1]))
+
+
+@torch.library.custom_op(f"{_LIB}::moe_combine", mutates_args=())
+def moe_combine(y: Tensor, rows: Tensor, offsets: Tensor, weights: Optional[Tensor] = None,
+                residual: Optional[Tensor] = None) -> Tensor:
+    return _combine(y, rows, weights, residual)
+
+
+@moe_combine.register_fake
+def _(y, rows, offsets, weights=None, residual=None):
+    return y.new_empty((rows.shape[0], y.shape[1]))
+
+
+@torch.library.custom_op(f"{_LIB}::moe_combine_backward", mutates_args=())
+def moe_combine_backward(dout: Tensor, y: Tensor, rows: Tensor, weights: Tensor,
+                         offsets: Tensor) -> Tuple[Tensor, Tensor]:
+    return _combine_bwd(dout, y, rows, weights, offsets)
+
+
+@moe_combine_backward.register_fake
+def _(dout, y, rows, weights, offsets):
+    return y.new_empty(y.shape), weights.new_empty(weights.shape)
+
+
+def _permute_setup(ctx, inputs, output):
+    _, rows, offsets = inputs
+    ctx.save_for_backward(rows, offsets)
+
+
+def _permute_grad(ctx, dxs):
+    rows, offsets = ctx.saved_tensors
+    return moe_combine(dxs.contiguous(), rows, offsets), None, None
+
+
+def _combine_setup(ctx, inputs, output):
+    y, rows, offsets, weights, residual = inputs
+    ctx.has_residual = residual is not None
+    ctx.save_for_backward(y, rows, offsets, weights)
+
+
+def _combine_grad(ctx, dout):
+    y, rows, offsets, weights = ctx.saved_tensors
+    dout = dout.contiguous()
+    dres = dout if ctx.has_residual else None
+    if weights is None:
+        return moe_permute(dout, rows, offsets), None, None, None, dres
+    dy, dw = moe_combine_backward(dout, y, rows, weights, offsets)
+    return dy, None, None, dw, dres
+
+
+moe_permute.register_autograd(_permute_grad, setup_context=_permute_setup)
+moe_combine.register_autograd(_combine_grad, setup_context=_combine_setup)
