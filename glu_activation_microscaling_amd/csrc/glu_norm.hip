@@ -113,13 +113,13 @@ __device__ __forceinline__ void param_row(float (&f)[V][8], const void* p, int64
 // worked on, and with 8 columns a thread the parameters stay in registers until the group changes
 // (gate w_post as one factor: g z = (g w_post) n); with 16 they are loaded for every row, which
 // keeps two workgroups on a compute unit.
-template <typename X, int V, bool RAGGED, bool MX, int MAXT>
-__global__ __launch_bounds__(MAXT) void k_block_norm(NormArgs a, uint32_t rows) {
+template <typename X, int V, bool RAGGED, bool MX, bool LAYER>
+__global__ __launch_bounds__(1024) void k_block_norm(NormArgs a, uint32_t rows) {
   __shared__ BlockParts<1> part;
   int turn = 0;
   clear_parts(part);
   const int H = (int)a.H;
-  const bool pf32 = a.flags & NORM_F32_PARAMS, layer = a.kind == NORM_LAYER, post = a.flags & NORM_POST;
+  const bool pf32 = a.flags & NORM_F32_PARAMS, post = a.flags & NORM_POST;
   const bool pre = a.flags & NORM_PRE, has_y = a.y != nullptr;
   const float invH = 1.0f / (float)H;
   uint32_t col[V];
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(MAXT) void k_block_norm(NormArgs a, uint32_t rows) 
   float mean = 0.0f;
   auto normalize = [&](float (&f)[V][8]) {
     mean = 0.0f;
-    if (layer) {
+    if constexpr (LAYER) {
       float s[1] = {0.0f};
 #pragma unroll
       for (int v = 0; v < V; v++)
@@ -272,15 +272,17 @@ enum { P_GATE, P_WPRE, P_BPRE, P_WPOST, P_COUNT };
 //   AHEAD: the next row is loaded while a row is worked on.
 //   ACC_BYTES: LDS for the column sums, where registers are short (16 columns a thread); 0 keeps
 //     them in registers.
-template <typename X, int V, bool RAGGED, int SUMS, bool AHEAD, int ACC_BYTES, int MAXT>
+template <typename X, int V, bool RAGGED, bool LAYER, int SUMS, bool AHEAD, int ACC_BYTES, int MAXT>
 __global__ __launch_bounds__(MAXT) void k_block_norm_bwd(NormBwdArgs a, NormBwdPlan plan) {
   constexpr bool LDS = ACC_BYTES > 0;
-  __shared__ BlockParts<2> part;
+  // rms: one sum over the row at a time; layer: two (with the mean of the gradient)
+  constexpr int ROW_SUMS = LAYER ? 2 : 1;
+  __shared__ BlockParts<ROW_SUMS> part;
   __shared__ v4f in_lds[LDS ? ACC_BYTES / 16 : 1];
   int turn = 0;
   clear_parts(part);
   const int H = (int)a.H;
-  const bool pf32 = a.flags & NORM_F32_PARAMS, layer = a.kind == NORM_LAYER;
+  const bool pf32 = a.flags & NORM_F32_PARAMS;
   const bool post = a.flags & NORM_POST, pre = a.flags & NORM_PRE, has_y = a.y != nullptr;
   const bool sums_y = a.gate.d != nullptr || a.w_post.d != nullptr;
   const float invH = 1.0f / (float)H;
@@ -319,6 +321,17 @@ __global__ __launch_bounds__(MAXT) void k_block_norm_bwd(NormBwdArgs a, NormBwdP
     } else {
 #pragma unroll
       for (int i = 0; i < 8; i++) acc[which][v][i] += f[i];
+    }
+  };
+  auto add_products = [&](int which, int v, const float (&f)[8], const float (&h)[8]) {
+    if constexpr (LDS) {
+      float t[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) t[i] = f[i] * h[i];
+      add(which, v, t);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i++) acc[which][v][i] = __builtin_fmaf(f[i], h[i], acc[which][v][i]);
     }
   };
   auto take = [&](int which, int v, float (&f)[8]) {
@@ -388,38 +401,47 @@ __global__ __launch_bounds__(MAXT) void k_block_norm_bwd(NormBwdArgs a, NormBwdP
         if (pre) lh[v].get(dh[v]);
       }
       if (AHEAD && row + 1 < r1) start(row + 1);
+      // Lanes past the row hold zeros throughout in the rms form; in the layer form the mean they
+      // lose makes them nonzero, so they are cleared where a sum over the row would see them.
       if (has_y) {
 #pragma unroll
         for (int v = 0; v < V; v++)
 #pragma unroll
           for (int i = 0; i < 8; i++) {
-            if (post) ny[v][i] = inside<RAGGED>(i, n[v]) ? (ny[v][i] - my) * ry : 0.0f;
+            if (post) {
+              if constexpr (LAYER) ny[v][i] = inside<RAGGED>(i, n[v]) ? (ny[v][i] - my) * ry : 0.0f;
+              else ny[v][i] *= ry;
+            }
             nx[v][i] = __builtin_fmaf(gw[v][i], ny[v][i], a.res_scale * nx[v][i]);
           }
       }
       if (pre) {
-        float s[2] = {0.0f, 0.0f};
+        float s[ROW_SUMS] = {};
 #pragma unroll
         for (int v = 0; v < V; v++) {
-          float t[8];
           if constexpr (SUMS > 2) add(2, v, dh[v]);
 #pragma unroll
           for (int i = 0; i < 8; i++) {
-            nx[v][i] = inside<RAGGED>(i, n[v]) ? (nx[v][i] - mx) * rx : 0.0f;
-            t[i] = dh[v][i] * nx[v][i];
+            if constexpr (LAYER) nx[v][i] = inside<RAGGED>(i, n[v]) ? (nx[v][i] - mx) * rx : 0.0f;
+            else nx[v][i] *= rx;
+          }
+          add_products(1, v, dh[v], nx[v]);
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
             dh[v][i] *= wq[v][i];
             s[0] = __builtin_fmaf(dh[v][i], nx[v][i], s[0]);
-            s[1] += dh[v][i];
+            if constexpr (LAYER) s[1] += dh[v][i];
           }
-          add(1, v, t);
         }
         block_sum(s, part, turn);
-        const float c0 = s[0] * invH, c1 = layer ? s[1] * invH : 0.0f;
+        const float c0 = s[0] * invH, c1 = LAYER ? s[ROW_SUMS - 1] * invH : 0.0f;
 #pragma unroll
         for (int v = 0; v < V; v++)
 #pragma unroll
-          for (int i = 0; i < 8; i++)
-            D[v][i] = __builtin_fmaf(rx, dh[v][i] - __builtin_fmaf(nx[v][i], c0, c1), D[v][i]);
+          for (int i = 0; i < 8; i++) {
+            const float d = LAYER ? dh[v][i] - c1 : dh[v][i];
+            D[v][i] = __builtin_fmaf(rx, __builtin_fmaf(-c0, nx[v][i], d), D[v][i]);
+          }
       }
 #pragma unroll
       for (int v = 0; v < V; v++) {
@@ -429,30 +451,31 @@ __global__ __launch_bounds__(MAXT) void k_block_norm_bwd(NormBwdArgs a, NormBwdP
         put<RAGGED>((X*)a.dx + (int64_t)row * a.ld_dx, col[v], d, n[v]);
       }
       if (has_y) {
-        float s[2] = {0.0f, 0.0f};
+        float s[ROW_SUMS] = {};
 #pragma unroll
         for (int v = 0; v < V; v++) {
-          float t[8];
+          if (sums_y) add_products(0, v, D[v], ny[v]);
 #pragma unroll
           for (int i = 0; i < 8; i++) {
-            t[i] = D[v][i] * ny[v][i];
-            D[v][i] = inside<RAGGED>(i, n[v]) ? D[v][i] * gw[v][i] : 0.0f;
+            D[v][i] *= gw[v][i];
+            if constexpr (LAYER) {
+              if (!inside<RAGGED>(i, n[v])) D[v][i] = 0.0f;
+              s[1] += D[v][i];
+            }
             s[0] = __builtin_fmaf(D[v][i], ny[v][i], s[0]);
-            s[1] += D[v][i];
           }
-          if (sums_y) add(0, v, t);
         }
         float c0 = 0.0f, c1 = 0.0f;
         if (post) {
           block_sum(s, part, turn);
           c0 = s[0] * invH;
-          c1 = layer ? s[1] * invH : 0.0f;
+          c1 = LAYER ? s[ROW_SUMS - 1] * invH : 0.0f;
         }
 #pragma unroll
         for (int v = 0; v < V; v++) {
           float d[8];
 #pragma unroll
-          for (int i = 0; i < 8; i++) d[i] = ry * (D[v][i] - __builtin_fmaf(ny[v][i], c0, c1));
+          for (int i = 0; i < 8; i++) d[i] = ry * __builtin_fmaf(-c0, ny[v][i], LAYER ? D[v][i] - c1 : D[v][i]);
           put<RAGGED>(a.dy + (int64_t)row * a.ld_dy, col[v], d, n[v]);
         }
       }
@@ -586,8 +609,11 @@ hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((a.M + rows - 1) / rows));
   const bool rag = ragged(a.H, {a.ld_x, a.y ? a.ld_y : 0, a.y ? a.ld_xo : 0, a.h ? a.ld_h : 0});
   auto go = [&](auto X, auto V, auto R, auto Q) {
-    return launch_kernel(k_block_norm<decltype(X), decltype(V)::value, decltype(R)::value, decltype(Q)::value, 1024>,
-                         grid, dim3(threads), s, a, rows);
+    return a.kind == NORM_LAYER
+               ? launch_kernel(k_block_norm<decltype(X), decltype(V)::value, decltype(R)::value, decltype(Q)::value, true>,
+                               grid, dim3(threads), s, a, rows)
+               : launch_kernel(k_block_norm<decltype(X), decltype(V)::value, decltype(R)::value, decltype(Q)::value, false>,
+                               grid, dim3(threads), s, a, rows);
   };
   auto with_v = [&](auto X, auto R, auto Q) {
     return vecs == 1 ? go(X, std::integral_constant<int, 1>{}, R, Q) : go(X, std::integral_constant<int, 2>{}, R, Q);
@@ -612,9 +638,13 @@ hipError_t launch_block_norm_bwd(const NormBwdArgs& a, int64_t groups, hipStream
                                 a.y ? a.ld_dy : 0});
   const int sums = !plan.split && a.gate.stride != 0 && a.w_post.d ? 4 : a.b_pre.d ? 3 : 2;
   auto go = [&](auto X, auto V, auto R, auto S, auto AHEAD, auto BYTES, auto T) {
-    return launch_kernel(k_block_norm_bwd<decltype(X), decltype(V)::value, decltype(R)::value, decltype(S)::value,
-                                          decltype(AHEAD)::value, decltype(BYTES)::value, decltype(T)::value>,
-                         dim3((unsigned)plan.blocks), dim3(plan.threads), s, a, plan);
+    auto of = [&](auto L) {
+      return launch_kernel(k_block_norm_bwd<decltype(X), decltype(V)::value, decltype(R)::value, decltype(L)::value,
+                                            decltype(S)::value, decltype(AHEAD)::value, decltype(BYTES)::value,
+                                            decltype(T)::value>,
+                           dim3(plan.blocks), dim3(plan.threads), s, a, plan);
+    };
+    return a.kind == NORM_LAYER ? of(std::true_type{}) : of(std::false_type{});
   };
 #define GLU_I(n) std::integral_constant<int, n>{}
   auto with_v = [&](auto X, auto R) {
