@@ -784,20 +784,28 @@ __global__ __launch_bounds__(256) void k_linear_grad(GradArgs a) {
   r0 = r0 + n * blockIdx.z / gridDim.z;
   float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   if (col < a.N) {
-    for (int64_t row = r0 + lr; row < r1; row += 8) {
-      Raw<uint16_t> q;
-      load<false>(q, a.dy + row * a.ld_dy, (uint32_t)col, 8);
-      float d[8];
-      q.get(d);
-      if constexpr (ACT != LIN_NONE) {
-        load<false>(q, a.pre + row * a.N, (uint32_t)col, 8);
+    constexpr int U = ACT == LIN_NONE ? 4 : 2;   // rows in flight
+    for (int64_t row = r0 + lr; row < r1; row += 8 * U) {
+      Raw<uint16_t> y[U], p[U];
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-          d[i] *= act_grad<ACT>((float)__builtin_bit_cast(_Float16, (uint16_t)(q.a[i / 2] >> (16 * (i & 1)))));
+      for (int u = 0; u < U; u++) {
+        const int n = row + 8 * u < r1 ? 8 : 0;
+        load<false>(y[u], a.dy + (row + 8 * u) * a.ld_dy, (uint32_t)col, n);
+        if constexpr (ACT != LIN_NONE) load<false>(p[u], a.pre + (row + 8 * u) * a.N, (uint32_t)col, n);
       }
-      if (a.dp != nullptr) store<false>(a.dp + row * a.N, (uint32_t)col, d, 8);
 #pragma unroll
-      for (int i = 0; i < 8; i++) s[i] += d[i];
+      for (int u = 0; u < U; u++) {
+        float d[8];
+        y[u].get(d);
+        if constexpr (ACT != LIN_NONE) {
+#pragma unroll
+          for (int i = 0; i < 8; i++)
+            d[i] *= act_grad<ACT>((float)__builtin_bit_cast(_Float16, (uint16_t)(p[u].a[i / 2] >> (16 * (i & 1)))));
+        }
+        if (a.dp != nullptr && row + 8 * u < r1) store<false>(a.dp + (row + 8 * u) * a.N, (uint32_t)col, d, 8);
+#pragma unroll
+        for (int i = 0; i < 8; i++) s[i] += d[i];
+      }
     }
   }
   if (a.sums == nullptr) return;
