@@ -321,12 +321,12 @@ __device__ __forceinline__ void finish(const ProductArgs& a, int64_t group, int6
 
 // WI x WJ waves of TI x TJ tiles of 16 x 16 each: a tile of 16 WI TI rows by 16 WJ TJ columns.
 //
-// Two LDS stages, each a step of BK elements.  A step's matrix work runs in two halves of 32
+// NS LDS stages, each a step of BK elements.  A step's matrix work runs in two halves of 32
 // elements.  While the first half multiplies, the second half's fragments are read; then one
 // barrier says both that every wave has read the stage and that the next stage has landed;
-// the loads of the step after next go into the stage just freed and the next stage's first
-// fragments are read while the second half multiplies.  A load so has a whole step to arrive.
-template <int MODE, int ACT, int WI, int WJ, int TI, int TJ>
+// the loads of the step NS further on go into the stage just freed and the next stage's first
+// fragments are read while the second half multiplies.  A load so has NS - 1 steps to arrive.
+template <int MODE, int ACT, int WI, int WJ, int TI, int TJ, int NS>
 __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_t tiles_i, uint32_t tiles_j,
                                                           uint32_t splits) {
   constexpr bool TA = MODE == WGRAD, TB = MODE != FWD;
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
   using OpB = Operand<TB, BJ, WAVES>;
   // both stages of A, then both of B: every fragment read's place is within the 16-bit offset
   // of a read instruction from the lane's base
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * (OpA::BYTES + OpB::BYTES)];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[NS * (OpA::BYTES + OpB::BYTES)];
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -468,7 +468,89 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
     wait_lds();   // long since arrived; said here so that the loop's head waits for no more
   };
 
-  if (k0 < k1) {
+  // More stages: a ring, whose present stage starts at byte `now`.  Every step starts the loads of
+  // one step, real or not, so that the count of loads under way is known.
+  constexpr uint32_t STAGE = OpA::BYTES + OpB::BYTES;
+  uint32_t now = 0;
+  auto issue_at = [&](uint32_t k, uint32_t at, auto TAIL) {
+#pragma unroll
+    for (int q = 0; q < OpA::LOADS; q++) oa.template issue<decltype(TAIL)::value>(q, k, k1, smem + at, wave, lane);
+#pragma unroll
+    for (int q = 0; q < OpB::LOADS; q++)
+      ob.template issue<decltype(TAIL)::value>(q, k, k1, smem + at + OpA::BYTES, wave, lane);
+  };
+  auto read_at = [&](uint32_t at, int h) {
+#pragma unroll
+    for (int i = 0; i < TI; i++) xa[h][i] = fa.read(smem + at, i, h);
+#pragma unroll
+    for (int j = 0; j < TJ; j++) xb[h][j] = fb.read(smem + at + OpA::BYTES, j, h);
+  };
+  auto ring_step = [&](auto&& feed) {
+    const uint32_t next = now == (NS - 1) * STAGE ? 0u : now + STAGE;
+    read_at(now, 1);
+    multiply(0);
+#pragma unroll
+    for (int q = 0; q < READS; q++) {
+      __builtin_amdgcn_sched_group_barrier(G_DS_READ, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(G_MFMA, PRODUCTS / READS, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vm<(NS - 2) * LOADS>();
+    lds_barrier();
+    feed(now);
+    read_at(next, 0);
+    multiply(1);
+#pragma unroll
+    for (int q = 0; q < LOADS; q++) {
+      __builtin_amdgcn_sched_group_barrier(G_VMEM, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(G_MFMA, 1, 0);
+    }
+#pragma unroll
+    for (int q = 0; q < READS; q++) {
+      __builtin_amdgcn_sched_group_barrier(G_DS_READ, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(G_MFMA, (PRODUCTS - LOADS) / READS > 1 ? (PRODUCTS - LOADS) / READS : 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    wait_lds();
+    now = next;
+  };
+
+  if constexpr (NS > 2) {
+    if (k0 < k1) {
+      // The steps are taken in turn from step `turn` on, those before it last.  Workgroups that all
+      // read the same columns of many rows meet in few memory channels when the rows are a power of
+      // two apart; each XCD and group starts elsewhere (within an XCD the workgroups stay together,
+      // for what they share in its L2).  32 groups of [8, 2048] x [2048, 2048]: 65 -> 50 us.  A
+      // partial step is the last one, unless every step may be partial (ANY).
+      constexpr bool ANY = BI <= 32;
+      const uint32_t steps = (k1 - k0 + BK - 1) / BK, whole = (k1 - k0) / BK;
+      const uint32_t turn = ANY || whole == steps ? (3u * (blockIdx.x % 8u) + (uint32_t)group) % steps : 0u;
+      uint32_t k = k0 + turn * BK, left = steps;
+      auto advance = [&] { k = k + BK < k1 ? k + BK : k0; };
+      auto feed = [&](uint32_t at) {
+        issue_at(left > 0 ? k : k1, at, std::true_type{});
+        left -= left > 0;
+        advance();
+      };
+      auto feed_whole = [&](uint32_t at) {
+        issue_at(k, at, std::false_type{});
+        advance();
+      };
+#pragma unroll
+      for (uint32_t q = 0; q < NS; q++) feed(q * STAGE);
+      wait_vm<(NS - 1) * LOADS>();
+      lds_barrier();
+      read_at(0, 0);
+      wait_lds();
+      uint32_t s = 0;
+      if (!ANY || whole == steps)
+        for (; s + NS < whole; s++) ring_step(feed_whole);
+      left = left > 0 ? steps - s - NS : 0;
+      for (; s < steps; s++) ring_step(feed);
+      wait_vm<0>();   // the stages hold the sums next
+      lds_barrier();
+    }
+  } else if (k0 < k1) {
     start(k0, 0);
     wait_vm<0>();
     lds_barrier();
@@ -563,134 +645,110 @@ __global__ __launch_bounds__(256) void k_product_join(ProductArgs a, uint32_t sp
 
 // ---- few rows --------------------------------------------------------------------------------
 
-// The forward for a few rows (up to 64 of one group): a pass over W at memory speed.  A wave takes
-// 16 rows of W (columns of C) and multiplies them, straight from memory, as 16 x 16 x 32 tiles
-// against 16, 32, 48 or 64 rows of x; KW waves share the sum, taking chunks of 128 elements in
-// turn, and join through LDS, so a call is one launch whatever its extents.  The next chunks of
-// W are in flight while the present ones are multiplied.
-//   HALF, for up to 8 rows in all: a wave takes 8 rows of W, and a tile's other 8 rows (and
-//   columns, of x) are the same ones 32 elements on: the products of matching halves add up to
-//   the result, the others are dropped.  Twice the workgroups, and 128 bytes of a row a load.
-constexpr int FEW_WAVES = 8, FEW_ROWS = 64, FEW_CHUNK = 128;
+// The forward for up to 8 rows of one group: a pass over W at memory speed, with no barrier in it.
+// A wave takes 8 rows of W (columns of C) and multiplies them, straight from memory, as 16 x 16 x 32
+// tiles against the rows of x; a tile's other 8 rows (and columns, of x) are the same ones 32
+// elements on: the products of matching halves add up to the result, the others are dropped, and a
+// load takes 128 bytes of a row.  KW waves share the sum, taking chunks of 128 elements in turn, and
+// join through LDS, so a call is one launch whatever its extents.  The next chunks of W are in
+// flight while the present ones are multiplied.
+constexpr int FEW_WAVES = 8, FEW_ROWS = 8, FEW_COLS = 8, FEW_CHUNK = 128;
 
-template <int RT, bool HALF>
-__device__ __forceinline__ void few_rows_sum(const ProductArgs& a, const RowTile& t, int64_t n0, uint32_t first,
-                                             uint32_t stride, uint32_t k1, uint32_t lane, v4f (&acc)[4]) {
-  constexpr int U = HALF ? 4 : RT == 1 ? 2 : 1;   // chunks per stage
-  constexpr int STEPS = HALF ? 2 : 4;             // tiles per chunk
-  const uint32_t g = lane >> 4, r = HALF ? lane & 7u : lane & 15u;
-  const uint32_t mine = 8u * g + (HALF ? 32u * (lane >> 3 & 1u) : 0u);   // the lane's elements in a tile
-  const uint32_t wo = n0 + r < a.J ? 2u * (r * (uint32_t)a.ld_b + mine) : kOob;
-  uint32_t xo[RT];
-#pragma unroll
-  for (int i = 0; i < RT; i++)
-    xo[i] = t.i0 + 16 * i + r < t.i1 ? 2u * ((16u * i + r) * (uint32_t)a.ld_a + mine) : kOob;
-  const auto rw = rsrc(uniform(a.b + t.group * a.b_group + n0 * a.ld_b)), rx = rsrc(uniform(a.a + t.i0 * a.ld_a));
-  v8bf w[2][U][STEPS];
-  auto load_w = [&](uint32_t k, int s) {
-#pragma unroll
-    for (int c = 0; c < U; c++)
-#pragma unroll
-      for (int u = 0; u < STEPS; u++) {
-        const uint32_t kk = k + stride * c + FEW_CHUNK / STEPS * u;
-        w[s][c][u] = __builtin_bit_cast(
-            v8bf, __builtin_amdgcn_raw_buffer_load_b128(rw, kk + mine < k1 ? wo : kOob, (int)(2u * kk), 0));
-      }
-  };
-  // x of this stage before W of the next: loads return in order, and the products wait for x
-  auto step = [&](uint32_t k, int s) {
-    v8bf x[U][STEPS][RT];
-#pragma unroll
-    for (int c = 0; c < U; c++)
-#pragma unroll
-      for (int u = 0; u < STEPS; u++) {
-        const uint32_t kk = k + stride * c + FEW_CHUNK / STEPS * u;
-#pragma unroll
-        for (int i = 0; i < RT; i++)
-          x[c][u][i] = __builtin_bit_cast(
-              v8bf, __builtin_amdgcn_raw_buffer_load_b128(rx, kk + mine < k1 ? xo[i] : kOob, (int)(2u * kk), 0));
-      }
-    __builtin_amdgcn_sched_barrier(0);
-    if (k + stride * U < k1) load_w(k + stride * U, 1 - s);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int c = 0; c < U; c++)
-#pragma unroll
-      for (int u = 0; u < STEPS; u++)
-#pragma unroll
-        for (int i = 0; i < RT; i++)
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[s][c][u], x[c][u][i], acc[i], 0, 0, 0);
-  };
-  if (first >= k1) return;
-  load_w(first, 0);
-  for (uint32_t k = first; k < k1; k += 2 * stride * U) {
-    step(k, 0);
-    if (k + stride * U < k1) step(k + stride * U, 1);
-  }
-}
-
-// grid: (column tiles of 16 FEW_WAVES / KW, or half that; row tiles)
-template <int ACT, int KW, bool HALF>
+// grid: column tiles of FEW_COLS FEW_WAVES / KW
+template <int ACT, int KW>
 __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_few_rows(ProductArgs a) {
-  __shared__ v4f sums[FEW_WAVES][HALF ? 1 : FEW_ROWS / 16][64];
-  constexpr int COLS = HALF ? 8 : 16;
+  __shared__ v4f sums[FEW_WAVES][64];
+  constexpr int U = 4, STEPS = 2;   // chunks per stage; tiles per chunk
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const RowTile t = find_tile(a.offsets, a.groups, a.I, blockIdx.y, FEW_ROWS);
-  if (t.group < 0) return;
-  const int64_t n0 = COLS * ((int64_t)blockIdx.x * (FEW_WAVES / KW) + wave / KW);
-  const int rt = HALF ? 1 : (int)((t.i1 - t.i0 + 15) / 16);
-  v4f acc[4];
+  const int64_t n0 = FEW_COLS * ((int64_t)blockIdx.x * (FEW_WAVES / KW) + wave / KW);
+  const uint32_t k1 = (uint32_t)a.K, first = FEW_CHUNK * (wave % KW), stride = FEW_CHUNK * KW;
+  v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (n0 < a.J && first < k1) {
+    const uint32_t r = lane & 7u, mine = 8u * (lane >> 4) + 32u * (lane >> 3 & 1u);   // the lane's row; its elements
+    const uint32_t wo = n0 + r < a.J ? 2u * (r * (uint32_t)a.ld_b + mine) : kOob;
+    const uint32_t xo = r < a.I ? 2u * (r * (uint32_t)a.ld_a + mine) : kOob;
+    const auto rw = rsrc(uniform(a.b + n0 * a.ld_b)), rx = rsrc(uniform(a.a));
+    v8bf w[2][U][STEPS];
+    auto load_w = [&](uint32_t k, int s) {
 #pragma unroll
-  for (int i = 0; i < 4; i++) acc[i] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  if (t.group < a.groups && n0 < a.J) {
-    const uint32_t first = FEW_CHUNK * (wave % KW), stride = FEW_CHUNK * KW, k1 = (uint32_t)a.K;
-    if constexpr (HALF) {
-      few_rows_sum<1, true>(a, t, n0, first, stride, k1, lane, acc);
-    } else {
-      if (rt == 1) few_rows_sum<1, false>(a, t, n0, first, stride, k1, lane, acc);
-      else if (rt == 2) few_rows_sum<2, false>(a, t, n0, first, stride, k1, lane, acc);
-      else if (rt == 3) few_rows_sum<3, false>(a, t, n0, first, stride, k1, lane, acc);
-      else few_rows_sum<4, false>(a, t, n0, first, stride, k1, lane, acc);
+      for (int c = 0; c < U; c++)
+#pragma unroll
+        for (int u = 0; u < STEPS; u++) {
+          const uint32_t kk = k + stride * c + FEW_CHUNK / STEPS * u;
+          w[s][c][u] = __builtin_bit_cast(
+              v8bf, __builtin_amdgcn_raw_buffer_load_b128(rw, kk + mine < k1 ? wo : kOob, (int)(2u * kk), 0));
+        }
+    };
+    // x of this stage before W of the next: loads return in order, and the products wait for x
+    auto step = [&](uint32_t k, int s) {
+      v8bf x[U][STEPS];
+#pragma unroll
+      for (int c = 0; c < U; c++)
+#pragma unroll
+        for (int u = 0; u < STEPS; u++) {
+          const uint32_t kk = k + stride * c + FEW_CHUNK / STEPS * u;
+          x[c][u] = __builtin_bit_cast(
+              v8bf, __builtin_amdgcn_raw_buffer_load_b128(rx, kk + mine < k1 ? xo : kOob, (int)(2u * kk), 0));
+        }
+      __builtin_amdgcn_sched_barrier(0);
+      if (k + stride * U < k1) load_w(k + stride * U, 1 - s);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int c = 0; c < U; c++)
+#pragma unroll
+        for (int u = 0; u < STEPS; u++)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[s][c][u], x[c][u], acc, 0, 0, 0);
+    };
+    load_w(first, 0);
+    for (uint32_t k = first; k < k1; k += 2 * stride * U) {
+      step(k, 0);
+      if (k + stride * U < k1) step(k + stride * U, 1);
     }
   }
-  if constexpr (KW > 1 || HALF) {
+  sums[wave][lane] = acc;
+  __syncthreads();
+  if (wave % KW != 0 || (lane & 40u) != 0) return;   // results are in rows and columns 0 .. 7 of the tile
+  v4f s = (v4f)0.0f;
 #pragma unroll
-    for (int i = 0; i < (HALF ? 1 : 4); i++)
-      if (i < rt) sums[wave][i][lane] = acc[i];
-    __syncthreads();
-  }
-  if (HALF && (lane & 40u) != 0) return;   // results are in rows and columns 0 .. 7 of the tile
-  // row tile i of a column tile is finished by wave i % KW of those that share it
-#pragma unroll
-  for (int i = 0; i < (HALF ? 1 : 4); i++) {
-    if (i >= rt || wave % KW != i % KW) continue;
-    v4f s = acc[i];
-    if constexpr (KW > 1 || HALF) {
-      s = (v4f)0.0f;
-#pragma unroll
-      for (int w = 0; w < KW; w++) {
-        s += sums[wave / KW * KW + w][i][lane];
-        if constexpr (HALF) s += sums[wave / KW * KW + w][i][lane + 40];   // rows and columns 8 .. 15
-      }
-    }
-    const int64_t row = t.i0 + 16 * i + (lane & 15u), col = n0 + 4 * (lane >> 4);
-    if (row >= t.i1 || col >= a.J) continue;
-    float v[4] = {s[0], s[1], s[2], s[3]};
-    finish<FWD, ACT, 4>(a, t.group, row, col, v);
-  }
+  for (int w = 0; w < KW; w++) s += sums[wave + w][lane] + sums[wave + w][lane + 40];   // and 8 .. 15
+  const int64_t row = lane & 15u, col = n0 + 4 * (lane >> 4);
+  if (row >= a.I || col >= a.J) return;
+  float v[4] = {s[0], s[1], s[2], s[3]};
+  finish<FWD, ACT, 4>(a, 0, row, col, v);
 }
 
 // ---- which kernel ----------------------------------------------------------------------------
 
-enum { TILE_256, TILE_128, FEW };
+// The tiled kernel's sizes: waves and 16 x 16 tiles a wave along the rows and the columns, LDS
+// stages.  The larger the tile, the fewer bytes go into LDS for a product (L1 delivers 64 bytes a
+// cycle: half the products' time at 256 x 256) and the more of the chip idles at the end.
+//   32 x 128, two workgroups a compute unit: a few rows of each of many groups, a pass over W.
+struct TileShape {
+  int wi, wj, ti, tj, stages;
+  constexpr int rows() const { return 16 * wi * ti; }
+  constexpr int cols() const { return 16 * wj * tj; }
+};
+enum { TILE_256, TILE_256_128, TILE_128, TILE_32, FEW };
+constexpr TileShape kShape[4] = {{2, 4, 8, 4, 2}, {4, 2, 4, 4, 3}, {2, 4, 4, 2, 3}, {1, 4, 2, 2, 4}};
 struct ProductPlan {
-  int kind, share;
-  bool half;
+  int kind;
+  int64_t share;             // FEW: waves sharing a sum
   int64_t tiles_i, tiles_j, splits;
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// What a tile takes, in microseconds a step of BK elements and for its start and end, from calls of
+// one round of workgroups (2048 to 8192 rows, sums of 1024 to 8192 elements), and what joining the
+// parts of a split sum takes.  The least total over the first three sizes decides.  Measured for
+// [I, J, K], 256x256 / 256x128 / 128x128:
+//   [ 1000, 1000, 1000]  25.9 / 15.8 / 11.4      [ 4096, 4096, 1024]  32.3 /  37.8 /  41.0
+//   [  968, 2048,16384]   274 / 65.0 / 69.6      [ 4096, 4096, 4096]  99.5 / 110.7 / 131.0
+//   [ 2048, 4096, 4096]  79.5 / 56.8 / 65.0      [16384, 2048, 2048]   106 /   121 /   150
+constexpr int64_t kUnits = 256;
+constexpr double kStepUs[3] = {1.29, 0.85, 0.5}, kTileUs[3] = {15.0, 5.0, 4.0}, kJoinUs = 2.5, kJoinTBps = 8.0;
+constexpr int64_t kLeastPart = 512;   // elements of a split sum's part: 256 costs up to 5 us more, and gains 0.5
 
 // A rule on extents alone, so that the scratch memory of split sums can be sized before the
 // launch.
@@ -698,29 +756,48 @@ ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t grou
   ProductPlan p{};
   p.splits = 1;
   if (I == 0 || J == 0) return p;   // nothing to launch
-  if (mode == FWD && I <= (grouped ? FEW_ROWS / 2 * groups : FEW_ROWS)) {
+  if (mode == FWD && !grouped && I <= FEW_ROWS) {
+    // [I, 2048, 16384], few rows against 128x128 tiles: 14.7 / 20.7 us for one row, 18.4 / 21.3 for 8
     p.kind = FEW;
-    p.tiles_i = ceil_div(I, FEW_ROWS) + (grouped ? groups : 0);
     // waves sharing a sum: as few as give 16 waves a compute unit, with four chunks or more each
-    p.half = !grouped && I <= 8;
-    const int64_t cols = p.half ? 8 : 16;
+    const int64_t cols = ceil_div(J, FEW_COLS);
     p.share = 1;
-    while (p.share < FEW_WAVES && ceil_div(J, cols) * p.tiles_i * p.share < 4096 && K >= 8 * p.share * FEW_CHUNK)
-      p.share *= 2;
-    p.tiles_j = ceil_div(J, cols * FEW_WAVES / p.share);
-  } else {
-    const int64_t extra = grouped && mode != WGRAD ? groups : 0, outer = mode == WGRAD ? groups : 1;
-    auto tiles = [&](int64_t b) { return (ceil_div(I, b) + extra) * ceil_div(J, b) * outer; };
-    p.kind = tiles(256) >= 192 ? TILE_256 : TILE_128;
-    const int64_t b = p.kind == TILE_256 ? 256 : 128;
-    p.tiles_i = ceil_div(I, b) + extra;
-    p.tiles_j = ceil_div(J, b);
-    if (!grouped && p.kind == TILE_128) {
-      const int64_t most = K / 512, want = 512 / tiles(128);
-      p.splits = want < most ? want : most;
+    while (p.share < FEW_WAVES && cols * p.share < 16 * kUnits && K >= 8 * p.share * FEW_CHUNK) p.share *= 2;
+    p.tiles_j = ceil_div(cols * p.share, FEW_WAVES);
+    return p;
+  }
+  if (mode == FWD && grouped && I <= kShape[TILE_32].rows() / 2 * groups) {
+    // 32 groups of W [2048, 2048], 32x128 against 128x128 tiles: 48.7 / 54 us for 8 rows a group on
+    // average, 49.5 / 54 for 16, 58 / 54 for 32 (groups of more than 32 rows read W twice)
+    p.kind = TILE_32;
+    p.tiles_i = ceil_div(I, kShape[TILE_32].rows()) + groups;
+    p.tiles_j = ceil_div(J, kShape[TILE_32].cols());
+    return p;
+  }
+  // groups: each ends inside a tile, half a tile more on average; every group may be one more
+  const int64_t extra = grouped && mode != WGRAD ? groups : 0, outer = mode == WGRAD ? groups : 1;
+  const int64_t steps = ceil_div(mode == WGRAD && grouped ? ceil_div(K, groups) : K, BK);
+  double best = 0.0;
+  for (int kind = TILE_256; kind <= TILE_128; kind++) {
+    const int64_t ti = ceil_div(I, kShape[kind].rows()), tj = ceil_div(J, kShape[kind].cols());
+    const int64_t tiles = (ti + extra / 2) * tj * outer;
+    int64_t splits = 1;
+    if (!grouped && kind != TILE_256) {
+      const int64_t most = K / kLeastPart, want = kUnits / tiles;
+      splits = want < most ? want : most;
+      if (splits < 1) splits = 1;
+    }
+    const double round = kTileUs[kind] + kStepUs[kind] * ceil_div(steps, splits);
+    double us = round * ceil_div(tiles * splits, kUnits);
+    if (splits > 1) us += kJoinUs + 8e-6 / kJoinTBps * splits * I * J;
+    if (best == 0.0 || us < best) {
+      best = us;
+      p.kind = kind;
+      p.tiles_i = ti + extra;
+      p.tiles_j = tj;
+      p.splits = splits;
     }
   }
-  if (p.splits < 1) p.splits = 1;
   return p;
 }
 
@@ -734,10 +811,8 @@ hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
   const ProductPlan p = plan_product(MODE, a.I, a.J, a.K, a.groups, a.offsets != nullptr);
   hipError_t e;
   if (p.kind == FEW) {
-    const dim3 grid((unsigned)p.tiles_j, (unsigned)p.tiles_i), block(64 * FEW_WAVES);
     auto go = [&](auto KW) {
-      return p.half ? launch_kernel(k_few_rows<ACT, decltype(KW)::value, true>, grid, block, s, a)
-                    : launch_kernel(k_few_rows<ACT, decltype(KW)::value, false>, grid, block, s, a);
+      return launch_kernel(k_few_rows<ACT, decltype(KW)::value>, dim3((unsigned)p.tiles_j), dim3(64 * FEW_WAVES), s, a);
     };
     return p.share == 1   ? go(std::integral_constant<int, 1>{})
            : p.share == 2 ? go(std::integral_constant<int, 2>{})
@@ -745,11 +820,15 @@ hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
                           : go(std::integral_constant<int, 8>{});
   } else {
     const unsigned n = (unsigned)(p.tiles_i * p.tiles_j * p.splits * (MODE == WGRAD ? a.groups : 1));
-    e = p.kind == TILE_256
-            ? launch_kernel(k_product<MODE, ACT, 2, 4, 8, 4>, dim3(n), dim3(512), s, a, (uint32_t)p.tiles_i,
-                            (uint32_t)p.tiles_j, (uint32_t)p.splits)
-            : launch_kernel(k_product<MODE, ACT, 2, 2, 4, 4>, dim3(n), dim3(256), s, a, (uint32_t)p.tiles_i,
-                            (uint32_t)p.tiles_j, (uint32_t)p.splits);
+    auto go = [&](auto KIND) {
+      constexpr TileShape t = kShape[decltype(KIND)::value];
+      return launch_kernel(k_product<MODE, ACT, t.wi, t.wj, t.ti, t.tj, t.stages>, dim3(n), dim3(64 * t.wi * t.wj), s,
+                           a, (uint32_t)p.tiles_i, (uint32_t)p.tiles_j, (uint32_t)p.splits);
+    };
+    e = p.kind == TILE_256       ? go(std::integral_constant<int, TILE_256>{})
+        : p.kind == TILE_256_128 ? go(std::integral_constant<int, TILE_256_128>{})
+        : p.kind == TILE_128     ? go(std::integral_constant<int, TILE_128>{})
+                                 : go(std::integral_constant<int, MODE == FWD ? TILE_32 : TILE_128>{});
   }
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t octets = (MODE == WGRAD ? a.groups : 1) * a.I * a.J / 8;

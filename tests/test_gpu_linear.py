@@ -55,7 +55,8 @@ def check_backward(gpu, t, pre, act="none", offsets=None):
 # one row, few rows, each tile size and their edges; sums split, ragged and shorter than a step
 SHAPES = [(1, 8, 8), (1, 24, 16), (2, 16, 72), (16, 40, 128), (17, 136, 1032), (33, 512, 64), (64, 248, 2048),
           (65, 128, 64), (100, 1000, 200), (128, 128, 136), (129, 264, 72), (300, 520, 1096), (511, 72, 4104),
-          (777, 1032, 520), (2500, 2056, 328), (3000, 4096, 64), (4100, 2304, 136)]
+          (777, 1032, 520), (2500, 2056, 328), (3000, 4096, 64), (4100, 2304, 136), (4000, 2056, 520),
+          (4000, 4008, 4040)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -66,7 +67,8 @@ def test_shapes(gpu, M, N, K):
 
 
 @pytest.mark.parametrize("act", ["none", "silu", "gelu", "gelu_erf"])
-@pytest.mark.parametrize("M,N,K", [(1, 64, 264), (20, 520, 2056), (200, 264, 512), (200, 264, 1032), (2300, 2304, 264)])
+@pytest.mark.parametrize("M,N,K", [(1, 64, 264), (20, 520, 2056), (200, 264, 512), (200, 264, 1032), (2300, 2304, 264),
+                                   (4000, 4008, 904)])
 def test_activations(gpu, act, M, N, K):
     t = draw(M, N, K, seed=N)
     pre = check_forward(gpu, t, act, save_pre=act != "none")
@@ -97,6 +99,13 @@ def test_groups(gpu, counts, after, N, K):
         check_backward(gpu, t, pre, act, off)
 
 
+def test_groups_of_many_rows(gpu):
+    counts = [2501, 3000, 0, 2099]
+    t = draw(sum(counts), 2000, 2008, groups=4, seed=4)
+    pre = check_forward(gpu, t, "silu", offsets_of(counts), save_pre=True)
+    check_backward(gpu, t, pre, "silu", offsets_of(counts))
+
+
 def test_offsets_out_of_range_are_clamped(gpu):
     t = draw(50, 64, 72, groups=3)
     off = torch.tensor([-5, 20, 1000, 2000], dtype=torch.int32, device="cuda")
@@ -107,7 +116,7 @@ def test_offsets_out_of_range_are_clamped(gpu):
         assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("M,N,K", [(3, 72, 136), (150, 136, 264), (2100, 2304, 72)])
+@pytest.mark.parametrize("M,N,K", [(3, 72, 136), (150, 136, 264), (2100, 2304, 72), (4000, 4008, 904)])
 def test_strides(gpu, M, N, K):
     t = draw(M, N, K, ld=24)
     check_forward(gpu, t)
