@@ -282,41 +282,52 @@ __device__ __forceinline__ void load_bf16(float (&f)[N], const uint16_t* p) {
   }
 }
 
-// Epilogue of N consecutive columns of one row, in place: v holds the sums, then what is stored.
-template <int MODE, int ACT, int N>
-__device__ __forceinline__ void finish(const ProductArgs& a, int64_t group, int64_t row, int64_t col, float (&v)[N],
-                                       const float (&bias)[N], const float (&res)[N]) {
-  typedef unsigned int vec __attribute__((ext_vector_type(N / 2)));
-  vec o;
-  if constexpr (MODE == FWD) {
-    const bool live = group < a.groups;
+template <int N>
+using bf16_vec = unsigned int __attribute__((ext_vector_type(N / 2)));
+
+// The saved pre-activation is FP16: 11 significant bits of what the backward evaluates act' at,
+// where BF16 has 8; larger values are clamped to its range, where act' is 0 or 1.
+template <int N>
+__device__ __forceinline__ bf16_vec<N> pack_pre(const float (&v)[N]) {
+  bf16_vec<N> o;
 #pragma unroll
-    for (int e = 0; e < N; e++) v[e] += bias[e];
-    if (a.pre != nullptr) {
-#pragma unroll
-      for (int e = 0; e < N / 2; e++) {
-        const uint16_t lo = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_fmed3f(v[2 * e], -65504.0f, 65504.0f));
-        const uint16_t hi =
-            __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_fmed3f(v[2 * e + 1], -65504.0f, 65504.0f));
-        o[e] = live ? lo | (uint32_t)hi << 16 : 0u;
-      }
-      *reinterpret_cast<vec*>(a.pre + row * a.J + col) = o;
-    }
-#pragma unroll
-    for (int e = 0; e < N; e++) v[e] = live ? act_of<ACT>(v[e]) + res[e] : 0.0f;
+  for (int e = 0; e < N / 2; e++) {
+    const uint16_t lo = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_fmed3f(v[2 * e], -65504.0f, 65504.0f));
+    const uint16_t hi =
+        __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_fmed3f(v[2 * e + 1], -65504.0f, 65504.0f));
+    o[e] = lo | (uint32_t)hi << 16;
   }
+  return o;
+}
+template <int N>
+__device__ __forceinline__ bf16_vec<N> pack_row(const float (&v)[N]) {
+  bf16_vec<N> o;
 #pragma unroll
   for (int e = 0; e < N / 2; e++) o[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-  *reinterpret_cast<vec*>(a.c + (MODE == WGRAD ? group * a.c_group : 0) + row * a.ld_c + col) = o;
+  return o;
 }
-// The same with bias and residual loaded here.
+
+// Epilogue of N consecutive columns of one row: v holds the sums.
 template <int MODE, int ACT, int N>
 __device__ __forceinline__ void finish(const ProductArgs& a, int64_t group, int64_t row, int64_t col, float (&v)[N]) {
-  float bias[N], res[N];
-  const bool live = MODE == FWD && group < a.groups;
-  load_bf16(bias, live && a.bias != nullptr ? a.bias + group * a.J + col : nullptr);
-  load_bf16(res, live && a.residual != nullptr ? a.residual + row * a.ld_res + col : nullptr);
-  finish<MODE, ACT, N>(a, group, row, col, v, bias, res);
+  if constexpr (MODE == FWD) {
+    float bias[N], res[N];
+    load_bf16(bias, a.bias != nullptr ? a.bias + group * a.J + col : nullptr);
+    load_bf16(res, a.residual != nullptr ? a.residual + row * a.ld_res + col : nullptr);
+#pragma unroll
+    for (int e = 0; e < N; e++) v[e] += bias[e];
+    if (a.pre != nullptr) *reinterpret_cast<bf16_vec<N>*>(a.pre + row * a.J + col) = pack_pre(v);
+#pragma unroll
+    for (int e = 0; e < N; e++) v[e] = act_of<ACT>(v[e]) + res[e];
+  }
+  *reinterpret_cast<bf16_vec<N>*>(a.c + (MODE == WGRAD ? group * a.c_group : 0) + row * a.ld_c + col) = pack_row(v);
+}
+
+// Stores 16 bytes at an offset of a buffer.  The offset is the lanes' alone: with a scalar offset
+// besides, the compiler takes the store to have read its registers when it is issued and may write
+// them in the next instruction, and lanes 12 to 15 of 16 then stored what was written.
+__device__ __forceinline__ void put16(u32x4 v, __amdgpu_buffer_rsrc_t to, uint32_t offset) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, to, offset, 0, 0);
 }
 
 // WI x WJ waves of TI x TJ tiles of 16 x 16 each: a tile of 16 WI TI rows by 16 WJ TJ columns.
@@ -568,17 +579,21 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
     }
   }
 
-  // acc[i][j][e] is C at row r of its row tile and column 4 g + e of its column tile
+  // acc[i][j][e] is C at row r of its row tile and column 4 g + e of its column tile.  Rows and
+  // columns past the tile's are given an offset that the buffer's bounds drop.
   const uint32_t g = lane >> 4, r = lane & 15u;
+  const uint32_t rows = (uint32_t)(t.i1 - t.i0), cols = (uint32_t)(j1 - j0);
   if (splits > 1) {
+    const int64_t at = (MODE == WGRAD ? part * a.groups + group : (int64_t)part) * a.I + t.i0;
+    const auto rw = rsrc(uniform((const uint16_t*)(a.work + at * a.J + j0)));
 #pragma unroll
     for (int i = 0; i < TI; i++) {
-      const int64_t row = t.i0 + 16u * FrA::tile(wi, i) + r;
-      const int64_t at = MODE == WGRAD ? (part * a.groups + group) * a.I + row : part * a.I + row;
+      const uint32_t first = 16u * FrA::tile(wi, i);
 #pragma unroll
       for (int j = 0; j < TJ; j++) {
-        const int64_t col = j0 + 16u * FrB::tile(wj, j) + 4u * g;
-        if (row < t.i1 && col < j1) *reinterpret_cast<v4f*>(a.work + at * a.J + col) = acc[i][j];
+        const uint32_t col = 16u * FrB::tile(wj, j) + 4u * g;
+        const uint32_t o = first + r < rows && col < cols ? 4u * ((first + r) * (uint32_t)a.J + col) : kOob;
+        put16(__builtin_bit_cast(u32x4, acc[i][j]), rw, o);
       }
     }
     return;
@@ -586,42 +601,68 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
   // A row tile's 16 x (16 TJ) sums go through the wave's own piece of LDS, so that a lane gets 8
   // consecutive columns of a row: 16-byte loads and stores.  (No wave reads the stages any
   // more: the last step's barrier comes after its last read.)
-  constexpr uint32_t PITCH = 16 * TJ + 4, CH = 2 * TJ, ROWS = 64 / CH;   // floats; lanes a row; rows a pass
+  constexpr uint32_t PITCH = 16 * TJ + 4, CH = 2 * TJ, ROWS = 64 / CH, PASSES = 16 / ROWS;   // floats; lanes a row
   static_assert(WAVES * 16 * PITCH * 4 <= sizeof(smem));
   float* const mine = reinterpret_cast<float*>(smem) + wave * (16 * PITCH);
   const uint32_t cc = 8u * (lane % CH), lrow = lane / CH;
-  const int64_t col = j0 + 16u * FrB::tile(wj, cc / 16) + cc % 16u;
-  const bool live = MODE == FWD && group < a.groups, in = col < j1;
-  float bias[8];
-  load_bf16(bias, live && in && a.bias != nullptr ? a.bias + group * a.J + col : nullptr);
-  u32x4 res[TI][16 / ROWS];
-  if constexpr (MODE == FWD) {
+  const uint32_t col = 16u * FrB::tile(wj, cc / 16) + cc % 16u;
+  const uint32_t left = col < cols ? rows - min(rows, lrow) : 0u;   // of the lane's rows lrow + 16 tile + ROWS p
+  // the place of pass p of row tile i in a matrix whose rows are ld apart
+  auto place = [&](uint32_t ld, int i, uint32_t p) {
+    const uint32_t first = 16u * FrA::tile(wi, i) + ROWS * p;
+    return first < left ? 2u * (lrow * ld + col) + 2u * first * ld : kOob;
+  };
+  const uint32_t ld_c = (uint32_t)a.ld_c, J = (uint32_t)a.J;
+  const auto rc = rsrc(uniform(a.c + (MODE == WGRAD ? group * a.c_group : 0) + t.i0 * a.ld_c + j0));
+  const bool has_pre = MODE == FWD && a.pre != nullptr;
+  const auto rp = rsrc(uniform(has_pre ? a.pre + t.i0 * a.J + j0 : a.c));
+  if (MODE == FWD && group == a.groups) {   // rows of no group are zero
 #pragma unroll
     for (int i = 0; i < TI; i++)
 #pragma unroll
-      for (uint32_t p = 0; p < 16 / ROWS; p++) {
-        const int64_t row = t.i0 + 16u * FrA::tile(wi, i) + ROWS * p + lrow;
-        res[i][p] = (u32x4)0u;
-        if (live && a.residual != nullptr && in && row < t.i1)
-          res[i][p] = *reinterpret_cast<const u32x4*>(a.residual + row * a.ld_res + col);
+      for (uint32_t p = 0; p < PASSES; p++) {
+        put16((u32x4)0u, rc, place(ld_c, i, p));
+        if (has_pre) put16((u32x4)0u, rp, place(J, i, p));
       }
+    return;
+  }
+  float bias[8];
+  u32x4 res[TI][PASSES];
+  if constexpr (MODE == FWD) {
+    load_bf16(bias, col < cols && a.bias != nullptr ? a.bias + group * a.J + j0 + col : nullptr);
+    if (a.residual != nullptr) {
+      const uint32_t ld = (uint32_t)a.ld_res;
+      const auto rr = rsrc(uniform(a.residual + t.i0 * a.ld_res + j0));
+#pragma unroll
+      for (int i = 0; i < TI; i++)
+#pragma unroll
+        for (uint32_t p = 0; p < PASSES; p++)
+          res[i][p] = __builtin_amdgcn_raw_buffer_load_b128(rr, place(ld, i, p), 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < TI; i++)
+#pragma unroll
+        for (uint32_t p = 0; p < PASSES; p++) res[i][p] = (u32x4)0u;
+    }
   }
 #pragma unroll
   for (int i = 0; i < TI; i++) {
 #pragma unroll
     for (int j = 0; j < TJ; j++) *reinterpret_cast<v4f*>(mine + r * PITCH + 16 * j + 4 * g) = acc[i][j];
 #pragma unroll
-    for (uint32_t p = 0; p < 16 / ROWS; p++) {
-      const int64_t row = t.i0 + 16u * FrA::tile(wi, i) + ROWS * p + lrow;
+    for (uint32_t p = 0; p < PASSES; p++) {
       const float* q = mine + (ROWS * p + lrow) * PITCH + cc;
       const v4f lo = *reinterpret_cast<const v4f*>(q), hi = *reinterpret_cast<const v4f*>(q + 4);
-      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}, rs[8];
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      if constexpr (MODE == FWD) {
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        rs[2 * e] = MODE == FWD ? bf_lo(res[i][p][e]) : 0.0f;
-        rs[2 * e + 1] = MODE == FWD ? bf_hi(res[i][p][e]) : 0.0f;
+        for (int e = 0; e < 8; e++) v[e] += bias[e];
+        if (has_pre) put16(pack_pre(v), rp, place(J, i, p));
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+          v[e] = act_of<ACT>(v[e]) + (e % 2 == 0 ? bf_lo(res[i][p][e / 2]) : bf_hi(res[i][p][e / 2]));
       }
-      if (in && row < t.i1) finish<MODE, ACT, 8>(a, group, row, col, v, bias, rs);
+      put16(pack_row(v), rc, place(ld_c, i, p));
     }
   }
 }
@@ -899,12 +940,20 @@ __global__ __launch_bounds__(256) void k_linear_grad(GradArgs a) {
   }
 }
 
+// 64 columns a workgroup, every fourth part a wave.
 __global__ __launch_bounds__(256) void k_linear_join(const float* sums, int64_t parts, int64_t n, uint16_t* out) {
-  const int64_t i = 256 * (int64_t)blockIdx.x + threadIdx.x;
-  if (i >= n) return;
+  __shared__ float part[4][64];
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  const int64_t i = 64 * (int64_t)blockIdx.x + lane;
   float s = 0.0f;
-  for (int64_t p = 0; p < parts; p++) s += sums[p * n + i];
-  out[i] = (uint16_t)pack_bf16(s, 0.0f);
+  if (i < n) {
+#pragma unroll 4
+    for (int64_t p = wave; p < parts; p += 4) s += sums[p * n + i];
+  }
+  part[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && i < n)
+    out[i] = (uint16_t)pack_bf16((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]), 0.0f);
 }
 
 // Parts each group's rows are cut into for the column sums: enough workgroups to fill the chip,
@@ -968,7 +1017,7 @@ hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t s) {
       return launch_kernel(k_linear_grad<decltype(A)::value>, grid, dim3(256), s, g);
     });
     if (st == hipSuccess && sums != nullptr)
-      st = launch_kernel(k_linear_join, dim3((unsigned)((a.groups * a.N + 255) / 256)), dim3(256), s, sums, parts,
+      st = launch_kernel(k_linear_join, dim3((unsigned)((a.groups * a.N + 63) / 64)), dim3(256), s, sums, parts,
                          a.groups * a.N, a.db);
     if (out != nullptr) {
       dp = out;
