@@ -134,6 +134,15 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
+// Sum over 16 lanes, in each of them: rotations by 8, 4, 2 and 1 lanes.
+__device__ __forceinline__ float row_sum(float v) {
+  v += __uint_as_float(dpp<0x128>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<0x124>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<0x122>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<0x121>(__float_as_uint(v)));
+  return v;
+}
+
 // Sums of N values over the workgroup (up to 16 waves), in every thread.  The two halves of `part`
 // are used in turn, so one barrier a call suffices: a half is written again only after the
 // barrier of the call in between.  Call clear_parts once before the first sum.
@@ -156,15 +165,10 @@ __device__ __forceinline__ void block_sum(float (&v)[N], BlockParts<N>& part, in
     for (int k = 0; k < N; k++) part.v[turn][threadIdx.x >> 6][k] = v[k];
   }
   __syncthreads();
-  // absent waves hold zero; four waves' sums at a time, to hold few registers
+  // absent waves hold zero; 16 lanes read a wave's sum each and add up in a ring, so every lane
+  // ends with all of it after one read
 #pragma unroll
-  for (int k = 0; k < N; k++) v[k] = 0.0f;
-#pragma unroll 1
-  for (int w = 0; w < 16; w += 4)
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-      for (int k = 0; k < N; k++) v[k] += part.v[turn][w + i][k];
+  for (int k = 0; k < N; k++) v[k] = row_sum(part.v[turn][threadIdx.x & 15u][k]);
   turn ^= 1;
 }
 
