@@ -357,9 +357,14 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
     if (blockIdx.x >= tiles_i * tiles_j) return;
   }
   const uint32_t per = tiles_i * tiles_j;
-  uint32_t b = xcd_run(blockIdx.x, MODE != WGRAD && a.offsets != nullptr ? per : gridDim.x);
-  const uint32_t outer = b / per;          // WGRAD: group; with splits: part of the sum
-  b -= outer * per;
+  // WGRAD of groups: their sums differ in length, so each XCD gets a share of every group's tiles
+  const bool each = MODE == WGRAD && a.offsets != nullptr;
+  uint32_t b = blockIdx.x, outer = each ? b / per : 0u;   // WGRAD: group; with splits: part of the sum
+  b = xcd_run(b - outer * per, each ? per : MODE != WGRAD && a.offsets != nullptr ? per : gridDim.x);
+  if (!each) {
+    outer = b / per;
+    b -= outer * per;
+  }
   const uint32_t in_group = GROUP_I * tiles_j, first_i = b / in_group * GROUP_I;
   const uint32_t gi = min(tiles_i - first_i, GROUP_I);
   const uint32_t ti = first_i + b % in_group % gi, tj = b % in_group / gi;
