@@ -11,7 +11,13 @@
 // With w = 1 the sum is also the gradient of the copy.  The copy and the gradients go by token,
 // so a token's row is read from memory once however many experts take it; every row of xs or dy
 // is written by one workgroup alone and sums run in the order of j: no atomics, and the same
-// bits every time.  All but the sort are bound by memory.
+// bits every time.
+//
+// All but the sort are bound by memory.  Measured on an MI355X (a copy of 1 GiB: 5.1 TB/s) for 8192
+// tokens, 8 of 64 experts, 7168 columns:
+//   sort 5.0 + 6.2 us, copy 186 us (5.7 TB/s, nearly all of it writes), sum 223 to 246 us (4.3 to
+//   4.7 TB/s, nearly all of it reads), gradients 394 us (5.1 TB/s)
+// and for 4 tokens of 2048 columns 4 us each, which is what a launch takes.
 #include "ffn_device.h"
 #include "ffn_launch.h"
 
@@ -27,7 +33,8 @@ __device__ __forceinline__ int expert_at(const void* ids, int64_t i, int bytes, 
 
 __device__ __forceinline__ int64_t sort_begin(int64_t n, int64_t parts, int64_t i) { return n * i / parts; }
 
-// Counts of each expert in each workgroup's part.
+// Counts of each expert in each workgroup's part, by integer additions in LDS (whose order does
+// not matter).
 __global__ __launch_bounds__(SORT_THREADS) void k_moe_count(MoeSortArgs a) {
   __shared__ int count[kMaxExperts];
   for (int e = threadIdx.x; e < a.experts; e += SORT_THREADS) count[e] = 0;
@@ -45,7 +52,7 @@ __global__ __launch_bounds__(SORT_THREADS) void k_moe_count(MoeSortArgs a) {
 // contiguous part of that, so a choice's place is the start of its expert, plus the choices
 // of that expert in earlier workgroups (from k_moe_count), in earlier waves, and in earlier
 // lanes of its own wave (a ballot for each bit of the expert's number finds the lanes that
-// share it).
+// share it).  Bound by latency: two passes over a part's numbers.
 __global__ __launch_bounds__(SORT_THREADS) void k_moe_place(MoeSortArgs a) {
   __shared__ int next[SORT_WAVES][kMaxExperts];   // counts, then the next place, per wave
   __shared__ int wave_total[SORT_WAVES], sum_all[kMaxExperts], sum_early[kMaxExperts];
@@ -153,7 +160,8 @@ __device__ __forceinline__ void zero_tail(uint8_t* out, int64_t ld, int64_t row_
   }
 }
 
-// grid: (parts of a row of 4 KiB, tokens)
+// The copy: 16 bytes a lane, read once and written to each of the token's places.  By bytes, so
+// one kernel serves every type, FP8 rows included.  grid: (parts of a row of 4 KiB, tokens)
 constexpr int64_t MOVE_PART = 16 * MOVE_THREADS;
 __global__ __launch_bounds__(MOVE_THREADS) void k_moe_permute(MoePermuteArgs a) {
   const int64_t c0 = MOVE_PART * blockIdx.x, c1 = min(c0 + MOVE_PART, a.row_bytes);
@@ -180,7 +188,8 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_moe_permute(MoePermuteArgs a) 
   }
 }
 
-// grid: (parts of 2048 columns, tokens)
+// The weighted sum: FP32 sums of up to eight rows in flight at a time, in the order of j, rounded
+// once.  grid: (parts of 2048 columns, tokens)
 constexpr int64_t SUM_PART = 8 * MOVE_THREADS;
 constexpr int SUM_CHOICES = 8;
 template <bool RAGGED>
@@ -223,7 +232,8 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_moe_combine(MoeCombineArgs a) 
   }
 }
 
-// One workgroup a token; eight choices at a time.
+// The gradients: one workgroup a token, so that a token's eight dot products are whole in it and its
+// row of dout is read once; eight choices at a time.
 constexpr int GRAD_CHOICES = 8;
 template <bool RAGGED>
 __global__ __launch_bounds__(MOVE_THREADS) void k_moe_combine_bwd(MoeCombineBwdArgs a) {
@@ -276,8 +286,9 @@ __global__ __launch_bounds__(MOVE_THREADS) void k_moe_combine_bwd(MoeCombineBwdA
 
 }  // namespace
 
-// Workgroups of the sort: one up to 4096 choices (one launch), else parts of 1024 choices or more,
-// at most 64 (each reads the others' counts).
+// Workgroups of the sort: one up to 4096 choices, in one launch, else parts of 1024 choices or more,
+// at most 64 (each reads the others' counts).  One part against several, back to back in a graph:
+// 2048 choices 4.8 / 6.6 us, 4096 6.5 / 6.7, 8192 10.1 / 6.8, 65536 59 / 7.9.
 int64_t moe_sort_blocks(int64_t n) {
   if (n <= 4 * SORT_THREADS) return 1;
   const int64_t b = (n + SORT_THREADS - 1) / SORT_THREADS;
