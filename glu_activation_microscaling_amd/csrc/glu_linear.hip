@@ -346,7 +346,7 @@ __device__ __forceinline__ void put16(u32x4 v, __amdgpu_buffer_rsrc_t to, uint32
 //   256x128  [968, 2048, 16384] in four parts 60 us (1.09 PFLOP/s), and 7 to join them
 //   128x128  [1021, 1000, 2056] in four parts 14.6 us, and 5.9 to join them
 //   32x128   32 groups, 256 rows, [2048, 2048], W from memory: 49 us (5.5 TB/s)
-// Tried and slower at [16384, 7168, 2048] (forward, with epilogue; 512 us then): 128x128 tiles 637;
+// Tried and slower at [16384, 7168, 2048] (forward with epilogue, 500 to 540 us as is): 128x128 tiles 637;
 // 4 waves of 128x128 798; four stages of 32 elements 558; two workgroups of 256x128 and three
 // stages of 32 a compute unit 581; workgroups that stay and load the next tile during the
 // epilogue 560.
