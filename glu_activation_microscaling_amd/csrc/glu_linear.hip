@@ -899,8 +899,8 @@ hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
 // ---- dp = dy act'(p) and its column sums -----------------------------------------------------
 // Bound by memory.  grid: (256 columns, group, part of the group's rows).  A thread holds 8 columns
 // of every eighth row; the eight row sums are joined through LDS, and the parts by k_linear_join in
-// a fixed order.  [16384, 7168] with GELU 166 us (4.2 TB/s; the exponentials cost about as long
-// as the bytes), [16384, 4096] in 16 groups without an activation 37 us (3.6 TB/s).
+// a fixed order.  [16384, 7168] with GELU 166 us (4.2 TB/s), [16384, 4096] in 16 groups without an
+// activation 37 us (3.6 TB/s).
 struct GradArgs {
   int64_t M, N, groups;
   const int32_t* offsets;

@@ -85,7 +85,7 @@ GROUPS = [([40, 50, 60], 0), ([0, 130, 0, 0, 257, 1, 0], 0), ([0, 0, 300], 0), (
 
 
 @pytest.mark.parametrize("counts,after", GROUPS, ids=[str(i) for i in range(len(GROUPS))])
-@pytest.mark.parametrize("N,K", [(136, 200), (264, 64)])
+@pytest.mark.parametrize("N,K", [(136, 200), (264, 64), (384, 1024), (72, 1032)])
 def test_groups(gpu, counts, after, N, K):
     M = sum(counts) + after
     t = draw(M, N, K, groups=len(counts), seed=M)
@@ -97,6 +97,15 @@ def test_groups(gpu, counts, after, N, K):
     for act in ("none", "silu"):
         pre = check_forward(gpu, t, act, off, save_pre=act != "none")
         check_backward(gpu, t, pre, act, off)
+
+
+@pytest.mark.parametrize("M", [1, 7, 8, 9, 16, 31, 130])
+@pytest.mark.parametrize("N,K", [(8, 4096), (520, 2048), (2056, 136), (4104, 1032)])
+def test_few_rows(gpu, M, N, K):
+    t = draw(M, N, K, seed=M, ld=8)
+    pre = check_forward(gpu, t, "gelu", save_pre=True)
+    check_backward(gpu, t, pre, "gelu")
+    check_forward(gpu, t, "none", bias=False)
 
 
 def test_groups_of_many_rows(gpu):
