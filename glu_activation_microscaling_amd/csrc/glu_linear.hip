@@ -581,9 +581,10 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
     }
   } else if (k0 < k1) {
     start(k0, 0);
-    wait_vm<0>();
-    lds_barrier();
     start(k0 + BK, 1);
+    if (k0 + 2 * BK <= k1) wait_vm<LOADS>();   // of the second step's
+    else wait_vm<0>();
+    lds_barrier();
     read(0, 0);
     wait_lds();
     uint32_t k = k0;
