@@ -78,9 +78,20 @@ struct ProductArgs {
   float* work;               // split sums: [parts, rows of C, J]
 };
 
-// Finds the group and the rows of row tile t when each group's rows are cut into tiles of
-// `size`, group after group; the rows after the last group count as group `groups`.  group is
-// -1 past the last tile.  64 groups are looked at together, one a lane.
+// Row segments of grouped products: 0 holds the rows before the first group, e + 1 those of group e,
+// groups + 1 those after the last group.  The first and the last are of no group and count as group
+// number `groups`.
+struct Rows {
+  int64_t begin, end;
+};
+__device__ __forceinline__ Rows segment(const int32_t* off, int64_t groups, int64_t I, int64_t s) {
+  const int64_t a = s == 0 ? 0 : min((int64_t)max(off[s - 1], 0), I);
+  return {a, s > groups ? I : max(a, min((int64_t)off[s], I))};
+}
+
+// Finds the group and the rows of row tile t when each segment's rows are cut into tiles of
+// `size`, segment after segment.  group is -1 past the last tile.  64 segments are looked at
+// together, one a lane.
 struct RowTile {
   int64_t group, i0, i1;
 };
@@ -92,15 +103,11 @@ __device__ __forceinline__ int64_t lane_value(int64_t v, int at) {
 __device__ __forceinline__ RowTile find_tile(const int32_t* off, int64_t groups, int64_t I, int64_t t, int64_t size) {
   if (off == nullptr) return {t * size < I ? 0 : -1, t * size, min((t + 1) * size, I)};
   const int lane = threadIdx.x & 63;
-  int64_t first = 0;   // tiles of the groups before this batch
-  for (int64_t e0 = 0; e0 <= groups; e0 += 64) {
-    const int64_t e = e0 + lane;
-    int64_t a = 0, b = 0;
-    if (e <= groups) {
-      a = e == 0 ? 0 : min((int64_t)max(off[e], 0), I);
-      b = e == groups ? I : max(a, min((int64_t)off[e + 1], I));
-    }
-    int64_t n = (b - a + size - 1) / size;
+  int64_t first = 0;   // tiles of the segments before this batch
+  for (int64_t s0 = 0; s0 < groups + 2; s0 += 64) {
+    Rows r = {0, 0};
+    if (s0 + lane < groups + 2) r = segment(off, groups, I, s0 + lane);
+    int64_t n = (r.end - r.begin + size - 1) / size;
     const int64_t own = n;
     for (int d = 1; d < 64; d <<= 1) {
       const int64_t v = __shfl_up(n, d);
@@ -109,22 +116,21 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* off, int64_t groups,
     const uint64_t hit = __ballot(t < first + n && t >= first + n - own);
     if (hit != 0) {
       const int at = __builtin_ctzll(hit);
-      const int64_t i0 = a + (t - (first + n - own)) * size;
-      return {e0 + at, lane_value(i0, at), lane_value(min(i0 + size, b), at)};
+      const int64_t i0 = r.begin + (t - (first + n - own)) * size, s = s0 + at;
+      return {s == 0 ? groups : s - 1, lane_value(i0, at), lane_value(min(i0 + size, r.end), at)};
     }
     first += lane_value(n, 63);
   }
   return {-1, 0, 0};
 }
 
-// Row tiles of all groups, the rows after the last one included.
+// Row tiles of all segments.
 __device__ __forceinline__ uint32_t count_tiles(const int32_t* off, int64_t groups, int64_t I, int64_t size) {
   const int lane = threadIdx.x & 63;
   int n = 0;
-  for (int64_t e = lane; e <= groups; e += 64) {
-    const int64_t a = e == 0 ? 0 : min((int64_t)max(off[e], 0), I);
-    const int64_t b = e == groups ? I : max(a, min((int64_t)off[e + 1], I));
-    n += (int)((b - a + size - 1) / size);
+  for (int64_t s = lane; s < groups + 2; s += 64) {
+    const Rows r = segment(off, groups, I, s);
+    n += (int)((r.end - r.begin + size - 1) / size);
   }
   for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
   return __builtin_amdgcn_readfirstlane(n);
@@ -831,17 +837,19 @@ ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t grou
     // 32 groups of W [2048, 2048], 32x128 against 128x128 tiles: 48.7 / 54 us for 8 rows a group on
     // average, 49.5 / 54 for 16, 58 / 54 for 32 (groups of more than 32 rows read W twice)
     p.kind = TILE_32;
-    p.tiles_i = ceil_div(I, kShape[TILE_32].rows()) + groups;
+    p.tiles_i = ceil_div(I, kShape[TILE_32].rows()) + groups + 1;
     p.tiles_j = ceil_div(J, kShape[TILE_32].cols());
     return p;
   }
-  // groups: each ends inside a tile, half a tile more on average; every group may be one more
-  const int64_t extra = grouped && mode != WGRAD ? groups : 0, outer = mode == WGRAD ? groups : 1;
+  // groups: each ends inside a tile, half a tile more on average; at most one tile more for each of
+  // the groups + 2 segments but one
+  const bool cut = grouped && mode != WGRAD;
+  const int64_t extra = cut ? groups + 1 : 0, outer = mode == WGRAD ? groups : 1;
   const int64_t steps = ceil_div(mode == WGRAD && grouped ? ceil_div(K, groups) : K, BK);
   double best = 0.0;
   for (int kind = TILE_256; kind <= TILE_128; kind++) {
     const int64_t ti = ceil_div(I, kShape[kind].rows()), tj = ceil_div(J, kShape[kind].cols());
-    const int64_t tiles = (ti + extra / 2) * tj * outer;
+    const int64_t tiles = (ti + (cut ? groups / 2 : 0)) * tj * outer;
     int64_t splits = 1;
     if (!grouped && kind != TILE_256) {
       const int64_t most = K / kLeastPart, want = kUnits / tiles;

@@ -1,0 +1,49 @@
+"""Linear products on the GPU where rows, values or extents are out of the ordinary, against the 64-bit
+references and bounds of ffn_reference.py."""
+import pytest
+import torch
+
+from test_gpu_linear import check_backward, check_forward, draw
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+# rows before the first group, rows of each group, rows after the last: a segment of each kind that
+# ends inside a tile, groups up to and past the 64 segments looked at together, no group with rows,
+# few rows a group and many
+LEADING = [(30, [40, 50], 0), (1, [300], 40), (129, [0, 70, 0, 257], 5), (7, [1] * 61, 0), (0, [1] * 62, 9),
+           (5, [1] * 62, 9), (5, [1] * 63, 0), (33, [2, 0, 1] * 43, 7), (200, [0, 0, 0], 0), (700, [3000, 1, 2500], 300)]
+
+
+@pytest.mark.parametrize("before,counts,after", LEADING, ids=[str(i) for i in range(len(LEADING))])
+@pytest.mark.parametrize("N,K", [(136, 200), (384, 1024), (2056, 520)])
+def test_rows_before_the_first_group(gpu, before, counts, after, N, K):
+    """offsets[0] > 0 (a slice of a longer list of offsets): the rows before it are of no group.  Whatever
+    they hold, their rows of y, pre and dx are zero and no gradient of w or b sees them."""
+    M = before + sum(counts) + after
+    t = draw(M, N, K, groups=len(counts), seed=M)
+    off = torch.tensor([before] + counts, device="cuda").cumsum(0).to(torch.int32)
+    for rows in (slice(0, before), slice(M - after, M)):
+        t["x"][rows], t["dy"][rows], t["residual"][rows] = float("nan"), float("inf"), float("nan")
+    for act in ("none", "silu"):
+        pre = check_forward(gpu, t, act, off, save_pre=act != "none")
+        check_backward(gpu, t, pre, act, off)
+
+
+def test_a_slice_of_the_experts(gpu):
+    """The products of experts 2 .. 4 alone, from a slice of all the offsets."""
+    counts = [70, 31, 0, 150, 64, 90]
+    t = draw(sum(counts), 264, 200, groups=6)
+    off = torch.tensor([0] + counts, device="cuda").cumsum(0).to(torch.int32)
+    part = dict(t, w=t["w"][2:5], bias=t["bias"][2:5])
+    pre = check_forward(gpu, part, "gelu", off[2:6], save_pre=True)
+    check_backward(gpu, part, pre, "gelu", off[2:6])
+    assert (pre[:101] == 0).all() and (pre[315:] == 0).all()
+
+
+def test_every_row_before_the_first_group(gpu):
+    t = draw(90, 64, 72, groups=2)
+    off = torch.tensor([400, 500, 600], dtype=torch.int32, device="cuda")
+    assert (gpu.glu_linear(t["x"], t["w"], t["bias"], t["residual"], offsets=off) == 0).all()
+    for g in gpu.glu_linear_bwd(t["dy"], t["x"], t["w"], offsets=off, bias=True):
+        assert (g == 0).all()
