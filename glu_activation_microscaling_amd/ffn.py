@@ -248,7 +248,8 @@ def _linear_setup(x, w, offsets, act):
 
 def glu_linear(x, w, bias=None, residual=None, *, act="none", offsets=None, save_pre=False, out=None):
     """y = act(x W^T + bias) + residual, [M, N].  w is [N, K], or [groups, N, K] with int32
-    offsets [groups + 1]: rows offsets[e] .. offsets[e + 1] - 1 of x go through w[e], bias[e].
+    offsets [groups + 1]: rows offsets[e] .. offsets[e + 1] - 1 of x go through w[e], bias[e], and rows
+    of no group give zeros, without bias or residual.
     save_pre=True returns (y, pre), pre the FP16 pre-activation that glu_linear_bwd takes."""
     M, N, K, groups, ld_x = _linear_setup(x, w, offsets, act)
     if bias is not None:
@@ -270,7 +271,7 @@ def glu_linear(x, w, bias=None, residual=None, *, act="none", offsets=None, save
 def glu_linear_bwd(dy, x, w, *, pre=None, act="none", offsets=None, bias=False, need_dx=True, need_dw=True):
     """Gradients of glu_linear: (dx [M, K], dw like w, db [N] or [groups, N]).  pre is the
     forward's (act other than "none"); bias=True asks for db.  What is not wanted comes back
-    zero-sized.  The residual's gradient is dy."""
+    zero-sized.  The residual's gradient is dy, with offsets zero in rows of no group."""
     M, N, K, groups, ld_x = _linear_setup(x, w, offsets, act)
     ld_dy = _matrix(dy, "dy", _BF16, M, N)
     a = LINEAR_ACT[act]

@@ -354,13 +354,22 @@ def _linear_setup(ctx, inputs, output):
     ctx.save_for_backward(x, w, None if ctx.act == "none" else output[1], offsets)
 
 
+def _rows_of_groups(dy, offsets):
+    """The residual's gradient: dy, but zero in rows of no group, where y is zero without it."""
+    if offsets is None:
+        return dy
+    row = torch.arange(dy.shape[0], device=dy.device)
+    return dy.masked_fill(((row < offsets[0]) | (row >= offsets[-1])).unsqueeze(1), 0.0)
+
+
 def _linear_grad(ctx, dy, _):
     if ctx.no_pre:
         raise RuntimeError("linear was called with save_pre=False: its activation has no gradient")
     x, w, pre, offsets = ctx.saved_tensors
     dy = dy.contiguous()
     dx, dw, db = linear_backward(dy, x, w, pre, offsets, ctx.act, ctx.has_bias)
-    return dx, dw, db if ctx.has_bias else None, dy if ctx.has_residual else None, None, None, None
+    dres = _rows_of_groups(dy, offsets) if ctx.has_residual else None
+    return dx, dw, db if ctx.has_bias else None, dres, None, None, None
 
 
 linear.register_autograd(_linear_grad, setup_context=_linear_setup)

@@ -420,8 +420,8 @@ glu_status glu_linear(int act, int64_t M, int64_t N, int64_t K, int64_t groups, 
 
 /* dp = dy act'(p);  dx = dp W,  dw[e] = dp^T x and db[e] = sum of dp over the rows of group e.
  * pre is the forward's (NULL when act is GLU_LINEAR_NONE).  dx [M, K], dw [groups, N, K],
- * db [groups, N], BF16, each NULL when not wanted.  The residual's gradient is dy itself.
- * Rows outside every group give zero rows of dx. */
+ * db [groups, N], BF16, each NULL when not wanted.  Rows outside every group give zero rows of dx.
+ * The residual's gradient is dy itself, in rows outside every group zero. */
 int64_t glu_linear_bwd_work_bytes(int act, int64_t M, int64_t N, int64_t K, int64_t groups, int grouped,
                                   int with_bias);
 glu_status glu_linear_bwd(int act, int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
