@@ -292,16 +292,18 @@ template <int N>
 using bf16_vec = unsigned int __attribute__((ext_vector_type(N / 2)));
 
 // The saved pre-activation is FP16: 11 significant bits of what the backward evaluates act' at,
-// where BF16 has 8; larger values are clamped to its range, where act' is 0 or 1.
+// where BF16 has 8; larger values are clamped to its range, where act' is 0 or 1.  The clamp keeps
+// NaN (maximum and minimum give NaN where the median of three would give a bound), so that what is
+// NaN in y is NaN in the gradients too.
 template <int N>
 __device__ __forceinline__ bf16_vec<N> pack_pre(const float (&v)[N]) {
+  typedef _Float16 half2 __attribute__((ext_vector_type(2)));
+  const half2 most = {(_Float16)65504.0f, (_Float16)65504.0f};
   bf16_vec<N> o;
 #pragma unroll
   for (int e = 0; e < N / 2; e++) {
-    const uint16_t lo = __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_fmed3f(v[2 * e], -65504.0f, 65504.0f));
-    const uint16_t hi =
-        __builtin_bit_cast(uint16_t, (_Float16)__builtin_amdgcn_fmed3f(v[2 * e + 1], -65504.0f, 65504.0f));
-    o[e] = lo | (uint32_t)hi << 16;
+    const half2 h = {(_Float16)v[2 * e], (_Float16)v[2 * e + 1]};   // infinite past the range
+    o[e] = __builtin_bit_cast(uint32_t, __builtin_elementwise_minimum(__builtin_elementwise_maximum(h, -most), most));
   }
   return o;
 }

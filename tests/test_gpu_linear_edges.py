@@ -47,3 +47,47 @@ def test_every_row_before_the_first_group(gpu):
     assert (gpu.glu_linear(t["x"], t["w"], t["bias"], t["residual"], offsets=off) == 0).all()
     for g in gpu.glu_linear_bwd(t["dy"], t["x"], t["w"], offsets=off, bias=True):
         assert (g == 0).all()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_erf"])
+@pytest.mark.parametrize("M,N,K", [(3, 136, 200), (150, 136, 200), (900, 520, 1032), (4000, 4008, 904)])
+def test_nan_reaches_the_gradients(gpu, act, M, N, K):
+    """A NaN of the bias makes its column of the pre-activation NaN, so that column of dp, its element of db,
+    its row of dw and all of dx; a NaN in a row of x, that row of dx and all of dw and db.  Nothing
+    else changes.  Few rows, sums split over workgroups and each tile size."""
+    t = draw(M, N, K)
+
+    def run():
+        y, pre = gpu.glu_linear(t["x"], t["w"], t["bias"], act=act, save_pre=True)
+        return (y, pre) + gpu.glu_linear_bwd(t["dy"], t["x"], t["w"], pre=pre, act=act, bias=True)
+
+    def nan(t):
+        return torch.isnan(t.float())
+
+    y, pre, dx, dw, db = run()
+    rest, keep = [i for i in range(N) if i != 5], t["bias"][5].item()
+    t["bias"][5] = float("nan")
+    y2, pre2, dx2, dw2, db2 = run()
+    assert nan(y2[:, 5]).all() and nan(pre2[:, 5]).all() and nan(dx2).all() and nan(dw2[5]).all() and nan(db2[5])
+    assert torch.equal(pre2[:, rest], pre[:, rest]) and torch.equal(dw2[rest], dw[rest]) and torch.equal(db2[rest], db[rest])
+    t["bias"][5] = keep
+    t["x"][1, 7] = float("nan")
+    y2, pre2, dx2, dw2, db2 = run()
+    rest = [i for i in range(M) if i != 1]
+    assert nan(y2[1]).all() and nan(pre2[1]).all() and nan(dx2[1]).all() and nan(dw2).all() and nan(db2).all()
+    assert torch.equal(pre2[rest], pre[rest]) and torch.equal(dx2[rest], dx[rest])
+
+
+def test_the_saved_pre_activation_is_clamped(gpu):
+    """Finite values past FP16's range and infinities are saved as its largest values, rounding at the edge
+    of the range included; subnormals stay."""
+    v = torch.tensor([65504.0, 65510.0, 65530.0, 1e6, 3e38, float("inf"), 1e-7, 6e-8, 1e-30, 0.0], device="cuda")
+    p = torch.cat([v, -v]).to(BF16)
+    bias = torch.zeros(24, device="cuda", dtype=BF16)
+    bias[:20] = p
+    want = bias.double().clamp(-65504, 65504).to(torch.float16)
+    for M in (2, 40):
+        x = torch.zeros(M, 8, device="cuda", dtype=BF16)
+        w = torch.zeros(24, 8, device="cuda", dtype=BF16)
+        _, pre = gpu.glu_linear(x, w, bias, act="gelu", save_pre=True)
+        assert torch.equal(pre, want.expand(M, 24))
