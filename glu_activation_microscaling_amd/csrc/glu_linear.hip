@@ -13,6 +13,7 @@
 // db sums it unrounded.
 #include "ffn_device.h"
 #include "ffn_launch.h"
+#include "ffn_split.h"
 
 namespace glu {
 namespace {
@@ -410,7 +411,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
   }
   if (splits > 1) {                  // whole steps to each part
     const uint32_t steps = (k1 - k0 + BK - 1) / BK;
-    const uint32_t s0 = steps * part / splits, s1 = steps * (part + 1) / splits;
+    const uint32_t s0 = part_begin(steps, part, splits), s1 = part_begin(steps, part + 1, splits);
     k1 = min(k1, k0 + s1 * BK);
     k0 += s0 * BK;
   }

@@ -91,3 +91,22 @@ def test_the_saved_pre_activation_is_clamped(gpu):
         w = torch.zeros(24, 8, device="cuda", dtype=BF16)
         _, pre = gpu.glu_linear(x, w, bias, act="gelu", save_pre=True)
         assert torch.equal(pre, want.expand(M, 24))
+
+
+def test_sum_over_2_to_the_30_rows(gpu):
+    """The gradient of w summed over 2^30 rows in 256 parts (17 GB an operand): rows that count lie at both
+    ends and around the bounds of the last parts, each a power of two, so that the sum is exact and
+    shows which of them are missing or counted twice."""
+    M, part = 1 << 30, 1 << 22
+    at = [0, 1, part - 1, part, 127 * part - 1, 127 * part, 254 * part, 255 * part - 1, 255 * part, 255 * part + 70000,
+          M - 65, M - 1]
+    x = torch.zeros(M, 8, device="cuda", dtype=BF16)
+    dy = torch.zeros(M, 8, device="cuda", dtype=BF16)
+    for i, row in enumerate(at):
+        dy[row, i % 8] = 1.0
+        x[row, i // 8] = 2.0 ** i
+    _, dw, _ = gpu.glu_linear_bwd(dy, x, torch.zeros(8, 8, device="cuda", dtype=BF16), need_dx=False)
+    want = torch.zeros(8, 8, device="cuda", dtype=BF16)
+    for i in range(len(at)):
+        want[i % 8, i // 8] = 2.0 ** i
+    assert torch.equal(dw, want)
