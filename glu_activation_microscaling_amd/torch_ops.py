@@ -267,6 +267,7 @@ def _(xq, xs, wq, ws, amax, act="geglu", sf_layout="rowmajor", fmt="mxfp8", w_la
 
 # ---- block norms, differentiable ------------------------------------------------------
 # Without y, x' is x itself and x_out comes back zero-sized (an op may not return its input).
+# stats is for the backward and has no gradient.
 
 @torch.library.custom_op(f"{_LIB}::block_norm", mutates_args=())
 def block_norm(x: Tensor, y: Optional[Tensor] = None, gate: Optional[Tensor] = None,
@@ -303,6 +304,7 @@ def _(x, y, stats, dx_out, dh, gate, w_pre, b_pre, w_post, post, res_scale, kind
 def _norm_setup(ctx, inputs, output):
     x, y, gate, w_pre, b_pre, w_post, ctx.post, ctx.res_scale, ctx.kind, _ = inputs
     ctx.save_for_backward(x, y, output[2], gate, w_pre, b_pre, w_post)
+    ctx.mark_non_differentiable(output[2])
 
 
 def _norm_grad(ctx, dx_out, dh, _):
@@ -320,7 +322,7 @@ block_norm.register_autograd(_norm_grad, setup_context=_norm_setup)
 
 # ---- linear products, differentiable ----------------------------------------------------
 # pre is the pre-activation the backward needs, zero-sized when act is "none" or save_pre is off
-# (then only y's residual has a gradient with an act).
+# (then only y's residual has a gradient with an act).  It has no gradient of its own.
 
 @torch.library.custom_op(f"{_LIB}::linear", mutates_args=())
 def linear(x: Tensor, w: Tensor, bias: Optional[Tensor] = None, residual: Optional[Tensor] = None,
@@ -352,6 +354,7 @@ def _linear_setup(ctx, inputs, output):
     ctx.has_bias, ctx.has_residual = bias is not None, residual is not None
     ctx.no_pre = ctx.act != "none" and not save_pre
     ctx.save_for_backward(x, w, None if ctx.act == "none" else output[1], offsets)
+    ctx.mark_non_differentiable(output[1])
 
 
 def _rows_of_groups(dy, offsets):

@@ -50,3 +50,14 @@ def test_autograd_routes_to_the_backward_ops():
     names = [str(t.target) for t in gm.graph.nodes if t.op == "call_function"]
     for op in ("block_norm_backward", "linear_backward", "moe_combine_backward", "moe_combine.default"):
         assert any("glu_mx." + op in s for s in names), op
+
+
+def test_side_outputs_have_no_gradient():
+    """stats and pre serve the backward: a loss on them is refused by autograd, not given zeros."""
+    x, w = (b(*s, device="meta").requires_grad_(True) for s in ((8, 64), (24, 64)))
+    y = b(8, 64, device="meta")
+    xo, h, stats = ops.block_norm(x, y)
+    assert xo.requires_grad and h.requires_grad and not stats.requires_grad
+    for act in ("none", "silu"):
+        out, pre = ops.linear(x, w, None, None, None, act)
+        assert out.requires_grad and not pre.requires_grad
