@@ -280,10 +280,9 @@ def glu_linear_bwd(dy, x, w, *, pre=None, act="none", offsets=None, bias=False, 
     if pre is not None:
         _like(pre, "pre", torch.float16, (M, N))
     _same_device(x, w, dy, pre, offsets)
-    none = x.new_empty((0,)) if not (need_dx and need_dw and bias) else None
-    dx = _empty(x, (M, K), _BF16) if need_dx else none
-    dw = torch.empty_like(w) if need_dw else none
-    db = x.new_empty(w.shape[:-1]) if bias else none
+    dx = _empty(x, (M, K), _BF16) if need_dx else x.new_empty((0,))
+    dw = torch.empty_like(w) if need_dw else x.new_empty((0,))
+    db = x.new_empty(w.shape[:-1] if bias else (0,))
     nbytes = _size("glu_linear_bwd_work_bytes", a, M, N, K, groups, int(offsets is not None), int(bias))
     work = x.new_empty((nbytes,), dtype=torch.uint8) if nbytes > 0 else None
     _call("glu_linear_bwd", a, M, N, K, groups, _ptr(offsets), _ptr(dy), ld_dy, _ptr(x), ld_x, _ptr(w), _ptr(pre),

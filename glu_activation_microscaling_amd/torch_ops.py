@@ -22,7 +22,8 @@ that torch.compile keeps whole; these ops do the same for the MI355X kernels:
   torch.ops.glu_mx.block_norm_backward(x, y, stats, dx_out, dh, gate, w_pre, b_pre, w_post, post,
                                        res_scale, kind)  -> (dx, dy, dgate, dw_post, dw_pre, db_pre)
   torch.ops.glu_mx.linear(x, w, bias, residual, offsets, act, save_pre) -> (y, pre)
-  torch.ops.glu_mx.linear_backward(dy, x, w, pre, offsets, act, bias)  -> (dx, dw, db)
+  torch.ops.glu_mx.linear_backward(dy, x, w, pre, offsets, act, bias, need_dx, need_dw)
+                                                                       -> (dx, dw, db)
   torch.ops.glu_mx.moe_sort(ids, experts)                              -> (rows, offsets)
   torch.ops.glu_mx.moe_permute(x, rows, offsets)                       -> xs
   torch.ops.glu_mx.moe_combine(y, rows, offsets, weights, residual)    -> out
@@ -340,18 +341,18 @@ def _(x, w, bias=None, residual=None, offsets=None, act="none", save_pre=True):
 
 @torch.library.custom_op(f"{_LIB}::linear_backward", mutates_args=())
 def linear_backward(dy: Tensor, x: Tensor, w: Tensor, pre: Optional[Tensor], offsets: Optional[Tensor], act: str,
-                    bias: bool) -> Tuple[Tensor, Tensor, Tensor]:
-    return _linear_bwd(dy, x, w, pre=pre, act=act, offsets=offsets, bias=bias)
+                    bias: bool, need_dx: bool = True, need_dw: bool = True) -> Tuple[Tensor, Tensor, Tensor]:
+    return _linear_bwd(dy, x, w, pre=pre, act=act, offsets=offsets, bias=bias, need_dx=need_dx, need_dw=need_dw)
 
 
 @linear_backward.register_fake
-def _(dy, x, w, pre, offsets, act, bias):
-    return x.new_empty(x.shape), w.new_empty(w.shape), w.new_empty(w.shape[:-1] if bias else (0,))
+def _(dy, x, w, pre, offsets, act, bias, need_dx=True, need_dw=True):
+    return (x.new_empty(x.shape if need_dx else (0,)), w.new_empty(w.shape if need_dw else (0,)),
+            w.new_empty(w.shape[:-1] if bias else (0,)))
 
 
 def _linear_setup(ctx, inputs, output):
-    x, w, bias, residual, offsets, ctx.act, save_pre = inputs
-    ctx.has_bias, ctx.has_residual = bias is not None, residual is not None
+    x, w, _, _, offsets, ctx.act, save_pre = inputs
     ctx.no_pre = ctx.act != "none" and not save_pre
     ctx.save_for_backward(x, w, None if ctx.act == "none" else output[1], offsets)
     ctx.mark_non_differentiable(output[1])
@@ -366,13 +367,17 @@ def _rows_of_groups(dy, offsets):
 
 
 def _linear_grad(ctx, dy, _):
-    if ctx.no_pre:
-        raise RuntimeError("linear was called with save_pre=False: its activation has no gradient")
     x, w, pre, offsets = ctx.saved_tensors
+    # arguments left to their defaults at the end of a call have no entry
+    need_dx, need_dw, need_db, need_dres = (tuple(ctx.needs_input_grad) + (False, False))[:4]
     dy = dy.contiguous()
-    dx, dw, db = linear_backward(dy, x, w, pre, offsets, ctx.act, ctx.has_bias)
-    dres = _rows_of_groups(dy, offsets) if ctx.has_residual else None
-    return dx, dw, db if ctx.has_bias else None, dres, None, None, None
+    dx = dw = db = None
+    if need_dx or need_dw or need_db:
+        if ctx.no_pre:
+            raise RuntimeError("linear was called with save_pre=False: its activation has no gradient")
+        dx, dw, db = linear_backward(dy, x, w, pre, offsets, ctx.act, need_db, need_dx, need_dw)
+    return (dx if need_dx else None, dw if need_dw else None, db if need_db else None,
+            _rows_of_groups(dy, offsets) if need_dres else None, None, None, None)
 
 
 linear.register_autograd(_linear_grad, setup_context=_linear_setup)

@@ -61,3 +61,33 @@ def test_side_outputs_have_no_gradient():
     for act in ("none", "silu"):
         out, pre = ops.linear(x, w, None, None, None, act)
         assert out.requires_grad and not pre.requires_grad
+
+
+def test_linear_s_backward_is_asked_for_what_is_wanted():
+    m = dict(device="meta")
+
+    def wanted(*names, act="silu"):
+        """(bias, need_dx, need_dw) of the backward op's call when these operands want gradients; None: no call."""
+        def f(x, w, bias, residual):
+            t = dict(x=x, w=w, bias=bias, residual=residual)
+            t.update({k: t[k].detach().requires_grad_(True) for k in names})
+            y, _ = ops.linear(t["x"], t["w"], t["bias"], t["residual"], None, act)
+            return torch.autograd.grad(y.sum(), [t[k] for k in names])
+
+        gm = make_fx(f)(b(8, 64, **m), b(24, 64, **m), b(24, **m), b(8, 24, **m))
+        calls = [n.args + (True,) * (9 - len(n.args)) for n in gm.graph.nodes if "linear_backward" in str(n.target)]
+        assert len(calls) <= 1
+        return calls[0][6:] if calls else None
+
+    assert wanted("x", "w", "bias") == (True, True, True) and wanted("x", "residual") == (False, True, False)
+    assert wanted("w") == (False, False, True) and wanted("bias") == (True, False, False)
+    assert wanted("residual") is None and wanted("residual", act="none") is None
+
+    # arguments by name and left out
+    x, w, r = (b(*s, **m).requires_grad_(True) for s in ((8, 64), (24, 64), (8, 24)))
+    for y, given in ((ops.linear(x, w), False), (ops.linear(x, w, act="silu"), False), (ops.linear(x, w, None, r), True),
+                     (ops.linear(x, w, residual=r, act="silu"), True)):
+        g = torch.autograd.grad(y[0].sum(), (x, w, r), allow_unused=True)
+        assert [t is not None for t in g] == [True, True, given]
+    y = ops.linear(x.detach(), w=w.detach(), residual=r)[0]
+    assert torch.autograd.grad(y.sum(), r)[0].shape == r.shape

@@ -28,3 +28,30 @@ def test_the_residual_s_gradient_is_zero_in_rows_of_no_group(gpu, act, first, la
     y, _ = ops.linear(x, w, None, res, off, act)
     (got,) = torch.autograd.grad(y, res, dy)
     assert torch.equal(got, torch.where(inside.unsqueeze(1), dy, torch.zeros_like(dy)))
+
+
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_gradients_of_linear_by_ones_and_twos(gpu, act):
+    """A gradient has the same bits whichever others are wanted with it."""
+    args = dict(x=n(50, 64), w=n(72, 64, seed=1), bias=n(72, seed=2), residual=n(50, 72, seed=3))
+    dy = n(50, 72, seed=4)
+
+    def grads(*names):
+        t = {k: v.clone().requires_grad_(k in names) for k, v in args.items()}
+        y, _ = ops.linear(t["x"], t["w"], t["bias"], t["residual"], None, act)
+        return dict(zip(names, torch.autograd.grad(y, [t[k] for k in names], dy)))
+
+    full = grads(*args)
+    for names in (("x",), ("w",), ("bias",), ("residual",), ("x", "bias"), ("w", "residual"), ("x", "w")):
+        for k, g in grads(*names).items():
+            assert torch.equal(g, full[k]), (names, k)
+
+
+def test_the_residual_alone_needs_no_pre_activation(gpu):
+    x, w, res, dy = n(50, 64), n(72, 64, seed=1), n(50, 72, seed=2).requires_grad_(True), n(50, 72, seed=3)
+    y, pre = ops.linear(x, w, None, res, None, "silu", False)
+    assert pre.numel() == 0
+    assert torch.equal(torch.autograd.grad(y, res, dy)[0], dy)
+    y, _ = ops.linear(x, w, n(72, seed=4).requires_grad_(True), res, None, "silu", False)
+    with pytest.raises(RuntimeError):
+        y.sum().backward()
