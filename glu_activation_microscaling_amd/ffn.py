@@ -130,6 +130,8 @@ def _norm_setup(x, y, gate, w_pre, b_pre, w_post, pre, post, kind):
                 raise ValueError("w_post is [H]; gate, w_pre and b_pre are [H] or share one number of groups")
             groups = shape[0]
             flags |= grouped
+    if groups == 0 and M == 0:
+        groups = 1   # a row of parameters for each row, of which there are none
     if groups == 0 or M % groups:
         raise ValueError(f"{M} rows are not a whole number of rows for each of {groups} groups")
     if dtype is _F32:
