@@ -61,9 +61,10 @@ def _ptr(t):
 
 def _matrix(t, name, dtype, rows=None, cols=None):
     """Row stride of a 2-D GPU tensor with unit column stride (of [rows, cols] where given).
-    The stride of a single row means nothing; a whole number of vectors is passed for it."""
+    The stride of a single row means nothing; a whole number of vectors is passed for it.  No stride
+    of a tensor without rows does: the gradient of a sum over one is expanded, and contiguous."""
     shape, stride = t.shape, t.stride()
-    if t.dtype is not dtype or not t.is_cuda or len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
+    if t.dtype is not dtype or not t.is_cuda or len(shape) != 2 or (stride[1] != 1 and shape[1] > 1 and shape[0] > 0):
         _rowmajor(t, name, dtype)   # says what is wrong
     M, N = shape
     if (rows is not None and M != rows) or (cols is not None and N != cols):
@@ -328,14 +329,15 @@ def glu_moe_permute(x, rows, offsets, *, out=None):
     """xs [tokens * choices, H] with xs[rows[t, j]] = x[t] and zero rows past offsets[-1]; x may
     have any dtype (codes and scales of quantized tokens too)."""
     T, k = _routing(rows, offsets)
-    M, H, ld = _rowmajor(x, "x", x.dtype)
+    ld_x = _matrix(x, "x", x.dtype)
+    M, H = x.shape
     if M != T:
         raise ValueError(f"x must have {T} rows, got {M}")
     _same_device(x, rows, offsets, out)
     xs = out if out is not None else x.new_empty((T * k, H))
     ld_xs = _matrix(xs, "out", x.dtype, T * k, H)
     e = x.element_size()
-    _call("glu_moe_permute", T, k, offsets.numel() - 1, H * e, _ptr(x), (ld if M > 1 else H) * e, _ptr(rows),
+    _call("glu_moe_permute", T, k, offsets.numel() - 1, H * e, _ptr(x), ld_x * e, _ptr(rows),
           _ptr(offsets), _ptr(xs), ld_xs * e, _stream(x))
     return xs
 

@@ -55,3 +55,28 @@ def test_the_residual_alone_needs_no_pre_activation(gpu):
     y, _ = ops.linear(x, w, n(72, seed=4).requires_grad_(True), res, None, "silu", False)
     with pytest.raises(RuntimeError):
         y.sum().backward()
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_gradients_of_no_rows(gpu, act):
+    """A batch without tokens: the gradient of a sum over no rows is an expanded tensor.  Parameters get
+    zeros, the rest is empty."""
+    def leaf(*shape, dtype=BF16):
+        return torch.ones(shape, device="cuda", dtype=dtype).requires_grad_(True)
+
+    x, y, w = leaf(0, 64), leaf(0, 64), leaf(64)
+    xo, h, _ = ops.block_norm(x, y, w, w, w, w, True)
+    for t, g in zip((x, y, w), torch.autograd.grad(xo.sum() + h.sum(), (x, y, w))):
+        assert g.shape == t.shape and (g == 0).all()
+    wt, b, res = leaf(3, 72, 64), leaf(3, 72), leaf(0, 72)
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for args in ((x, wt, b, res, off), (x, leaf(72, 64), leaf(72), res, None)):
+        out, _ = ops.linear(*args, act)
+        for t, g in zip(args, torch.autograd.grad(out.sum(), args[:4])):
+            assert g.shape == t.shape and (g == 0).all()
+    rows, offsets = ops.moe_sort(torch.empty((0, 2), dtype=torch.int32, device="cuda"), 3)
+    ys, wts = leaf(0, 64), leaf(0, 2, dtype=torch.float32)
+    for out in (ops.moe_permute(x, rows, offsets), ops.moe_combine(ys, rows, offsets, wts, y),
+                ops.moe_combine(ys, rows, offsets)):
+        for g in torch.autograd.grad(out.sum(), (x, y, ys, wts), allow_unused=True):
+            assert g is None or g.numel() == 0
