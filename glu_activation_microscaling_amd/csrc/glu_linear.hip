@@ -349,13 +349,13 @@ __device__ __forceinline__ void put16(u32x4 v, __amdgpu_buffer_rsrc_t to, uint32
 //
 // Bound by the matrix cores at large sizes; what is lost there is the start and the end of a tile,
 // which nothing overlaps (one workgroup fills a compute unit's LDS).  Measured on an MI355X:
-//   256x256  [16384, 7168, 2048] (I, J, K) alone 380 us (1.27 PFLOP/s), with bias, GELU, residual and
-//            saved pre-activation 500 to 513; gradient of x 380 to 398, of W 409 to 426
-//            16 groups, 16384 rows, [4096, 2048]: 295 to 320, gradients 296 to 331 and 352 to 383
-//   256x128  [968, 2048, 16384] in four parts 60 us (1.09 PFLOP/s), and 7 to join them
-//   128x128  [1021, 1000, 2056] in four parts 14.6 us, and 5.9 to join them
+//   256x256  [16384, 7168, 2048] (I, J, K) alone 364 to 373 us (1.3 PFLOP/s), with bias, GELU, residual
+//            and saved pre-activation 488 to 506; gradient of x 377 to 388, of W 408 to 410
+//            16 groups, 16384 rows, [4096, 2048]: 290 to 323, gradients 296 to 329 and 296 to 326
+//   256x128  [968, 2048, 16384] in four parts 59 us (1.1 PFLOP/s), and 7 to join them
+//   128x128  [1021, 1000, 2056] in four parts 14.9 us, and 5.6 to join them
 //   32x128   32 groups, 256 rows, [2048, 2048], W from memory: 49 us (5.5 TB/s)
-// Tried and slower at [16384, 7168, 2048] (forward with epilogue, 500 to 540 us as is): 128x128 tiles 637;
+// Tried and slower at [16384, 7168, 2048] (forward with epilogue, 500 to 540 us at the time): 128x128 tiles 637;
 // 4 waves of 128x128 798; four stages of 32 elements 558; two workgroups of 256x128 and three
 // stages of 32 a compute unit 581; workgroups that stay and load the next tile during the
 // epilogue 560.
@@ -721,7 +721,7 @@ __global__ __launch_bounds__(256) void k_product_join(ProductArgs a, uint32_t sp
 // elements on: the products of matching halves add up to the result, the others are dropped, and a
 // load takes 128 bytes of a row.  KW waves share the sum, taking chunks of 128 elements in turn, and
 // join through LDS, so a call is one launch whatever its extents.  The next chunks of W are in
-// flight while the present ones are multiplied.  [1, 2048, 16384]: 13.2 to 14.5 us (4.6 to 5.1 TB/s).
+// flight while the present ones are multiplied.  [1, 2048, 16384]: 13.2 to 14.9 us (4.5 to 5.1 TB/s).
 constexpr int FEW_WAVES = 8, FEW_ROWS = 8, FEW_COLS = 8, FEW_CHUNK = 128;
 
 // grid: column tiles of FEW_COLS FEW_WAVES / KW
@@ -813,9 +813,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // one round of workgroups (2048 to 8192 rows, sums of 1024 to 8192 elements), and what joining the
 // parts of a split sum takes.  The least total over the first three sizes decides.  Measured for
 // [I, J, K], 256x256 / 256x128 / 128x128:
-//   [ 1000, 1000, 1000]  25.9 / 15.8 / 11.4      [ 4096, 4096, 1024]  32.3 /  37.8 /  41.0
-//   [  968, 2048,16384]   274 / 65.0 / 69.6      [ 4096, 4096, 4096]  99.5 / 110.7 / 131.0
-//   [ 2048, 4096, 4096]  79.5 / 56.8 / 65.0      [16384, 2048, 2048]   106 /   121 /   150
+//   [ 1000, 1000, 1000]  24.8 / 15.8 / 11.2      [ 4096, 4096, 1024]  33.2 /  41.6 /  45.7
+//   [  968, 2048,16384]   278 / 65.8 / 72.0      [ 4096, 4096, 4096]  99.2 / 113.7 / 136.3
+//   [ 2048, 4096, 4096]  87.6 / 58.2 / 69.1      [16384, 2048, 2048]   107 /   126 /   151
+// (of 33 such shapes the rule takes the fastest of the three on 32 and is 0.5% behind on one).
 constexpr int64_t kUnits = 256;
 constexpr double kStepUs[3] = {1.29, 0.85, 0.5}, kTileUs[3] = {15.0, 5.0, 4.0}, kJoinUs = 2.5, kJoinTBps = 8.0;
 constexpr int64_t kLeastPart = 512;   // elements of a split sum's part: 256 costs up to 5 us more, and gains 0.5

@@ -33,8 +33,8 @@ Each real implementation is the binding function of the same name (argument mars
 the HIP kernels compute everything).  Each fake implementation gives the output shapes and
 dtypes without touching a GPU, so FakeTensor tracing and torch.compile(fullgraph=True)
 capture the ops as single graph nodes.  `glu` is differentiable: its backward is the
-`glu_backward` op (the fused BF16 backward kernel); so are block_norm, linear, moe_permute and
-moe_combine, through the backward ops beside them.  The quantized ops are not
+`glu_backward` op (the fused BF16 backward kernel); so are block_norm, linear, moe_permute (of
+BF16 rows) and moe_combine, through the backward ops beside them.  The quantized ops are not
 differentiable.  In the split layout `up` is the second operand; in the paired layout pass
 an empty `up` (a 0-element tensor), since a custom op cannot take None for a tensor that
 other layouts need.
