@@ -266,6 +266,13 @@ def _(xq, xs, wq, ws, amax, act="geglu", sf_layout="rowmajor", fmt="mxfp8", w_la
             xq.new_empty(_nv_scale_shape(M, N, sf_layout), dtype=torch.uint8))
 
 
+def _incoming(grad):
+    """A gradient as the kernels take it: contiguous, from a 16-byte boundary.  That of one part of a
+    concatenation is a view that starts where the part does."""
+    grad = grad.contiguous()
+    return grad.clone() if grad.storage_offset() * grad.element_size() % 16 else grad
+
+
 # ---- block norms, differentiable ------------------------------------------------------
 # Without y, x' is x itself and x_out comes back zero-sized (an op may not return its input).
 # stats is for the backward and has no gradient.
@@ -311,7 +318,7 @@ def _norm_setup(ctx, inputs, output):
 def _norm_grad(ctx, dx_out, dh, _):
     x, y, stats, gate, w_pre, b_pre, w_post = ctx.saved_tensors
     dx, dy, dgate, dw_post, dw_pre, db_pre = block_norm_backward(
-        x, y, stats, None if y is None else dx_out.contiguous(), dh.contiguous(), gate, w_pre, b_pre, w_post,
+        x, y, stats, None if y is None else _incoming(dx_out), _incoming(dh), gate, w_pre, b_pre, w_post,
         ctx.post, ctx.res_scale, ctx.kind)
     grads = [g if t is not None else None for g, t in ((dy, y), (dgate, gate), (dw_pre, w_pre), (db_pre, b_pre),
                                                       (dw_post, w_post))]
@@ -370,7 +377,7 @@ def _linear_grad(ctx, dy, _):
     x, w, pre, offsets = ctx.saved_tensors
     # arguments left to their defaults at the end of a call have no entry
     need_dx, need_dw, need_db, need_dres = (tuple(ctx.needs_input_grad) + (False, False))[:4]
-    dy = dy.contiguous()
+    dy = _incoming(dy)
     dx = dw = db = None
     if need_dx or need_dw or need_db:
         if ctx.no_pre:
@@ -434,7 +441,7 @@ def _permute_setup(ctx, inputs, output):
 
 def _permute_grad(ctx, dxs):
     rows, offsets = ctx.saved_tensors
-    return moe_combine(dxs.contiguous(), rows, offsets), None, None
+    return moe_combine(_incoming(dxs), rows, offsets), None, None
 
 
 def _combine_setup(ctx, inputs, output):
@@ -445,7 +452,7 @@ def _combine_setup(ctx, inputs, output):
 
 def _combine_grad(ctx, dout):
     y, rows, offsets, weights = ctx.saved_tensors
-    dout = dout.contiguous()
+    dout = _incoming(dout)
     dres = dout if ctx.has_residual else None
     if weights is None:
         return moe_permute(dout, rows, offsets), None, None, None, dres

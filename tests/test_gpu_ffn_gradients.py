@@ -80,3 +80,32 @@ def test_gradients_of_no_rows(gpu, act):
                 ops.moe_combine(ys, rows, offsets)):
         for g in torch.autograd.grad(out.sum(), (x, y, ys, wts), allow_unused=True):
             assert g is None or g.numel() == 0
+
+
+def test_gradients_that_start_off_a_16_byte_boundary(gpu):
+    """The gradient of one part of a concatenation is a view that starts where the part does: at widths that
+    are no multiple of 8, anywhere.  It gives the bits of the same gradient on a boundary."""
+    H = 101
+    x, y, w = (t.requires_grad_(True) for t in (n(6, H), n(6, H, seed=1), n(H, seed=2)))
+    ids = torch.randint(0, 3, (6, 2), device="cuda", dtype=torch.int32)
+    rows, offsets = ops.moe_sort(ids, 3)
+    wts = torch.rand(6, 2, device="cuda").requires_grad_(True)
+    ys = n(12, H, seed=3).requires_grad_(True)
+    for make, leaves in ((lambda: ops.block_norm(x, y, w, w, w, w, True)[0], (x, y, w)),
+                         (lambda: ops.block_norm(x, y, w, w, w, w, True)[1], (x, y, w)),
+                         (lambda: ops.moe_permute(x, rows, offsets), (x,)),
+                         (lambda: ops.moe_combine(ys, rows, offsets, wts, y), (ys, wts, y)),
+                         (lambda: ops.moe_combine(ys, rows, offsets), (ys,))):
+        t = make()
+        d = n(t.shape[0] + 1, H, seed=4)
+        want = torch.autograd.grad(t, leaves, d[1:].clone())
+        t = torch.cat([n(1, H), make()])
+        for a, b in zip(torch.autograd.grad(t, leaves, d), want):
+            assert torch.equal(a, b)
+    wt, res = n(40, 72, seed=5).requires_grad_(True), n(6, 40, seed=6).requires_grad_(True)
+    t = ops.linear(n(6, 72), wt, None, res, None, "silu")[0]
+    d = n(1 + 240, seed=7)
+    want = torch.autograd.grad(t, (wt, res), d[1:].reshape(6, 40).clone())
+    t = torch.cat([n(1), ops.linear(n(6, 72), wt, None, res, None, "silu")[0].flatten()])
+    for a, b in zip(torch.autograd.grad(t, (wt, res), d), want):
+        assert torch.equal(a, b)
