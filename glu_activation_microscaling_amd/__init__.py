@@ -22,8 +22,9 @@ Entry points (C names in include/glu_mx.h):
   (fmt "mxfp8": E4M3 codes, or "mxfp4": packed E2M1 codes; w_layout "split" or "paired")
   glu_quant_mxfp8_f32(x, rowwise=, colwise=)                -> (q_row, q_col, s_row, s_col)
   glu_quant_nvfp4_f32(x, sf_layout=)                        -> (q, sf)
-The operators around the GLU (ffn.py: glu_block_norm*, glu_linear*, glu_moe_*) are names of
-the package too.
+The operators around the GLU (ffn.py: glu_block_norm*, glu_linear*, glu_moe_*) and the gated
+projections and checkpoints (gated.py: glu_gated_linear*, glu_*_ckpt) are names of the package
+too.
 A disabled MXFP8 direction comes back as zero-sized tensors (fixed arity), as in the
 MXFP8 page's API section.  Codes and scales are uint8 tensors; BF16 data is torch.bfloat16.
 """
@@ -94,6 +95,11 @@ _FFN_SIGNATURES = {  # without the stream: the arguments that glu_check_* takes 
     "moe_permute": [_i64, _i64, _int, _i64, _p, _i64, _p, _p, _p, _i64],
     "moe_combine": [_i64, _i64, _i64, _p, _i64, _p, _p, _p, _i64, _p, _i64],
     "moe_combine_bwd": [_i64, _i64, _i64, _int, _p, _i64, _p, _i64, _p, _p, _p, _p, _i64, _p],
+    "gated_linear": [_int, _int, _int, _i64, _i64, _i64, _i64, _p, _p, _i64, _p, _p, _p, _i64, _p, _p, _p, _i64],
+    "gated_linear_bwd": [_int, _int, _int, _i64, _i64, _i64, _i64, _p, _p, _i64, _p, _i64, _p, _p, _p, _p, _i64, _p,
+                         _p, _p, _i64, _p, _i64],
+    "fwd_ckpt": [_int, _int, _i64, _i64, _p, _p, _i64, _p, _i64, _p, _p],
+    "bwd_ckpt": [_int, _int, _i64, _i64, _p, _p, _p, _i64, _p, _i64, _p, _i64],
 }
 for _n, _args in _FFN_SIGNATURES.items():
     _SIGNATURES["glu_" + _n] = _args + [_p]
@@ -103,6 +109,9 @@ _SIZES = {   # functions that give a number of bytes
     "glu_block_norm_bwd_work_bytes": [_i64, _i64, _i64], "glu_linear_work_bytes": [_i64, _i64, _i64, _i64, _int],
     "glu_linear_bwd_work_bytes": [_int, _i64, _i64, _i64, _i64, _int, _int],
     "glu_moe_sort_work_bytes": [_i64, _i64, _int],
+    "glu_gated_linear_work_bytes": [_int, _i64, _i64, _i64, _i64, _int],
+    "glu_gated_linear_bwd_work_bytes": [_i64, _i64, _i64, _i64, _int, _int],
+    "glu_ckpt_scale_bytes": [_i64, _i64],
 }
 
 _lib = None
@@ -480,3 +489,4 @@ def glu_stream_probe(srcs, dsts):
 
 from .ffn import (glu_block_norm, glu_block_norm_bwd, glu_block_norm_mxfp8, glu_linear,  # noqa: E402,F401
                   glu_linear_bwd, glu_moe_combine, glu_moe_combine_bwd, glu_moe_permute, glu_moe_sort)
+from .gated import glu_bwd_ckpt, glu_fwd_ckpt, glu_gated_linear, glu_gated_linear_bwd  # noqa: E402,F401

@@ -25,7 +25,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libglu_mx.so")
 SOURCES = ["api.cpp", "glu_bf16.hip", "glu_mxfp8.hip", "glu_nvfp4.hip", "glu_gemm.hip", "glu_stream.hip",
-           "api_ffn.cpp", "glu_norm.hip", "glu_linear.hip", "glu_moe.hip"]
+           "api_ffn.cpp", "glu_norm.hip", "glu_linear.hip", "glu_moe.hip",
+           "api_gated.cpp", "glu_gated.hip", "glu_ckpt.hip"]
 ARCH = "gfx950"
 
 COMMON = [
@@ -57,7 +58,7 @@ def _compile(src, verbose):
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(6, len(SOURCES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]

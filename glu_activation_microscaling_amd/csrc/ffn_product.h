@@ -7,6 +7,9 @@
 #include "ffn_device.h"
 #include "ffn_launch.h"
 #include "ffn_split.h"
+#include "mx_block.h"
+
+#include <type_traits>
 
 namespace glu {
 namespace {
@@ -53,7 +56,8 @@ hipError_t with_linear_act(int act, F&& f) {
 // ---- the product ---------------------------------------------------------------------------
 // C[i, j] = sum_k A(i, k) B(j, k).  An operand is stored with k along its rows (element (i, k)
 // at i ld + k) or transposed (at k ld + i).
-enum { FWD, DGRAD, WGRAD };
+// GATED: C[i, n] = act(gate) * up of two such sums, B's rows in pairs (see GatedOperand).
+enum { FWD, DGRAD, WGRAD, GATED };
 
 struct ProductArgs {
   int64_t I, J, K;           // rows of C, columns of C, length of the sum
@@ -71,6 +75,24 @@ struct ProductArgs {
   uint16_t* pre;             // [I, J]
   float* work;               // split sums: [parts, rows of C, J]
 };
+struct GatedArgs : ProductArgs {   // J outputs from 2 J rows of B; bias [groups, 2 J] in their order
+  int paired;                // B's rows are gate0, up0, gate1, ... instead of all gates, then all ups
+  uint8_t* codes;            // MXFP8 codes [I, 2 J] of [gate | up], or null; pre is then null
+  uint8_t* scales;           // and their scales [I, 2 ceil(J / 32)]
+};
+// The arguments by the kind of product.  (A kernel's parameter type must not be spelled with a nameless
+// enumeration's value: host and device may number nameless types differently, and then the
+// host does not find the kernel.)
+template <bool IS_GATED>
+struct ArgsOf {
+  using type = ProductArgs;
+};
+template <>
+struct ArgsOf<true> {
+  using type = GatedArgs;
+};
+// Columns of a gated product's sums: 16 gate and 16 up for each 16 outputs.
+__host__ __device__ constexpr int64_t gated_columns(int64_t J) { return (J + 15) / 16 * 32; }
 
 // Row segments of grouped products: 0 holds the rows before the first group, e + 1 those of group e,
 // groups + 1 those after the last group.  The first and the last are of no group and count as group
@@ -220,6 +242,42 @@ struct Operand {
   }
 };
 
+// The B operand of a gated product: row R of a tile is the gate (R / 16 even) or up row of output
+// 16 (R / 32) + R % 16 of the tile, so a wave's neighbouring 16 x 16 results are the gate and the up
+// values of the same outputs in the same lanes.  Gate and up rows may be farther apart than 32-bit
+// offsets reach: each half has its base, and an 8-row load is of one half.
+template <int B_, int WAVES>
+struct GatedOperand {
+  static constexpr int LOADS = B_ * BK * 2 / 1024 / WAVES;
+  static constexpr uint32_t BYTES = B_ * BK * 2;
+  static_assert(LOADS >= 1 && LOADS * WAVES * 1024 == (int)BYTES);
+  uint32_t off[LOADS];
+  const uint16_t* base[2];
+
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t K, int64_t N, bool paired, int64_t n0, uint32_t wave,
+                                       uint32_t lane) {
+    const int64_t step = paired ? 2 * K : K;
+    base[0] = uniform(p + n0 * step);
+    base[1] = uniform(p + n0 * step + (paired ? K : N * K));
+#pragma unroll
+    for (int q = 0; q < LOADS; q++) {
+      const uint32_t row = 8u * (wave * LOADS + q) + (lane >> 3), n = 16u * (row >> 5) + (row & 15u);
+      const uint32_t chunk = (lane & 7u) ^ ((row >> 1) & 7u);
+      off[q] = n0 + n < N ? 2u * (n * (uint32_t)step + 8u * chunk) : kOob;
+    }
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void issue(int q, uint32_t k, uint32_t k1, uint8_t* lds, uint32_t wave, uint32_t lane) const {
+    uint32_t o = off[q];
+    if constexpr (TAIL) {
+      const uint32_t row = 8u * (wave * LOADS + q) + (lane >> 3);
+      if (k + 8u * ((lane & 7u) ^ ((row >> 1) & 7u)) >= k1) o = kOob;
+    }
+    const auto r = rsrc(((wave * LOADS + q) & 2u ? base[1] : base[0]) + k);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(lds + (wave * LOADS + q) * 1024u), 16, o, 0, 0, 0);
+  }
+};
+
 // Four elements of a 4 x 16 block (per 16 lanes) of 16-bit values in LDS, transposed.  The
 // restricted pointer tells the compiler that no copy into LDS that is under way writes here;
 // without it every such read would wait for all of them.
@@ -332,6 +390,110 @@ __device__ __forceinline__ void put16(u32x4 v, __amdgpu_buffer_rsrc_t to, uint32
   __builtin_amdgcn_raw_buffer_store_b128(v, to, offset, 0, 0);
 }
 
+// ---- the gated epilogue ----------------------------------------------------------------------
+
+// Four consecutive BF16 values of a bias of gates and ups: gates at n, ups J later, or pairs.
+__device__ __forceinline__ void load_gated_bias(float (&g)[4], float (&u)[4], const GatedArgs& a, int64_t group, int64_t n) {
+  const uint16_t* b = a.bias == nullptr || n >= a.J ? nullptr : a.bias + group * 2 * a.J;
+  if (a.paired) {
+    float v[8];
+    load_bf16(v, b == nullptr ? nullptr : b + 2 * n);
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      g[e] = v[2 * e];
+      u[e] = v[2 * e + 1];
+    }
+  } else {
+    load_bf16(g, b == nullptr ? nullptr : b + n);
+    load_bf16(u, b == nullptr ? nullptr : b + a.J + n);
+  }
+}
+
+// Each wave holds 32 outputs (tiles 2 q and 2 q + 1 are gate and up of outputs 16 q ..) of its rows:
+// the GLU in registers, then, a row tile at a time, through the wave's piece of LDS into 16-byte
+// pieces of rows.  Gate and up are kept for the gradient as BF16 or as MXFP8 codes of those
+// BF16 values, a block of 32 being the wave's part of a row.
+constexpr uint32_t GATED_PITCH = 80, GATED_LDS = 3 * 16 * GATED_PITCH;
+template <int ACT, int TI, int TJ, typename FrA>
+__device__ __forceinline__ void gated_epilogue(const GatedArgs& a, int64_t group, const RowTile& t, int64_t n0, uint32_t wi,
+                                               uint32_t wj, uint32_t lane, uint8_t* mine, v4f (&acc)[TI][TJ]) {
+  static_assert(TJ == 4, "a wave's outputs are one MXFP8 block");
+  const uint32_t g = lane >> 4, r = lane & 15u, c0 = 32u * wj, ld = (uint32_t)a.ld_c, N = (uint32_t)a.J;
+  const uint32_t rows = (uint32_t)(t.i1 - t.i0), NB = (N + 31u) / 32u;
+  const uint32_t lrow = lane >> 2, col = c0 + 8u * (lane & 3u);    // of the lane's eight outputs once in rows
+  const bool in = n0 + col < a.J, any = n0 + c0 < a.J;
+  const auto rh = rsrc(uniform(a.c + t.i0 * a.ld_c + n0));
+  const bool has_pre = a.pre != nullptr, has_codes = a.codes != nullptr;
+  const auto rp = rsrc(uniform(has_pre ? a.pre + t.i0 * 2 * a.J + n0 : a.c));
+  const auto rq = rsrc(uniform((const uint16_t*)(has_codes ? (const void*)(a.codes + t.i0 * 2 * a.J + n0) : a.c)));
+  const auto rs = rsrc(uniform((const uint16_t*)(has_codes ? (const void*)(a.scales + t.i0 * 2 * NB + n0 / 32) : a.c)));
+  const bool none = group == a.groups;   // rows of no group are zero
+  float bg[2][4], bu[2][4];
+#pragma unroll
+  for (int q = 0; q < 2; q++) {
+    if (none) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) bg[q][e] = bu[q][e] = 0.0f;
+    } else {
+      load_gated_bias(bg[q], bu[q], a, group, n0 + c0 + 16u * q + 4u * g);
+    }
+  }
+  auto through = [&](uint8_t* at, const uint32_t (&p)[2][2]) {
+#pragma unroll
+    for (int q = 0; q < 2; q++) *reinterpret_cast<u32x2*>(at + r * GATED_PITCH + 32 * q + 8 * g) = (u32x2){p[q][0], p[q][1]};
+    return *reinterpret_cast<const u32x4*>(at + lrow * GATED_PITCH + 16 * (lane & 3u));
+  };
+#pragma unroll
+  for (int i = 0; i < TI; i++) {
+    const uint32_t first = 16u * FrA::tile(wi, i), row = first + lrow;
+    const bool ok = in && row < rows;
+    uint32_t H[2][2], G[2][2], U[2][2];
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+      float gate[4], up[4], h[4];
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        gate[e] = acc[i][2 * q][e] + bg[q][e];
+        up[e] = acc[i][2 * q + 1][e] + bu[q][e];
+      }
+      glu_of<ACT>(h, gate, up);
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        H[q][e] = pack_bf16(h[2 * e], h[2 * e + 1]);
+        G[q][e] = pack_bf16(gate[2 * e], gate[2 * e + 1]);
+        U[q][e] = pack_bf16(up[2 * e], up[2 * e + 1]);
+      }
+    }
+    put16(through(mine, H), rh, ok ? 2u * (row * ld + col) : kOob);
+    if (has_pre) {
+      put16(through(mine + 16 * GATED_PITCH, G), rp, ok ? 2u * (row * 2u * N + col) : kOob);
+      put16(through(mine + 32 * GATED_PITCH, U), rp, ok ? 2u * (row * 2u * N + N + col) : kOob);
+    }
+    if (has_codes) {
+      const uint32_t g4[4] = {G[0][0], G[0][1], G[1][0], G[1][1]}, u4[4] = {U[0][0], U[0][1], U[1][0], U[1][1]};
+      uint32_t m = top_of(g4) | top_of(u4) << 16;   // over the row's four lanes
+      m = pkmax(m, swz_xor16(m));
+      m = pkmax(m, (uint32_t)__builtin_amdgcn_ds_bpermute((int)(4u * (lane ^ 32u)), (int)m));
+      const uint32_t sg = block_scale(lo16(m)), su = block_scale(hi16(m));
+      uint8_t* at = mine + 16 * GATED_PITCH;
+#pragma unroll
+      for (int q = 0; q < 2; q++) {
+        *reinterpret_cast<uint32_t*>(at + r * 40 + 16 * q + 4 * g) = block_codes(G[q][0], G[q][1], sg);
+        *reinterpret_cast<uint32_t*>(at + 640 + r * 40 + 16 * q + 4 * g) = block_codes(U[q][0], U[q][1], su);
+      }
+      const u32x2 cg = *reinterpret_cast<const u32x2*>(at + lrow * 40 + 8 * (lane & 3u));
+      const u32x2 cu = *reinterpret_cast<const u32x2*>(at + 640 + lrow * 40 + 8 * (lane & 3u));
+      __builtin_amdgcn_raw_buffer_store_b64(cg, rq, ok ? row * 2u * N + col : kOob, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(cu, rq, ok ? row * 2u * N + N + col : kOob, 0, 0);
+      const uint32_t at_s = any && g == 0 && first + r < rows ? (first + r) * 2u * NB + c0 / 32u : kOob;
+      __builtin_amdgcn_raw_buffer_store_b8((uint8_t)sg, rs, at_s, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b8((uint8_t)su, rs, at_s == kOob ? kOob : at_s + NB, 0, 0);
+    }
+  }
+}
+
+// ---- the tiled product -----------------------------------------------------------------------
+
 // WI x WJ waves of TI x TJ tiles of 16 x 16 each: a tile of 16 WI TI rows by 16 WJ TJ columns.
 //
 // NS LDS stages, each a step of BK elements.  A step's matrix work runs in two halves of 32
@@ -353,12 +515,13 @@ __device__ __forceinline__ void put16(u32x4 v, __amdgpu_buffer_rsrc_t to, uint32
 // stages of 32 a compute unit 581; workgroups that stay and load the next tile during the
 // epilogue 560.
 template <int MODE, int ACT, int WI, int WJ, int TI, int TJ, int NS>
-__global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_t tiles_i, uint32_t tiles_j,
-                                                          uint32_t splits) {
-  constexpr bool TA = MODE == WGRAD, TB = MODE != FWD;
+__global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE == 3>::type a,
+                                                          uint32_t tiles_i, uint32_t tiles_j, uint32_t splits) {
+  static_assert(GATED == 3);
+  constexpr bool TA = MODE == WGRAD, TB = MODE == DGRAD || MODE == WGRAD;
   constexpr int BI = 16 * WI * TI, BJ = 16 * WJ * TJ, WAVES = WI * WJ;
   using OpA = Operand<TA, BI, WAVES>;
-  using OpB = Operand<TB, BJ, WAVES>;
+  using OpB = std::conditional_t<MODE == GATED, GatedOperand<BJ, WAVES>, Operand<TB, BJ, WAVES>>;
   // both stages of A, then both of B: every fragment read's place is within the 16-bit offset
   // of a read instruction from the lane's base
   __shared__ __attribute__((aligned(16))) uint8_t smem[NS * (OpA::BYTES + OpB::BYTES)];
@@ -408,14 +571,20 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
     k1 = min(k1, k0 + s1 * BK);
     k0 += s0 * BK;
   }
-  const int64_t j0 = (int64_t)tj * BJ, j1 = min(j0 + BJ, a.J);
+  const int64_t width = MODE == GATED ? gated_columns(a.J) : a.J;   // columns of the sums
+  const int64_t j0 = (int64_t)tj * BJ, j1 = min(j0 + BJ, width);
   const uint32_t wi = wave / WJ, wj = wave % WJ;
 
   OpA oa;
   OpB ob;
   oa.init(a.a, a.ld_a, t.i0, t.i1, wave, lane);
-  ob.init(a.b + group * a.b_group, a.ld_b, j0, j1, wave, lane);
-  if (MODE != WGRAD && group == a.groups) ob.base = a.b;
+  const bool none = MODE != WGRAD && group == a.groups;   // rows of no group
+  if constexpr (MODE == GATED) {
+    ob.init(none ? a.b : a.b + group * a.b_group, a.ld_b, a.J, a.paired != 0, j0 / 2, wave, lane);
+  } else {
+    ob.init(a.b + group * a.b_group, a.ld_b, j0, j1, wave, lane);
+    if (none) ob.base = a.b;
+  }
   using FrA = Fragments<TA, BI, WI, TI>;
   using FrB = Fragments<TB, BJ, WJ, TJ>;
   FrA fa;
@@ -606,17 +775,22 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
   const uint32_t rows = (uint32_t)(t.i1 - t.i0), cols = (uint32_t)(j1 - j0);
   if (splits > 1) {
     const int64_t at = (MODE == WGRAD ? part * a.groups + group : (int64_t)part) * a.I + t.i0;
-    const auto rw = rsrc(uniform((const uint16_t*)(a.work + at * a.J + j0)));
+    const auto rw = rsrc(uniform((const uint16_t*)(a.work + at * width + j0)));
 #pragma unroll
     for (int i = 0; i < TI; i++) {
       const uint32_t first = 16u * FrA::tile(wi, i);
 #pragma unroll
       for (int j = 0; j < TJ; j++) {
         const uint32_t col = 16u * FrB::tile(wj, j) + 4u * g;
-        const uint32_t o = first + r < rows && col < cols ? 4u * ((first + r) * (uint32_t)a.J + col) : kOob;
+        const uint32_t o = first + r < rows && col < cols ? 4u * ((first + r) * (uint32_t)width + col) : kOob;
         put16(__builtin_bit_cast(u32x4, acc[i][j]), rw, o);
       }
     }
+    return;
+  }
+  if constexpr (MODE == GATED) {
+    static_assert(WAVES * GATED_LDS <= sizeof(smem));
+    gated_epilogue<ACT, TI, TJ, FrA>(a, group, t, j0 / 2, wi, wj, lane, smem + wave * GATED_LDS, acc);
     return;
   }
   // A row tile's 16 x (16 TJ) sums go through the wave's own piece of LDS, so that a lane gets 8
@@ -637,7 +811,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(ProductArgs a, uint32_
   const auto rc = rsrc(uniform(a.c + (MODE == WGRAD ? group * a.c_group : 0) + t.i0 * a.ld_c + j0));
   const bool has_pre = MODE == FWD && a.pre != nullptr;
   const auto rp = rsrc(uniform(has_pre ? a.pre + t.i0 * a.J + j0 : a.c));
-  if (MODE == FWD && group == a.groups) {   // rows of no group are zero
+  if (MODE == FWD && none) {   // rows of no group are zero
 #pragma unroll
     for (int i = 0; i < TI; i++)
 #pragma unroll
@@ -901,6 +1075,36 @@ hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
   return launch_kernel(k_product_join<MODE, ACT>, dim3(grid_for(ceil_div(octets, 256), 4096)), dim3(256), s, a,
                        (uint32_t)p.splits);
 }
+
+// ---- column sums in parts --------------------------------------------------------------------
+
+// 64 columns a workgroup, every fourth part a wave.
+__global__ __launch_bounds__(256) void k_linear_join(const float* sums, int64_t parts, int64_t n, uint16_t* out) {
+  __shared__ float part[4][64];
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  const int64_t i = 64 * (int64_t)blockIdx.x + lane;
+  float s = 0.0f;
+  if (i < n) {
+#pragma unroll 4
+    for (int64_t p = wave; p < parts; p += 4) s += sums[p * n + i];
+  }
+  part[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && i < n)
+    out[i] = (uint16_t)pack_bf16((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]), 0.0f);
+}
+
+// Parts each group's rows are cut into for the column sums: enough workgroups to fill the chip,
+// with 64 rows or more of an average group each.
+int64_t grad_parts(int64_t M, int64_t N, int64_t groups) {
+  if (N == 0) return 1;
+  const int64_t tiles = (N + 255) / 256 * groups, want = (1024 + tiles - 1) / tiles;
+  const int64_t most = (M / groups + 63) / 64;
+  const int64_t p = want < most ? want : most;
+  return p < 1 ? 1 : p;
+}
+
+int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
 
 }  // namespace
 }  // namespace glu

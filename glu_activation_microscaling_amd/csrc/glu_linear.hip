@@ -81,34 +81,6 @@ __global__ __launch_bounds__(256) void k_linear_grad(GradArgs a) {
   }
 }
 
-// 64 columns a workgroup, every fourth part a wave.
-__global__ __launch_bounds__(256) void k_linear_join(const float* sums, int64_t parts, int64_t n, uint16_t* out) {
-  __shared__ float part[4][64];
-  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-  const int64_t i = 64 * (int64_t)blockIdx.x + lane;
-  float s = 0.0f;
-  if (i < n) {
-#pragma unroll 4
-    for (int64_t p = wave; p < parts; p += 4) s += sums[p * n + i];
-  }
-  part[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && i < n)
-    out[i] = (uint16_t)pack_bf16((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]), 0.0f);
-}
-
-// Parts each group's rows are cut into for the column sums: enough workgroups to fill the chip,
-// with 64 rows or more of an average group each.
-int64_t grad_parts(int64_t M, int64_t N, int64_t groups) {
-  if (N == 0) return 1;
-  const int64_t tiles = (N + 255) / 256 * groups, want = (1024 + tiles - 1) / tiles;
-  const int64_t most = (M / groups + 63) / 64;
-  const int64_t p = want < most ? want : most;
-  return p < 1 ? 1 : p;
-}
-
-int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
-
 }  // namespace
 
 int64_t linear_work_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, bool grouped) {

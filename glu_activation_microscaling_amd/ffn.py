@@ -55,6 +55,18 @@ def _stream(t):
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+_device = getattr(torch._C, "_cuda_getDevice", None)   # torch.cuda.current_device() without its checks
+
+
+def _launch(t, name, *args):
+    """_call on t's device, whichever is current, with the current stream of that device."""
+    dev = t.get_device()
+    if (torch.cuda.current_device() if _device is None else _device()) == dev:
+        return _call(name, *args, _stream(t))
+    with torch.cuda.device(dev):
+        return _call(name, *args, _stream(t))
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr() or None   # an empty tensor's pointer is 0
 

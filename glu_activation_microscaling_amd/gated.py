@@ -1,0 +1,141 @@
+"""Binding of the gated projections and of the GLU's 8-bit checkpoints.
+
+Argument marshalling only, as for the other entry points (C names and formulas in
+include/glu_mx.h); every function is also a name of the package:
+  glu_gated_linear(x, w, bias, act=, w_layout=, offsets=, save=)  -> h, or (h, pre, scales)
+  glu_gated_linear_bwd(dh, x, w, pre, scales, ...)                -> (dx, dw, db, h)
+  glu_fwd_ckpt(gate, up, act=, layout=)                           -> (h, q, s)
+  glu_bwd_ckpt(q, s, dh, act=, layout=)                           -> (d, h)
+What is disabled comes back zero-sized (fixed arity).  Scratch memory is a torch allocation of
+the call, on the current stream.
+"""
+import torch
+
+from . import ACT, LAYOUT, W_LAYOUT, _operands
+from .ffn import _BF16, _I32, _empty, _launch, _like, _matrix, _one_row, _ptr, _same_device, _size
+
+SAVE = {"none": 0, "bf16": 1, "mxfp8": 2}
+_U8 = torch.uint8
+
+
+def _choice(value, table, name):
+    if value not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)}")
+    return table[value]
+
+
+def _gated_setup(x, w, bias, offsets, act, w_layout):
+    a, layout = _choice(act, ACT, "act"), _choice(w_layout, W_LAYOUT, "w_layout")
+    if w.dim() not in (2, 3) or w.shape[-2] % 2:
+        raise ValueError("w must be [2N, K], or [groups, 2N, K] with offsets")
+    if (w.dim() == 3) != (offsets is not None):
+        raise ValueError("offsets go with w [groups, 2N, K], and only with it")
+    N, K = w.shape[-2] // 2, w.shape[-1]
+    groups = w.shape[0] if w.dim() == 3 else 1
+    _like(w, "w", _BF16, w.shape)
+    ld_x = _matrix(x, "x", _BF16, None, K)
+    if bias is not None:
+        _like(bias, "bias", _BF16, w.shape[:-1])
+    if offsets is not None:
+        _like(offsets, "offsets", _I32, (groups + 1,))
+    return a, layout, x.shape[0], N, K, groups, ld_x
+
+
+def _scale_columns(N):
+    return 2 * ((N + 31) // 32)
+
+
+def glu_gated_linear(x, w, bias=None, *, act="swiglu", w_layout="split", offsets=None, save="none", out=None):
+    """h = act(x Wg^T + bg) * (x Wu^T + bu), [M, N].  w [2N, K] and bias [2N] hold gates above ups
+    (w_layout "split") or in turn ("paired"); with int32 offsets [groups + 1], w is [groups, 2N, K],
+    rows offsets[e] .. offsets[e + 1] - 1 of x go through w[e] and bias[e], and rows of no group give
+    zeros.  save="bf16" or "mxfp8" returns (h, pre, scales) with what glu_gated_linear_bwd takes,
+    [gate | up]: BF16 pre [M, 2N] (scales zero-sized), or E4M3 codes [M, 2N] and E8M0 scales [M, 2
+    ceil(N/32)]."""
+    a, layout, M, N, K, groups, ld_x = _gated_setup(x, w, bias, offsets, act, w_layout)
+    keep = _choice(save, SAVE, "save")
+    _same_device(x, w, bias, offsets, out)
+    if out is None:
+        h, ld_h = x.new_empty((M, N)), N
+    else:
+        h, ld_h = out, _matrix(out, "out", _BF16, M, N)
+    pre = scales = None
+    if keep:
+        pre = x.new_empty((M, 2 * N), dtype=_BF16 if keep == 1 else _U8)
+        scales = x.new_empty((0,) if keep == 1 else (M, _scale_columns(N)), dtype=_U8)
+    nbytes = _size("glu_gated_linear_work_bytes", keep, M, N, K, groups, int(offsets is not None))
+    work = x.new_empty((nbytes,), dtype=_U8) if nbytes > 0 else None
+    _launch(x, "glu_gated_linear", a, layout, keep, M, N, K, groups, _ptr(offsets), _ptr(x), ld_x, _ptr(w), _ptr(bias),
+          _ptr(h), ld_h, _ptr(pre), _ptr(scales), _ptr(work), nbytes)
+    return (h, pre, scales) if keep else h
+
+
+def glu_gated_linear_bwd(dh, x, w, pre, scales=None, *, act="swiglu", w_layout="split", offsets=None, bias=False,
+                         need_dx=True, need_dw=True, need_h=False):
+    """Gradients of glu_gated_linear from what its save kept (pre, and scales with "mxfp8"), taken at
+    the values kept: (dx [M, K], dw like w, db [2N] or [groups, 2N] in w's order, h [M, N] formed again).
+    bias=True asks for db.  What is not wanted comes back zero-sized."""
+    a, layout, M, N, K, groups, ld_x = _gated_setup(x, w, None, offsets, act, w_layout)
+    ld_dh = _matrix(dh, "dh", _BF16, M, N)
+    if pre.dtype is _U8:
+        if scales is None:
+            raise ValueError("codes need their scales")
+        keep = 2
+        _like(scales, "scales", _U8, (M, _scale_columns(N)))
+    else:
+        if scales is not None and scales.numel():
+            raise ValueError("scales go with codes, and only with them")
+        keep, scales = 1, None
+    _like(pre, "pre", _U8 if keep == 2 else _BF16, (M, 2 * N))
+    _same_device(x, w, dh, pre, scales, offsets)
+    dx = _empty(x, (M, K), _BF16) if need_dx else x.new_empty((0,))
+    dw = torch.empty_like(w) if need_dw else x.new_empty((0,))
+    db = x.new_empty(w.shape[:-1] if bias else (0,))
+    h = x.new_empty((M, N) if need_h else (0,))
+    nbytes = _size("glu_gated_linear_bwd_work_bytes", M, N, K, groups, int(offsets is not None), int(bias))
+    work = x.new_empty((nbytes,), dtype=_U8) if nbytes > 0 else None
+    _launch(x, "glu_gated_linear_bwd", a, layout, keep, M, N, K, groups, _ptr(offsets), _ptr(dh), ld_dh, _ptr(x), ld_x,
+          _ptr(w), _ptr(pre), _ptr(scales), _ptr(dx) if need_dx else None, K, _ptr(dw) if need_dw else None,
+          _ptr(db) if bias else None, _ptr(h) if need_h else None, N, _ptr(work), nbytes)
+    return dx, dw, db, h
+
+
+def glu_fwd_ckpt(gate, up=None, *, act="swiglu", layout="split", need_h=True, out=None):
+    """(h [M, N], q [M, 2N], s [M, 2 ceil(N/32)]): h = act(gate) * up as glu_fwd, and the MXFP8 codes
+    and scales of [gate | up] that glu_bwd_ckpt takes in place of gate and up.  need_h=False leaves h
+    zero-sized."""
+    a, lay = _choice(act, ACT, "act"), _choice(layout, LAYOUT, "layout")
+    M, N, ld = _operands(gate, up, layout)
+    _same_device(gate, up, out)
+    if M == 1:
+        ld = _one_row(gate.shape[1])
+    if not need_h:
+        if out is not None:
+            raise ValueError("out is for h (need_h=True)")
+        h, ld_h = gate.new_empty((0,)), 0
+    elif out is None:
+        h, ld_h = gate.new_empty((M, N)), N
+    else:
+        h, ld_h = out, _matrix(out, "out", _BF16, M, N)
+    q, s = gate.new_empty((M, 2 * N), dtype=_U8), gate.new_empty((M, _scale_columns(N)), dtype=_U8)
+    _launch(gate, "glu_fwd_ckpt", a, lay, M, N, _ptr(gate), _ptr(up), ld, _ptr(h) if need_h else None, ld_h, _ptr(q), _ptr(s))
+    return h, q, s
+
+
+def glu_bwd_ckpt(q, s, dh, *, act="swiglu", layout="split", need_h=False, out=None):
+    """(d [M, 2N], h [M, N]): the gradients of gate and up, [da | db] (layout "split") or in turn
+    ("paired"), at the values that glu_fwd_ckpt's q and s stand for, and act(gate) * up of those values
+    (zero-sized without need_h)."""
+    a, lay = _choice(act, ACT, "act"), _choice(layout, LAYOUT, "layout")
+    ld_dh = _matrix(dh, "dh", _BF16)
+    M, N = dh.shape
+    _like(q, "q", _U8, (M, 2 * N))
+    _like(s, "s", _U8, (M, _scale_columns(N)))
+    _same_device(dh, q, s, out)
+    if out is None:
+        d, ld_d = dh.new_empty((M, 2 * N)), 2 * N
+    else:
+        d, ld_d = out, _matrix(out, "out", _BF16, M, 2 * N)
+    h = dh.new_empty((M, N) if need_h else (0,))
+    _launch(dh, "glu_bwd_ckpt", a, lay, M, N, _ptr(q), _ptr(s), _ptr(dh), ld_dh, _ptr(d), ld_d, _ptr(h) if need_h else None, N)
+    return d, h

@@ -455,6 +455,53 @@ glu_status glu_moe_combine_bwd(int64_t tokens, int64_t choices, int64_t H, int e
                                const float* weights, const int32_t* offsets, uint16_t* dy, int64_t ld_dy,
                                float* dweights, void* stream);
 
+/* ---- Gated projections
+ *   g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) u     (act: GLU_SWIGLU ...)
+ * in one call: both products, the activation and the product.  x [M, K], h [M, N]; w
+ * [groups, 2N, K] contiguous holds Wg's rows above Wu's (w_layout GLU_SPLIT) or gate0, up0,
+ * gate1, ... (GLU_PAIRED), bias [groups, 2N] or NULL in the same order; all BF16.  Sums, bias,
+ * activation and product in FP32, rounded once.  offsets and groups as for glu_linear; rows of no
+ * group give zero rows of h and of what is kept.
+ * What is kept for the backward, [gate | up] whatever w_layout:
+ *   GLU_SAVE_BF16 : pre, BF16 [M, 2N].
+ *   GLU_SAVE_MXFP8: pre, E4M3 codes [M, 2N], and scales, E8M0 bytes [M, 2 ceil(N/32)], of those
+ *                   BF16 values: a checkpoint of glu_fwd_ckpt.
+ * Otherwise pre and scales are NULL.  N is a multiple of 8 up to 2^19, K as for glu_linear. */
+enum { GLU_SAVE_NONE = 0, GLU_SAVE_BF16 = 1, GLU_SAVE_MXFP8 = 2 };
+int64_t glu_gated_linear_work_bytes(int save, int64_t M, int64_t N, int64_t K, int64_t groups, int grouped);
+glu_status glu_gated_linear(int act, int w_layout, int save, int64_t M, int64_t N, int64_t K, int64_t groups,
+                            const int32_t* offsets, const uint16_t* x, int64_t ld_x, const uint16_t* w,
+                            const uint16_t* bias, uint16_t* h, int64_t ld_h, void* pre, uint8_t* scales, void* work,
+                            int64_t work_bytes, void* stream);
+
+/* dp = [dh u act'(g) | dh act(g)] at the gate and up values kept (GLU_SAVE_BF16 or _MXFP8);
+ * dx = dp W, dw[e] = dp^T x and dbias[e] = sum of dp over the rows of group e.  dx [M, K], dw
+ * [groups, 2N, K] and dbias [groups, 2N] in W's order, BF16, each NULL when not wanted; so is h,
+ * act(g) u formed again from the values kept (what the next product's weight gradient needs).  Rows
+ * of no group give zero rows of dx. */
+int64_t glu_gated_linear_bwd_work_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, int grouped, int with_bias);
+glu_status glu_gated_linear_bwd(int act, int w_layout, int save, int64_t M, int64_t N, int64_t K, int64_t groups,
+                                const int32_t* offsets, const uint16_t* dh, int64_t ld_dh, const uint16_t* x,
+                                int64_t ld_x, const uint16_t* w, const void* pre, const uint8_t* scales, uint16_t* dx,
+                                int64_t ld_dx, uint16_t* dw, uint16_t* dbias, uint16_t* h, int64_t ld_h, void* work,
+                                int64_t work_bytes, void* stream);
+
+/* ---- 8-bit checkpoints of the GLU's operands
+ * glu_fwd_ckpt: h = bf16(act(g) u) as glu_fwd (NULL: not wanted), and what the backward needs in 8
+ * bits: q [M, 2N], E4M3 codes of [gate | up], and s [M, 2 ceil(N/32)], one E8M0 byte for each 32
+ * columns of each half (the last block of a half may be shorter).  Codes and scales are the library's
+ * MXFP8 rowwise (for N % 32 == 0 byte for byte what glu_quant_mxfp8_f32 gives for [gate | up]).
+ * glu_bwd_ckpt: g~, u~ = what q and s stand for; d [M, 2N] = [dh u~ act'(g~) | dh act(g~)]
+ * (layout GLU_SPLIT) or in turn (GLU_PAIRED), and h [M, N] = act(g~) u~ (NULL: not wanted).
+ * A block that holds NaN or infinity comes back as NaN; magnitudes of 248 * 2^120 and more may come
+ * back as infinity.  N is a multiple of 8 up to 2^28, row strides multiples of 8. */
+int64_t glu_ckpt_scale_bytes(int64_t M, int64_t N);
+glu_status glu_fwd_ckpt(int act, int layout, int64_t M, int64_t N, const uint16_t* gate, const uint16_t* up,
+                        int64_t ld_in, uint16_t* h, int64_t ld_h, uint8_t* q, uint8_t* s, void* stream);
+glu_status glu_bwd_ckpt(int act, int layout, int64_t M, int64_t N, const uint8_t* q, const uint8_t* s,
+                        const uint16_t* dh, int64_t ld_dh, uint16_t* d, int64_t ld_d, uint16_t* h, int64_t ld_h,
+                        void* stream);
+
 /* Argument checks of the entry points above, as for the others. */
 glu_status glu_check_block_norm(int kind, int flags, int64_t M, int64_t H, int64_t groups, const void* x,
                                 int64_t ld_x, const uint16_t* y, int64_t ld_y, const void* gate,
@@ -490,6 +537,20 @@ glu_status glu_check_moe_combine_bwd(int64_t tokens, int64_t choices, int64_t H,
                                      int64_t ld_dout, const uint16_t* y, int64_t ld_y, const int32_t* rows,
                                      const float* weights, const int32_t* offsets, uint16_t* dy, int64_t ld_dy,
                                      float* dweights);
+
+glu_status glu_check_gated_linear(int act, int w_layout, int save, int64_t M, int64_t N, int64_t K, int64_t groups,
+                                  const int32_t* offsets, const uint16_t* x, int64_t ld_x, const uint16_t* w,
+                                  const uint16_t* bias, uint16_t* h, int64_t ld_h, void* pre, uint8_t* scales,
+                                  void* work, int64_t work_bytes);
+glu_status glu_check_gated_linear_bwd(int act, int w_layout, int save, int64_t M, int64_t N, int64_t K, int64_t groups,
+                                      const int32_t* offsets, const uint16_t* dh, int64_t ld_dh, const uint16_t* x,
+                                      int64_t ld_x, const uint16_t* w, const void* pre, const uint8_t* scales,
+                                      uint16_t* dx, int64_t ld_dx, uint16_t* dw, uint16_t* dbias, uint16_t* h,
+                                      int64_t ld_h, void* work, int64_t work_bytes);
+glu_status glu_check_fwd_ckpt(int act, int layout, int64_t M, int64_t N, const uint16_t* gate, const uint16_t* up,
+                              int64_t ld_in, uint16_t* h, int64_t ld_h, uint8_t* q, uint8_t* s);
+glu_status glu_check_bwd_ckpt(int act, int layout, int64_t M, int64_t N, const uint8_t* q, const uint8_t* s,
+                              const uint16_t* dh, int64_t ld_dh, uint16_t* d, int64_t ld_d, uint16_t* h, int64_t ld_h);
 
 /* Static text for a status code (never NULL). */
 const char* glu_status_string(glu_status status);

@@ -1,0 +1,51 @@
+"""Code-generation checks on the gated projections, the checkpoints and the 8-bit products, compiled
+here for gfx950 (CPU only), as test_ffn_codegen.py's on the kernels around the GLU; and on every
+source that no kernel's name depends on the numbering of nameless types, which differs
+between the host's and the device's compilation (such a kernel is not found when it is launched).
+"""
+import os
+import re
+import shutil
+from concurrent.futures import ThreadPoolExecutor
+
+import pytest
+
+from glu_activation_microscaling_amd import build
+from test_ffn_codegen import PACKED_FP32, hazards, instructions
+
+SOURCES = ["glu_gated.hip", "glu_ckpt.hip"]
+ALL = [s for s in build.SOURCES if s.endswith(".hip")]
+
+pytestmark = pytest.mark.skipif(
+    shutil.which(os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "bin", "hipcc")) is None,
+    reason="hipcc not available")
+
+
+@pytest.fixture(scope="module")
+def asm():
+    with ThreadPoolExecutor(8) as ex:
+        return dict(zip(ALL, ex.map(build.device_asm, ALL)))
+
+
+@pytest.mark.parametrize("src", SOURCES)
+def test_no_packed_fp32_instructions(asm, src):
+    found = PACKED_FP32.findall(asm[src])
+    assert not found, f"{src}: {len(found)} packed-FP32 instructions"
+
+
+@pytest.mark.parametrize("src", SOURCES)
+def test_stores_keep_their_registers(asm, src):
+    found = hazards(instructions(asm[src]))
+    assert not found, f"{src}: {found[:5]}"
+
+
+@pytest.mark.parametrize("src", ALL)
+def test_kernel_names_hold_no_nameless_type(asm, src):
+    names = re.findall(r"^\s*\.amdhsa_kernel (\S+)", asm[src], re.M)
+    assert names and not [n for n in names if "$_" in n or "Ut_" in n]
+
+
+@pytest.mark.parametrize("src", SOURCES)
+def test_no_kernel_uses_scratch(asm, src):
+    used = re.findall(r"^\s*\.amdhsa_private_segment_fixed_size (\d+)", asm[src], re.M)
+    assert used and set(used) == {"0"}
