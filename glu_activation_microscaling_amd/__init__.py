@@ -23,8 +23,9 @@ Entry points (C names in include/glu_mx.h):
   glu_quant_mxfp8_f32(x, rowwise=, colwise=)                -> (q_row, q_col, s_row, s_col)
   glu_quant_nvfp4_f32(x, sf_layout=)                        -> (q, sf)
 The operators around the GLU (ffn.py: glu_block_norm*, glu_linear*, glu_moe_*) and the gated
-projections and checkpoints (gated.py: glu_gated_linear*, glu_*_ckpt) are names of the package
-too.
+projections and checkpoints (gated.py: glu_gated_linear*, glu_*_ckpt) and products in 8-bit
+floating point with a scale per 128 (fp8.py: glu_quant_fp8*, glu_fwd_fp8, glu_linear_fp8) are
+names of the package too.
 A disabled MXFP8 direction comes back as zero-sized tensors (fixed arity), as in the
 MXFP8 page's API section.  Codes and scales are uint8 tensors; BF16 data is torch.bfloat16.
 """
@@ -100,6 +101,10 @@ _FFN_SIGNATURES = {  # without the stream: the arguments that glu_check_* takes 
                          _p, _p, _i64, _p, _i64],
     "fwd_ckpt": [_int, _int, _i64, _i64, _p, _p, _i64, _p, _i64, _p, _p],
     "bwd_ckpt": [_int, _int, _i64, _i64, _p, _p, _p, _i64, _p, _i64, _p, _i64],
+    "quant_fp8": [_int, _i64, _i64, _p, _i64, _p, _p, _p, _p],
+    "fwd_fp8": [_int, _int, _int, _i64, _i64, _p, _p, _i64, _p, _p, _p, _p],
+    "quant_fp8_weight": [_i64, _i64, _i64, _p, _p, _p, _p, _p],
+    "linear_fp8": [_int, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p, _i64, _p, _i64, _p, _i64],
 }
 for _n, _args in _FFN_SIGNATURES.items():
     _SIGNATURES["glu_" + _n] = _args + [_p]
@@ -112,6 +117,7 @@ _SIZES = {   # functions that give a number of bytes
     "glu_gated_linear_work_bytes": [_int, _i64, _i64, _i64, _i64, _int],
     "glu_gated_linear_bwd_work_bytes": [_i64, _i64, _i64, _i64, _int, _int],
     "glu_ckpt_scale_bytes": [_i64, _i64],
+    "glu_linear_fp8_work_bytes": [_i64, _i64, _i64, _i64, _int],
 }
 
 _lib = None
@@ -490,3 +496,4 @@ def glu_stream_probe(srcs, dsts):
 from .ffn import (glu_block_norm, glu_block_norm_bwd, glu_block_norm_mxfp8, glu_linear,  # noqa: E402,F401
                   glu_linear_bwd, glu_moe_combine, glu_moe_combine_bwd, glu_moe_permute, glu_moe_sort)
 from .gated import glu_bwd_ckpt, glu_fwd_ckpt, glu_gated_linear, glu_gated_linear_bwd  # noqa: E402,F401
+from .fp8 import glu_fwd_fp8, glu_linear_fp8, glu_quant_fp8, glu_quant_fp8_weight  # noqa: E402,F401

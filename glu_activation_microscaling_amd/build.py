@@ -26,7 +26,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libglu_mx.so")
 SOURCES = ["api.cpp", "glu_bf16.hip", "glu_mxfp8.hip", "glu_nvfp4.hip", "glu_gemm.hip", "glu_stream.hip",
            "api_ffn.cpp", "glu_norm.hip", "glu_linear.hip", "glu_moe.hip",
-           "api_gated.cpp", "glu_gated.hip", "glu_ckpt.hip"]
+           "api_gated.cpp", "glu_gated.hip", "glu_ckpt.hip",
+           "api_fp8.cpp", "glu_fp8.hip", "glu_fp8_linear.hip"]
 ARCH = "gfx950"
 
 COMMON = [

@@ -502,6 +502,42 @@ glu_status glu_bwd_ckpt(int act, int layout, int64_t M, int64_t N, const uint8_t
                         const uint16_t* dh, int64_t ld_dh, uint16_t* d, int64_t ld_d, uint16_t* h, int64_t ld_h,
                         void* stream);
 
+/* ---- 8-bit floating point with a scale for each block of 128
+ * E4M3 codes and FP32 scales.  With a = max(largest magnitude of the block, 2^-100): scale a / 448,
+ * code = E4M3(x 448 / a), nearest to the real quotient, ties to even.  A block holding NaN or
+ * infinity gets scale NaN and codes 0x7F.  Code rows are contiguous and filled up with zero codes to a
+ * multiple of 16; |n| below is n rounded up to it, and n/128 the number of blocks, rounded up.
+ * glu_quant_fp8: x [M, N] BF16; GLU_ROWWISE: q_row [M, |N|], s_row [N/128, M], a scale for each 128
+ * of a row; GLU_COLWISE: q_col [N, |M|], s_col [M/128, N], a scale for each 128 of a column.  A
+ * disabled direction is NULL.  (Scales of one block of the sum lie together: the products read them
+ * a block at a time.)
+ * glu_fwd_fp8: the same of h = bf16(act(gate) up), operands as for glu_fwd.
+ * glu_quant_fp8_weight: w [groups, N, K] contiguous BF16, a scale for each 128 x 128: q [groups, N,
+ * |K|], s [groups, N/128, K/128], and unless both are NULL the transposed qt [groups, K, |N|], st
+ * [groups, K/128, N/128].
+ * N (and K of weights) are multiples of 8 up to 2^28, row strides multiples of 8. */
+glu_status glu_quant_fp8(int flags, int64_t M, int64_t N, const uint16_t* x, int64_t ld_x, uint8_t* q_row, float* s_row,
+                         uint8_t* q_col, float* s_col, void* stream);
+glu_status glu_fwd_fp8(int act, int layout, int flags, int64_t M, int64_t N, const uint16_t* gate, const uint16_t* up,
+                       int64_t ld_in, uint8_t* q_row, float* s_row, uint8_t* q_col, float* s_col, void* stream);
+glu_status glu_quant_fp8_weight(int64_t groups, int64_t N, int64_t K, const uint16_t* w, uint8_t* q, float* s, uint8_t* qt,
+                                float* st, void* stream);
+
+/* y = x W^T + bias + residual of such operands, [M, N] BF16: products of codes summed over each block
+ * of 128 on the matrix cores, the blocks' sums scaled and added in FP32, rounded once.
+ * xq [M, K], xs [K/128, M]; wq [groups, N, K]; ws [groups, N/128, K/128] (GLU_FP8_W_BLOCK) or [groups,
+ * K/128, N] (GLU_FP8_W_ROW: W was quantized along the sum); bias [groups, N] or NULL, residual [M, N] or
+ * NULL, BF16; offsets and groups as for glu_linear.  K, the length of a code row, is a multiple of 16 up
+ * to 2^20, N a multiple of 8 up to 2^20; row strides of y and residual multiples of 8 up to 2^21.
+ * The gradients are products of the same kind: dx of dy (rowwise) and wt, dW of dy and x (both colwise,
+ * GLU_FP8_W_ROW). */
+enum { GLU_FP8_W_BLOCK = 0, GLU_FP8_W_ROW = 1 };
+int64_t glu_linear_fp8_work_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, int grouped);
+glu_status glu_linear_fp8(int w_scales, int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
+                          const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const uint16_t* bias,
+                          const uint16_t* residual, int64_t ld_res, uint16_t* y, int64_t ld_y, void* work,
+                          int64_t work_bytes, void* stream);
+
 /* Argument checks of the entry points above, as for the others. */
 glu_status glu_check_block_norm(int kind, int flags, int64_t M, int64_t H, int64_t groups, const void* x,
                                 int64_t ld_x, const uint16_t* y, int64_t ld_y, const void* gate,
@@ -551,6 +587,18 @@ glu_status glu_check_fwd_ckpt(int act, int layout, int64_t M, int64_t N, const u
                               int64_t ld_in, uint16_t* h, int64_t ld_h, uint8_t* q, uint8_t* s);
 glu_status glu_check_bwd_ckpt(int act, int layout, int64_t M, int64_t N, const uint8_t* q, const uint8_t* s,
                               const uint16_t* dh, int64_t ld_dh, uint16_t* d, int64_t ld_d, uint16_t* h, int64_t ld_h);
+
+glu_status glu_check_quant_fp8(int flags, int64_t M, int64_t N, const uint16_t* x, int64_t ld_x, uint8_t* q_row,
+                               float* s_row, uint8_t* q_col, float* s_col);
+glu_status glu_check_fwd_fp8(int act, int layout, int flags, int64_t M, int64_t N, const uint16_t* gate,
+                             const uint16_t* up, int64_t ld_in, uint8_t* q_row, float* s_row, uint8_t* q_col,
+                             float* s_col);
+glu_status glu_check_quant_fp8_weight(int64_t groups, int64_t N, int64_t K, const uint16_t* w, uint8_t* q, float* s,
+                                      uint8_t* qt, float* st);
+glu_status glu_check_linear_fp8(int w_scales, int64_t M, int64_t N, int64_t K, int64_t groups, const int32_t* offsets,
+                                const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
+                                const uint16_t* bias, const uint16_t* residual, int64_t ld_res, uint16_t* y,
+                                int64_t ld_y, void* work, int64_t work_bytes);
 
 /* Static text for a status code (never NULL). */
 const char* glu_status_string(glu_status status);

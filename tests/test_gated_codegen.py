@@ -13,7 +13,7 @@ import pytest
 from glu_activation_microscaling_amd import build
 from test_ffn_codegen import PACKED_FP32, hazards, instructions
 
-SOURCES = ["glu_gated.hip", "glu_ckpt.hip"]
+SOURCES = ["glu_gated.hip", "glu_ckpt.hip", "glu_fp8.hip", "glu_fp8_linear.hip"]
 ALL = [s for s in build.SOURCES if s.endswith(".hip")]
 
 pytestmark = pytest.mark.skipif(
