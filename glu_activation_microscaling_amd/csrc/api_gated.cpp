@@ -42,16 +42,17 @@ glu_status check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld) {
 }
 
 // What is kept of [gate | up]: the pointers that go with `save`.
-glu_status check_kept(int save, const void* pre, const uint8_t* scales) {
+glu_status check_kept(int save, const void* pre, const uint8_t* extra) {
   if ((pre == nullptr) != (save == GLU_SAVE_NONE)) return pre == nullptr ? GLU_ERR_NULL : GLU_ERR_ARG;
-  if ((scales == nullptr) != (save != GLU_SAVE_MXFP8)) return scales == nullptr ? GLU_ERR_NULL : GLU_ERR_ARG;
-  return aligned16(pre) && aligned16(scales) ? GLU_OK : GLU_ERR_ALIGN;
+  if ((extra == nullptr) != (save == GLU_SAVE_NONE)) return extra == nullptr ? GLU_ERR_NULL : GLU_ERR_ARG;
+  return aligned16(pre) && aligned16(extra) ? GLU_OK : GLU_ERR_ALIGN;
 }
 Operand kept(int save, const void* pre, int64_t M, int64_t N) {
   return mat(pre, M, 2 * N, 2 * N, save == GLU_SAVE_MXFP8 ? 1 : 2);
 }
-Operand kept_scales(const uint8_t* scales, int64_t M, int64_t N) {
-  return mat(scales, M, scale_columns(N), scale_columns(N), 1);
+Operand kept_extra(int save, const uint8_t* extra, int64_t M, int64_t N) {
+  const int64_t cols = save == GLU_SAVE_MXFP8 ? scale_columns(N) : N;
+  return mat(extra, M, cols, cols, 1);
 }
 
 glu_status check_ckpt_shape(int act, int layout, int64_t M, int64_t N) {
@@ -78,7 +79,7 @@ int64_t glu_gated_linear_work_bytes(int save, int64_t M, int64_t N, int64_t K, i
 
 glu_status glu_check_gated_linear(int act, int w_layout, int save, int64_t M, int64_t N, int64_t K, int64_t groups,
                                   const int32_t* offsets, const uint16_t* x, int64_t ld_x, const uint16_t* w,
-                                  const uint16_t* bias, uint16_t* h, int64_t ld_h, void* pre, uint8_t* scales,
+                                  const uint16_t* bias, uint16_t* h, int64_t ld_h, void* pre, uint8_t* extra,
                                   void* work, int64_t work_bytes) {
   glu_status st = check_gated_shape(act, w_layout, save, M, N, K, groups, offsets != nullptr);
   if (st != GLU_OK || M == 0 || N == 0) return st;
@@ -86,14 +87,14 @@ glu_status glu_check_gated_linear(int act, int w_layout, int save, int64_t M, in
   if ((st = check_matrix(x, M, K, ld_x)) != GLU_OK) return st;
   if ((st = check_matrix(w, groups * 2 * N, K, K)) != GLU_OK) return st;
   if ((st = check_matrix(h, M, N, ld_h)) != GLU_OK) return st;
-  if ((st = check_kept(save, pre, scales)) != GLU_OK) return st;
+  if ((st = check_kept(save, pre, extra)) != GLU_OK) return st;
   if (!aligned16(bias) || !aligned16(work)) return GLU_ERR_ALIGN;
   const int64_t need = glu::gated_linear_work_bytes(save, M, N, K, groups, offsets != nullptr);
   if (need > 0 && work == nullptr) return GLU_ERR_NULL;
   if (need > work_bytes) return GLU_ERR_SHAPE;
   const Operand X = mat(K ? x : nullptr, M, K, ld_x, 2), W = mat(K ? w : nullptr, groups * 2 * N, K, K, 2),
                 B = mat(bias, groups, 2 * N, 2 * N, 2), H = mat(h, M, N, ld_h, 2), P = kept(save, pre, M, N),
-                S = kept_scales(scales, M, N), O = mat(offsets, 1, groups + 1, groups + 1, 4),
+                S = kept_extra(save, extra, M, N), O = mat(offsets, 1, groups + 1, groups + 1, 4),
                 WS = mat(need ? work : nullptr, 1, need, need, 1);
   if (any_overflow({X, W, B, H, P, S, O, WS})) return GLU_ERR_SHAPE;
   return check_no_overlap({H, P, S, WS}, {X, W, B, O});
@@ -101,12 +102,12 @@ glu_status glu_check_gated_linear(int act, int w_layout, int save, int64_t M, in
 
 glu_status glu_gated_linear(int act, int w_layout, int save, int64_t M, int64_t N, int64_t K, int64_t groups,
                             const int32_t* offsets, const uint16_t* x, int64_t ld_x, const uint16_t* w,
-                            const uint16_t* bias, uint16_t* h, int64_t ld_h, void* pre, uint8_t* scales, void* work,
+                            const uint16_t* bias, uint16_t* h, int64_t ld_h, void* pre, uint8_t* extra, void* work,
                             int64_t work_bytes, void* stream) {
   const glu_status st = glu_check_gated_linear(act, w_layout, save, M, N, K, groups, offsets, x, ld_x, w, bias, h, ld_h,
-                                               pre, scales, work, work_bytes);
+                                               pre, extra, work, work_bytes);
   if (st != GLU_OK || M == 0 || N == 0) return st;
-  const glu::GatedLinearArgs a{act, w_layout, save, M, N, K, groups, offsets, x, ld_x, w, bias, h, ld_h, pre, scales,
+  const glu::GatedLinearArgs a{act, w_layout, save, M, N, K, groups, offsets, x, ld_x, w, bias, h, ld_h, pre, extra,
                                (float*)work};
   return status_of(glu::launch_gated_linear(a, (hipStream_t)stream));
 }
@@ -118,7 +119,7 @@ int64_t glu_gated_linear_bwd_work_bytes(int64_t M, int64_t N, int64_t K, int64_t
 
 glu_status glu_check_gated_linear_bwd(int act, int w_layout, int save, int64_t M, int64_t N, int64_t K, int64_t groups,
                                       const int32_t* offsets, const uint16_t* dh, int64_t ld_dh, const uint16_t* x,
-                                      int64_t ld_x, const uint16_t* w, const void* pre, const uint8_t* scales,
+                                      int64_t ld_x, const uint16_t* w, const void* pre, const uint8_t* extra,
                                       uint16_t* dx, int64_t ld_dx, uint16_t* dw, uint16_t* dbias, uint16_t* h,
                                       int64_t ld_h, void* work, int64_t work_bytes) {
   glu_status st = check_gated_shape(act, w_layout, save, M, N, K, groups, offsets != nullptr);
@@ -126,7 +127,10 @@ glu_status glu_check_gated_linear_bwd(int act, int w_layout, int save, int64_t M
   if (save == GLU_SAVE_NONE) return GLU_ERR_ARG;
   if (((uintptr_t)offsets & 3u) != 0) return GLU_ERR_ALIGN;
   if ((st = check_matrix(dh, M, N, ld_dh)) != GLU_OK) return st;
-  if (M > 0 && N > 0 && (st = check_kept(save, pre, scales)) != GLU_OK) return st;
+  if (M > 0 && N > 0) {
+    if (pre == nullptr || (extra == nullptr && save == GLU_SAVE_MXFP8)) return GLU_ERR_NULL;
+    if (!aligned16(pre) || !aligned16(extra)) return GLU_ERR_ALIGN;
+  }
   if (dx != nullptr) {
     if ((st = check_matrix(w, groups * 2 * N, K, K)) != GLU_OK) return st;
     if ((st = check_matrix(dx, M, K, ld_dx)) != GLU_OK) return st;
@@ -140,7 +144,7 @@ glu_status glu_check_gated_linear_bwd(int act, int w_layout, int save, int64_t M
   const bool some = M > 0 && N > 0, sum = K > 0;
   const Operand DH = mat(some ? dh : nullptr, M, N, ld_dh, 2), X = mat(dw && M && sum ? x : nullptr, M, K, ld_x, 2),
                 W = mat(dx && N && sum ? w : nullptr, groups * 2 * N, K, K, 2),
-                P = kept(save, some ? pre : nullptr, M, N), S = kept_scales(some ? scales : nullptr, M, N),
+                P = kept(save, some ? pre : nullptr, M, N), S = kept_extra(save, some ? extra : nullptr, M, N),
                 O = mat(offsets, 1, groups + 1, groups + 1, 4), DX = mat(M && sum ? dx : nullptr, M, K, ld_dx, 2),
                 DW = mat(N && sum ? dw : nullptr, groups * 2 * N, K, K, 2),
                 DB = mat(N ? dbias : nullptr, groups, 2 * N, 2 * N, 2), H = mat(some ? h : nullptr, M, N, ld_h, 2),
@@ -151,14 +155,14 @@ glu_status glu_check_gated_linear_bwd(int act, int w_layout, int save, int64_t M
 
 glu_status glu_gated_linear_bwd(int act, int w_layout, int save, int64_t M, int64_t N, int64_t K, int64_t groups,
                                 const int32_t* offsets, const uint16_t* dh, int64_t ld_dh, const uint16_t* x,
-                                int64_t ld_x, const uint16_t* w, const void* pre, const uint8_t* scales, uint16_t* dx,
+                                int64_t ld_x, const uint16_t* w, const void* pre, const uint8_t* extra, uint16_t* dx,
                                 int64_t ld_dx, uint16_t* dw, uint16_t* dbias, uint16_t* h, int64_t ld_h, void* work,
                                 int64_t work_bytes, void* stream) {
   const glu_status st = glu_check_gated_linear_bwd(act, w_layout, save, M, N, K, groups, offsets, dh, ld_dh, x, ld_x, w,
-                                                   pre, scales, dx, ld_dx, dw, dbias, h, ld_h, work, work_bytes);
+                                                   pre, extra, dx, ld_dx, dw, dbias, h, ld_h, work, work_bytes);
   if (st != GLU_OK) return st;
   // what has no elements is not launched for; with M == 0, dw and dbias are still written (zero)
-  const glu::GatedLinearBwdArgs a{act, w_layout, save, M, N, K, groups, offsets, dh, ld_dh, x, ld_x, w, pre, scales,
+  const glu::GatedLinearBwdArgs a{act, w_layout, save, M, N, K, groups, offsets, dh, ld_dh, x, ld_x, w, pre, extra,
                                   M && K ? dx : nullptr, ld_dx, N && K ? dw : nullptr, N ? dbias : nullptr,
                                   M && N ? h : nullptr, ld_h, (uint8_t*)work};
   if (a.dx == nullptr && a.dw == nullptr && a.db == nullptr && a.h == nullptr) return GLU_OK;
@@ -183,7 +187,7 @@ glu_status glu_check_fwd_ckpt(int act, int layout, int64_t M, int64_t N, const u
   if (h != nullptr && (st = check_rows(h, N, ld_h)) != GLU_OK) return st;
   if (!aligned16(up) || !aligned16(q) || !aligned16(s)) return GLU_ERR_ALIGN;
   const Operand G = mat(gate, M, cols, ld_in, 2), U = mat(up, M, N, ld_in, 2), H = mat(h, M, N, ld_h, 2),
-                Q = kept(GLU_SAVE_MXFP8, q, M, N), S = kept_scales(s, M, N);
+                Q = kept(GLU_SAVE_MXFP8, q, M, N), S = kept_extra(GLU_SAVE_MXFP8, s, M, N);
   if (any_overflow({G, U, H, Q, S})) return GLU_ERR_SHAPE;
   return check_no_overlap({H, Q, S}, {G, U});
 }
@@ -203,7 +207,7 @@ glu_status glu_check_bwd_ckpt(int act, int layout, int64_t M, int64_t N, const u
   if ((st = check_rows(dh, N, ld_dh)) != GLU_OK || (st = check_rows(d, 2 * N, ld_d)) != GLU_OK) return st;
   if (h != nullptr && (st = check_rows(h, N, ld_h)) != GLU_OK) return st;
   if (!aligned16(q) || !aligned16(s)) return GLU_ERR_ALIGN;
-  const Operand Q = kept(GLU_SAVE_MXFP8, q, M, N), S = kept_scales(s, M, N), DH = mat(dh, M, N, ld_dh, 2),
+  const Operand Q = kept(GLU_SAVE_MXFP8, q, M, N), S = kept_extra(GLU_SAVE_MXFP8, s, M, N), DH = mat(dh, M, N, ld_dh, 2),
                 DD = mat(d, M, 2 * N, ld_d, 2), H = mat(h, M, N, ld_h, 2);
   if (any_overflow({Q, S, DH, DD, H})) return GLU_ERR_SHAPE;
   return check_no_overlap({DD, H}, {Q, S, DH});

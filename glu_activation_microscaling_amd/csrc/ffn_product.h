@@ -77,6 +77,7 @@ struct ProductArgs {
 };
 struct GatedArgs : ProductArgs {   // J outputs from 2 J rows of B; bias [groups, 2 J] in their order
   int paired;                // B's rows are gate0, up0, gate1, ... instead of all gates, then all ups
+  uint8_t* rest;             // with pre [I, 2 J] of [gate | up]: four more bits of each value, [I, J] bytes
   uint8_t* codes;            // MXFP8 codes [I, 2 J] of [gate | up], or null; pre is then null
   uint8_t* scales;           // and their scales [I, 2 ceil(J / 32)]
 };
@@ -411,9 +412,9 @@ __device__ __forceinline__ void load_gated_bias(float (&g)[4], float (&u)[4], co
 
 // Each wave holds 32 outputs (tiles 2 q and 2 q + 1 are gate and up of outputs 16 q ..) of its rows:
 // the GLU in registers, then, a row tile at a time, through the wave's piece of LDS into 16-byte
-// pieces of rows.  Gate and up are kept for the gradient as BF16 or as MXFP8 codes of those
-// BF16 values, a block of 32 being the wave's part of a row.
-constexpr uint32_t GATED_PITCH = 80, GATED_LDS = 3 * 16 * GATED_PITCH;
+// pieces of rows.  Gate and up are kept for the gradient as BF16 with four more bits (wide_pair) or
+// as MXFP8 codes of BF16 values, a block of 32 being the wave's part of a row.
+constexpr uint32_t GATED_PITCH = 80, REST_PITCH = 20, GATED_LDS = 3 * 16 * GATED_PITCH + 2 * 16 * REST_PITCH;
 template <int ACT, int TI, int TJ, typename FrA>
 __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, int64_t group, const RowTile& t, int64_t n0, uint32_t wi,
                                                uint32_t wj, uint32_t lane, uint8_t* mine, v4f (&acc)[TI][TJ]) {
@@ -425,6 +426,7 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, int64_t group
   const auto rh = rsrc(uniform(a.c + t.i0 * a.ld_c + n0));
   const bool has_pre = a.pre != nullptr, has_codes = a.codes != nullptr;
   const auto rp = rsrc(uniform(has_pre ? a.pre + t.i0 * 2 * a.J + n0 : a.c));
+  const auto rn = rsrc(uniform((const uint16_t*)(has_pre ? (const void*)(a.rest + t.i0 * a.J + n0 / 2) : a.c)));
   const auto rq = rsrc(uniform((const uint16_t*)(has_codes ? (const void*)(a.codes + t.i0 * 2 * a.J + n0) : a.c)));
   const auto rs = rsrc(uniform((const uint16_t*)(has_codes ? (const void*)(a.scales + t.i0 * 2 * NB + n0 / 32) : a.c)));
   const bool none = group == a.groups;   // rows of no group are zero
@@ -447,7 +449,7 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, int64_t group
   for (int i = 0; i < TI; i++) {
     const uint32_t first = 16u * FrA::tile(wi, i), row = first + lrow;
     const bool ok = in && row < rows;
-    uint32_t H[2][2], G[2][2], U[2][2];
+    uint32_t H[2][2], G[2][2], U[2][2], ng[2], nu[2];
 #pragma unroll
     for (int q = 0; q < 2; q++) {
       float gate[4], up[4], h[4];
@@ -460,14 +462,27 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, int64_t group
 #pragma unroll
       for (int e = 0; e < 2; e++) {
         H[q][e] = pack_bf16(h[2 * e], h[2 * e + 1]);
-        G[q][e] = pack_bf16(gate[2 * e], gate[2 * e + 1]);
-        U[q][e] = pack_bf16(up[2 * e], up[2 * e + 1]);
+        G[q][e] = has_pre ? wide_pair(gate[2 * e], gate[2 * e + 1]) : pack_bf16(gate[2 * e], gate[2 * e + 1]);
+        U[q][e] = has_pre ? wide_pair(up[2 * e], up[2 * e + 1]) : pack_bf16(up[2 * e], up[2 * e + 1]);
       }
+      ng[q] = wide_rests(gate[0], gate[1], gate[2], gate[3]);
+      nu[q] = wide_rests(up[0], up[1], up[2], up[3]);
     }
     put16(through(mine, H), rh, ok ? 2u * (row * ld + col) : kOob);
     if (has_pre) {
       put16(through(mine + 16 * GATED_PITCH, G), rp, ok ? 2u * (row * 2u * N + col) : kOob);
       put16(through(mine + 32 * GATED_PITCH, U), rp, ok ? 2u * (row * 2u * N + N + col) : kOob);
+      uint8_t* at = mine + 48 * GATED_PITCH;
+#pragma unroll
+      for (int q = 0; q < 2; q++) {
+        *reinterpret_cast<uint16_t*>(at + r * REST_PITCH + 8 * q + 2 * g) = (uint16_t)ng[q];
+        *reinterpret_cast<uint16_t*>(at + (16 + r) * REST_PITCH + 8 * q + 2 * g) = (uint16_t)nu[q];
+      }
+      // (read as vectors, which may alias the 16-bit stores)
+      const uint32_t wg = as_u32(*reinterpret_cast<const u16x2*>(at + lrow * REST_PITCH + 4 * (lane & 3u)));
+      const uint32_t wu = as_u32(*reinterpret_cast<const u16x2*>(at + (16 + lrow) * REST_PITCH + 4 * (lane & 3u)));
+      __builtin_amdgcn_raw_buffer_store_b32(wg, rn, ok ? row * N + col / 2u : kOob, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b32(wu, rn, ok ? row * N + N / 2u + col / 2u : kOob, 0, 0);
     }
     if (has_codes) {
       const uint32_t g4[4] = {G[0][0], G[0][1], G[1][0], G[1][1]}, u4[4] = {U[0][0], U[0][1], U[1][0], U[1][1]};

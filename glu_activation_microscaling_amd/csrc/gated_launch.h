@@ -22,7 +22,7 @@ struct GatedLinearArgs {
   uint16_t* h;               // [M, N]
   int64_t ld_h;
   void* pre;                 // [M, 2N] = [gate | up]: BF16 or E4M3 codes
-  uint8_t* scales;           // [M, 2 ceil(N/32)] of the codes
+  uint8_t* extra;            // BF16: [M, N], four more bits of each; codes: scales [M, 2 ceil(N/32)]
   float* work;
 };
 
@@ -36,7 +36,7 @@ struct GatedLinearBwdArgs {
   int64_t ld_x;
   const uint16_t* w;
   const void* pre;
-  const uint8_t* scales;
+  const uint8_t* extra;      // BF16: may be null
   uint16_t* dx;              // [M, K], or null
   int64_t ld_dx;
   uint16_t* dw;              // [groups, 2N, K], or null
@@ -51,8 +51,8 @@ struct GluGradArgs {
   int act, layout;           // layout: of d
   int64_t M, N, groups;
   const int32_t* offsets;    // or null; with sums only
-  const uint16_t* pre;       // BF16 [M, 2N], or null:
-  const uint8_t* q;          // MXFP8 codes [M, 2N] and scales [M, 2 ceil(N/32)]
+  const uint16_t* pre;       // BF16 [M, 2N], s then null or four more bits of each, [M, N]; or null:
+  const uint8_t* q;          // MXFP8 codes [M, 2N] and scales s [M, 2 ceil(N/32)]
   const uint8_t* s;
   const uint16_t* dh;
   int64_t ld_dh;

@@ -88,6 +88,18 @@ __device__ __forceinline__ void restore8(float (&v)[8], u32x2 q, uint32_t scale)
   }
 }
 
+// Eight values from BF16 and four more bits of each.
+__device__ __forceinline__ void widen8(float (&v)[8], u32x4 p, uint32_t rest) {
+  v[0] = wide_value<0>(p[0] << 16, rest);
+  v[1] = wide_value<1>(p[0] & 0xffff0000u, rest);
+  v[2] = wide_value<2>(p[1] << 16, rest);
+  v[3] = wide_value<3>(p[1] & 0xffff0000u, rest);
+  v[4] = wide_value<4>(p[2] << 16, rest);
+  v[5] = wide_value<5>(p[2] & 0xffff0000u, rest);
+  v[6] = wide_value<6>(p[3] << 16, rest);
+  v[7] = wide_value<7>(p[3] & 0xffff0000u, rest);
+}
+
 // grid: (256 columns, group, part of the group's rows); with sums and h, group number `groups` is the
 // rows of no group, whose h is formed too.
 template <int ACT, bool MX, int LAYOUT>
@@ -122,8 +134,15 @@ __global__ __launch_bounds__(256) void k_glu_grad(GluGradArgs a) {
         restore8(g, *reinterpret_cast<const u32x2*>(q), s[0]);
         restore8(u, *reinterpret_cast<const u32x2*>(q + a.N), s[NB]);
       } else {
-        unpack8(g, *reinterpret_cast<const u32x4*>(a.pre + row * 2 * a.N + col));
-        unpack8(u, *reinterpret_cast<const u32x4*>(a.pre + row * 2 * a.N + a.N + col));
+        const uint16_t* p = a.pre + row * 2 * a.N + col;
+        const uint8_t* s = a.s + row * a.N + col / 2;
+        uint32_t rg = 0, ru = 0;
+        if (a.s != nullptr) {
+          rg = *reinterpret_cast<const uint32_t*>(s);
+          ru = *reinterpret_cast<const uint32_t*>(s + a.N / 2);
+        }
+        widen8(g, *reinterpret_cast<const u32x4*>(p), rg);
+        widen8(u, *reinterpret_cast<const u32x4*>(p + a.N), ru);
       }
       if (a.d != nullptr || a.sums != nullptr) {
         unpack8(d, *reinterpret_cast<const u32x4*>(a.dh + row * a.ld_dh + col));

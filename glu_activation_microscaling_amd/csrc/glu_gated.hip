@@ -7,8 +7,8 @@
 // W [groups, 2N, K] holds Wg above Wu, or their rows in turn.  The sums are the tiled product's
 // (ffn_product.h) with gate and up rows of W interleaved by 16 in LDS, so that a lane gets the
 // gate and the up value of the same outputs and the pre-activation need not reach memory.  For the
-// gradient it is kept as BF16, the type the GLU takes its operands in, or as MXFP8 codes of those BF16
-// values; the gradient is that of the GLU at the values kept.  dp is rounded to BF16 for the matrix
+// gradient it is kept as BF16, the type the GLU takes its operands in, with four more bits of each
+// value beside it, or as MXFP8 codes of BF16 values; the gradient is that of the GLU at the values kept.  dp is rounded to BF16 for the matrix
 // cores; dbias sums it unrounded.
 #include "ffn_product.h"
 #include "gated_launch.h"
@@ -34,15 +34,22 @@ __device__ __forceinline__ void finish_gated(const GatedArgs& a, int64_t group, 
   }
   float h[N];
   glu_of<ACT>(h, g, u);
+  const bool wide = a.pre != nullptr;
 #pragma unroll
   for (int e = 0; e < N / 2; e++) {
-    G[e] = pack_bf16(g[2 * e], g[2 * e + 1]);
-    U[e] = pack_bf16(u[2 * e], u[2 * e + 1]);
+    G[e] = wide ? wide_pair(g[2 * e], g[2 * e + 1]) : pack_bf16(g[2 * e], g[2 * e + 1]);
+    U[e] = wide ? wide_pair(u[2 * e], u[2 * e + 1]) : pack_bf16(u[2 * e], u[2 * e + 1]);
   }
   if (n >= a.J) return;
   *reinterpret_cast<bf16_vec<N>*>(a.c + row * a.ld_c + n) = pack_row(h);
-  if (a.pre != nullptr) {
+  if (wide) {
     bf16_vec<N> pg, pu;
+    uint16_t* rest = reinterpret_cast<uint16_t*>(a.rest + row * a.J + n / 2);
+#pragma unroll
+    for (int q = 0; q < N / 4; q++) {
+      rest[q] = (uint16_t)wide_rests(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]);
+      rest[a.J / 4 + q] = (uint16_t)wide_rests(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+    }
 #pragma unroll
     for (int e = 0; e < N / 2; e++) {
       pg[e] = G[e];
@@ -283,8 +290,9 @@ hipError_t launch_gated_linear(const GatedLinearArgs& a, hipStream_t s) {
   p.pre = a.save == SAVE_BF16 ? (uint16_t*)a.pre : nullptr;
   p.work = a.work;
   p.paired = a.w_layout == PAIRED;
+  p.rest = a.extra;
   p.codes = a.save == SAVE_MXFP8 ? (uint8_t*)a.pre : nullptr;
-  p.scales = a.scales;
+  p.scales = a.extra;
   return with_act(a.act, [&](auto A) { return launch_gated<decltype(A)::value>(p, a.save, s); });
 }
 
@@ -302,7 +310,7 @@ hipError_t launch_gated_linear_bwd(const GatedLinearBwdArgs& a, hipStream_t s) {
   g.offsets = sums == nullptr ? nullptr : a.offsets;
   g.pre = a.save == SAVE_BF16 ? (const uint16_t*)a.pre : nullptr;
   g.q = (const uint8_t*)a.pre;
-  g.s = a.scales;
+  g.s = a.extra;
   g.dh = a.dh;
   g.ld_dh = a.ld_dh;
   g.d = dp;

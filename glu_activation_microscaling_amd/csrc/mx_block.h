@@ -19,6 +19,26 @@ __device__ __forceinline__ void glu_of(float (&h)[N], const float (&g)[N], const
   }
 }
 
+// Values kept as BF16 with four more bits beside it (12 significant bits in all), so that gradients
+// taken at them are not less exact than BF16 gradients are anyway: gate and up in BF16 alone move dx and
+// dW by 0.0018 (2-norm, relative), as much as their own rounding does; so kept, by 0.0001.
+// With v' the FP32 bits rounded to 12 significant bits, BF16 is v' rounded to 8 (halves away from zero),
+// and the nibble, taken as -8 .. 7, is v' less it: the next four bits.  NaN keeps its kind: a NaN that
+// comes of BF16 operands has zeros in the low half, which the roundings do not carry out of.
+__device__ __forceinline__ uint32_t wide_pair(float a, float b) {   // two BF16
+  return __builtin_amdgcn_perm(__float_as_uint(b) + 0x8800u, __float_as_uint(a) + 0x8800u, 0x07060302u);
+}
+__device__ __forceinline__ uint32_t wide_rest(float v) { return (__float_as_uint(v) + 0x800u) >> 12 & 15u; }   // a nibble
+// Four nibbles, the first lowest.
+__device__ __forceinline__ uint32_t wide_rests(float a, float b, float c, float d) {
+  return wide_rest(a) | wide_rest(b) << 4 | wide_rest(c) << 8 | wide_rest(d) << 12;
+}
+// The value of BF16 `hi` (in the upper half of a word whose lower half is zero) and nibble I of `rest`.
+template <int I>
+__device__ __forceinline__ float wide_value(uint32_t hi, uint32_t rest) {
+  return __uint_as_float(hi + (uint32_t)((int32_t)(rest << (28 - 4 * I)) >> 28 << 12));
+}
+
 // The largest magnitude of packed BF16 pairs, as a BF16 bit pattern.
 template <int N>
 __device__ __forceinline__ uint32_t top_of(const uint32_t (&p)[N]) {

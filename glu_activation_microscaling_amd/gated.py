@@ -2,8 +2,8 @@
 
 Argument marshalling only, as for the other entry points (C names and formulas in
 include/glu_mx.h); every function is also a name of the package:
-  glu_gated_linear(x, w, bias, act=, w_layout=, offsets=, save=)  -> h, or (h, pre, scales)
-  glu_gated_linear_bwd(dh, x, w, pre, scales, ...)                -> (dx, dw, db, h)
+  glu_gated_linear(x, w, bias, act=, w_layout=, offsets=, save=)  -> h, or (h, pre, extra)
+  glu_gated_linear_bwd(dh, x, w, pre, extra, ...)                -> (dx, dw, db, h)
   glu_fwd_ckpt(gate, up, act=, layout=)                           -> (h, q, s)
   glu_bwd_ckpt(q, s, dh, act=, layout=)                           -> (d, h)
 What is disabled comes back zero-sized (fixed arity).  Scratch memory is a torch allocation of
@@ -49,9 +49,9 @@ def glu_gated_linear(x, w, bias=None, *, act="swiglu", w_layout="split", offsets
     """h = act(x Wg^T + bg) * (x Wu^T + bu), [M, N].  w [2N, K] and bias [2N] hold gates above ups
     (w_layout "split") or in turn ("paired"); with int32 offsets [groups + 1], w is [groups, 2N, K],
     rows offsets[e] .. offsets[e + 1] - 1 of x go through w[e] and bias[e], and rows of no group give
-    zeros.  save="bf16" or "mxfp8" returns (h, pre, scales) with what glu_gated_linear_bwd takes,
-    [gate | up]: BF16 pre [M, 2N] (scales zero-sized), or E4M3 codes [M, 2N] and E8M0 scales [M, 2
-    ceil(N/32)]."""
+    zeros.  save="bf16" or "mxfp8" returns (h, pre, extra) with what glu_gated_linear_bwd takes,
+    [gate | up]: BF16 pre [M, 2N] with four more bits of each value in extra [M, N], or E4M3 codes
+    [M, 2N] with E8M0 scales [M, 2 ceil(N/32)]."""
     a, layout, M, N, K, groups, ld_x = _gated_setup(x, w, bias, offsets, act, w_layout)
     keep = _choice(save, SAVE, "save")
     _same_device(x, w, bias, offsets, out)
@@ -59,35 +59,33 @@ def glu_gated_linear(x, w, bias=None, *, act="swiglu", w_layout="split", offsets
         h, ld_h = x.new_empty((M, N)), N
     else:
         h, ld_h = out, _matrix(out, "out", _BF16, M, N)
-    pre = scales = None
+    pre = extra = None
     if keep:
         pre = x.new_empty((M, 2 * N), dtype=_BF16 if keep == 1 else _U8)
-        scales = x.new_empty((0,) if keep == 1 else (M, _scale_columns(N)), dtype=_U8)
+        extra = x.new_empty((M, N if keep == 1 else _scale_columns(N)), dtype=_U8)
     nbytes = _size("glu_gated_linear_work_bytes", keep, M, N, K, groups, int(offsets is not None))
     work = x.new_empty((nbytes,), dtype=_U8) if nbytes > 0 else None
     _launch(x, "glu_gated_linear", a, layout, keep, M, N, K, groups, _ptr(offsets), _ptr(x), ld_x, _ptr(w), _ptr(bias),
-          _ptr(h), ld_h, _ptr(pre), _ptr(scales), _ptr(work), nbytes)
-    return (h, pre, scales) if keep else h
+          _ptr(h), ld_h, _ptr(pre), _ptr(extra), _ptr(work), nbytes)
+    return (h, pre, extra) if keep else h
 
 
-def glu_gated_linear_bwd(dh, x, w, pre, scales=None, *, act="swiglu", w_layout="split", offsets=None, bias=False,
+def glu_gated_linear_bwd(dh, x, w, pre, extra=None, *, act="swiglu", w_layout="split", offsets=None, bias=False,
                          need_dx=True, need_dw=True, need_h=False):
-    """Gradients of glu_gated_linear from what its save kept (pre, and scales with "mxfp8"), taken at
-    the values kept: (dx [M, K], dw like w, db [2N] or [groups, 2N] in w's order, h [M, N] formed again).
+    """Gradients of glu_gated_linear from what its save kept (pre and extra; BF16 pre may come alone), taken
+    at the values kept: (dx [M, K], dw like w, db [2N] or [groups, 2N] in w's order, h [M, N] formed again).
     bias=True asks for db.  What is not wanted comes back zero-sized."""
     a, layout, M, N, K, groups, ld_x = _gated_setup(x, w, None, offsets, act, w_layout)
     ld_dh = _matrix(dh, "dh", _BF16, M, N)
-    if pre.dtype is _U8:
-        if scales is None:
-            raise ValueError("codes need their scales")
-        keep = 2
-        _like(scales, "scales", _U8, (M, _scale_columns(N)))
-    else:
-        if scales is not None and scales.numel():
-            raise ValueError("scales go with codes, and only with them")
-        keep, scales = 1, None
+    keep = 2 if pre.dtype is _U8 else 1
+    if extra is not None and keep == 1 and extra.numel() == 0:
+        extra = None
+    if extra is not None:
+        _like(extra, "extra", _U8, (M, N if keep == 1 else _scale_columns(N)))
+    elif keep == 2:
+        raise ValueError("codes need their scales")
     _like(pre, "pre", _U8 if keep == 2 else _BF16, (M, 2 * N))
-    _same_device(x, w, dh, pre, scales, offsets)
+    _same_device(x, w, dh, pre, extra, offsets)
     dx = _empty(x, (M, K), _BF16) if need_dx else x.new_empty((0,))
     dw = torch.empty_like(w) if need_dw else x.new_empty((0,))
     db = x.new_empty(w.shape[:-1] if bias else (0,))
@@ -95,7 +93,7 @@ def glu_gated_linear_bwd(dh, x, w, pre, scales=None, *, act="swiglu", w_layout="
     nbytes = _size("glu_gated_linear_bwd_work_bytes", M, N, K, groups, int(offsets is not None), int(bias))
     work = x.new_empty((nbytes,), dtype=_U8) if nbytes > 0 else None
     _launch(x, "glu_gated_linear_bwd", a, layout, keep, M, N, K, groups, _ptr(offsets), _ptr(dh), ld_dh, _ptr(x), ld_x,
-          _ptr(w), _ptr(pre), _ptr(scales), _ptr(dx) if need_dx else None, K, _ptr(dw) if need_dw else None,
+          _ptr(w), _ptr(pre), _ptr(extra), _ptr(dx) if need_dx else None, K, _ptr(dw) if need_dw else None,
           _ptr(db) if bias else None, _ptr(h) if need_h else None, N, _ptr(work), nbytes)
     return dx, dw, db, h
 

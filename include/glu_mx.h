@@ -463,18 +463,22 @@ glu_status glu_moe_combine_bwd(int64_t tokens, int64_t choices, int64_t H, int e
  * activation and product in FP32, rounded once.  offsets and groups as for glu_linear; rows of no
  * group give zero rows of h and of what is kept.
  * What is kept for the backward, [gate | up] whatever w_layout:
- *   GLU_SAVE_BF16 : pre, BF16 [M, 2N].
- *   GLU_SAVE_MXFP8: pre, E4M3 codes [M, 2N], and scales, E8M0 bytes [M, 2 ceil(N/32)], of those
- *                   BF16 values: a checkpoint of glu_fwd_ckpt.
- * Otherwise pre and scales are NULL.  N is a multiple of 8 up to 2^19, K as for glu_linear. */
+ *   GLU_SAVE_BF16 : pre, BF16 [M, 2N], and extra, four more bits of each value, [M, N] bytes: value n of a
+ *                   half in the low (n even) or high nibble of byte n/2 of that half's N/2.  The value
+ *                   kept is the FP32 number whose bits are pre << 16 plus the nibble, taken as -8 .. 7,
+ *                   << 12: 12 significant bits, so that the gradients are as exact as BF16 lets them be.
+ *   GLU_SAVE_MXFP8: pre, E4M3 codes [M, 2N], and extra, their E8M0 scales [M, 2 ceil(N/32)], of the
+ *                   values rounded to BF16: a checkpoint of glu_fwd_ckpt.
+ * Otherwise pre and extra are NULL.  N is a multiple of 8 up to 2^19, K as for glu_linear. */
 enum { GLU_SAVE_NONE = 0, GLU_SAVE_BF16 = 1, GLU_SAVE_MXFP8 = 2 };
 int64_t glu_gated_linear_work_bytes(int save, int64_t M, int64_t N, int64_t K, int64_t groups, int grouped);
 glu_status glu_gated_linear(int act, int w_layout, int save, int64_t M, int64_t N, int64_t K, int64_t groups,
                             const int32_t* offsets, const uint16_t* x, int64_t ld_x, const uint16_t* w,
-                            const uint16_t* bias, uint16_t* h, int64_t ld_h, void* pre, uint8_t* scales, void* work,
+                            const uint16_t* bias, uint16_t* h, int64_t ld_h, void* pre, uint8_t* extra, void* work,
                             int64_t work_bytes, void* stream);
 
-/* dp = [dh u act'(g) | dh act(g)] at the gate and up values kept (GLU_SAVE_BF16 or _MXFP8);
+/* dp = [dh u act'(g) | dh act(g)] at the gate and up values kept (GLU_SAVE_BF16, with which extra may be
+ * NULL: BF16 values alone, or GLU_SAVE_MXFP8);
  * dx = dp W, dw[e] = dp^T x and dbias[e] = sum of dp over the rows of group e.  dx [M, K], dw
  * [groups, 2N, K] and dbias [groups, 2N] in W's order, BF16, each NULL when not wanted; so is h,
  * act(g) u formed again from the values kept (what the next product's weight gradient needs).  Rows
@@ -482,7 +486,7 @@ glu_status glu_gated_linear(int act, int w_layout, int save, int64_t M, int64_t 
 int64_t glu_gated_linear_bwd_work_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, int grouped, int with_bias);
 glu_status glu_gated_linear_bwd(int act, int w_layout, int save, int64_t M, int64_t N, int64_t K, int64_t groups,
                                 const int32_t* offsets, const uint16_t* dh, int64_t ld_dh, const uint16_t* x,
-                                int64_t ld_x, const uint16_t* w, const void* pre, const uint8_t* scales, uint16_t* dx,
+                                int64_t ld_x, const uint16_t* w, const void* pre, const uint8_t* extra, uint16_t* dx,
                                 int64_t ld_dx, uint16_t* dw, uint16_t* dbias, uint16_t* h, int64_t ld_h, void* work,
                                 int64_t work_bytes, void* stream);
 
@@ -576,11 +580,11 @@ glu_status glu_check_moe_combine_bwd(int64_t tokens, int64_t choices, int64_t H,
 
 glu_status glu_check_gated_linear(int act, int w_layout, int save, int64_t M, int64_t N, int64_t K, int64_t groups,
                                   const int32_t* offsets, const uint16_t* x, int64_t ld_x, const uint16_t* w,
-                                  const uint16_t* bias, uint16_t* h, int64_t ld_h, void* pre, uint8_t* scales,
+                                  const uint16_t* bias, uint16_t* h, int64_t ld_h, void* pre, uint8_t* extra,
                                   void* work, int64_t work_bytes);
 glu_status glu_check_gated_linear_bwd(int act, int w_layout, int save, int64_t M, int64_t N, int64_t K, int64_t groups,
                                       const int32_t* offsets, const uint16_t* dh, int64_t ld_dh, const uint16_t* x,
-                                      int64_t ld_x, const uint16_t* w, const void* pre, const uint8_t* scales,
+                                      int64_t ld_x, const uint16_t* w, const void* pre, const uint8_t* extra,
                                       uint16_t* dx, int64_t ld_dx, uint16_t* dw, uint16_t* dbias, uint16_t* h,
                                       int64_t ld_h, void* work, int64_t work_bytes);
 glu_status glu_check_fwd_ckpt(int act, int layout, int64_t M, int64_t N, const uint16_t* gate, const uint16_t* up,

@@ -102,3 +102,11 @@ def restored(q, s, N):
         f = torch.where(sc == 255, float("nan"), torch.exp2(sc.to(D) - 127.0))
         out.append(v[:, h * N:(h + 1) * N] * f)
     return out
+
+
+def widened(pre, extra, N):
+    """[gate, up] in 64 bits from BF16 [M, 2N] and the four more bits of each, [M, N] bytes."""
+    nib = torch.stack([extra & 15, extra >> 4], 2).flatten(1).to(torch.int32)
+    bits = pre.view(torch.int16).to(torch.int32) * 65536 + torch.where(nib > 7, nib - 16, nib) * 4096
+    v = bits.view(torch.float32).to(D)
+    return v[:, :N], v[:, N:]

@@ -49,9 +49,11 @@ def check(gpu, t, act="swiglu", layout="split", save="bf16", offsets=None, bias=
     h2, pre, scales = gpu.glu_gated_linear(t["x"], t["w"], b, save=save, **p)
     close("h beside what is kept", h2, h, eh)
     if save == "bf16":
-        close("gate", pre[:, :N], g, eg)
-        close("up", pre[:, N:], u, eu)
-        kg, ku = pre[:, :N], pre[:, N:]
+        kg, ku = ref.widened(pre, scales, N)
+        for name, v, e, k, b16 in (("gate", g, eg, kg, pre[:, :N]), ("up", u, eu, ku, pre[:, N:])):
+            # 12 significant bits, and BF16 the nearest to that (2^-8 of it at most)
+            assert ((k - v).abs() <= 2.0 ** -12 * v.abs() + 1.01 * e + 2.0 ** -120).all(), name
+            assert ((b16.to(D) - k).abs() <= BF16_HALF_ULP * k.abs() + 2.0 ** -120).all(), name
     else:
         # the codes are those of BF16 values within rounding of the exact ones
         kg, ku = ref.restored(pre, scales, N)
@@ -117,7 +119,7 @@ def test_groups(gpu, counts, after, N, K, save):
         want[M - after:], err[M - after:] = 0.0, 0.0
         close("h", h, want, err)
         dx, dw, db, again = gpu.glu_gated_linear_bwd(t["dh"], x, t["w"], pre, scales, bias=True, need_h=True, **p)
-        kg, ku = (pre[:, :N], pre[:, N:]) if save == "bf16" else ref.restored(pre, scales, N)
+        kg, ku = ref.widened(pre, scales, N) if save == "bf16" else ref.restored(pre, scales, N)
         d0 = t["dh"].nan_to_num(0.0, 0.0, 0.0)
         ref_bwd = ref.backward(d0, t["x"], t["w"], kg, ku, "geglu", layout, off)
         for name, a, terms in zip(("dx", "dw", "db"), (dx, dw, db), (2 * N, M, M)):
@@ -164,6 +166,20 @@ def test_lengths_of_zero(gpu):
         assert h.shape == (M, 0)
         dx, dw, db, _ = gpu.glu_gated_linear_bwd(t["dh"], t["x"], t["w"], pre, bias=True)
         assert (dx == 0).all() and dw.shape == (0, 64) and db.shape == (0,)
+
+
+def test_bf16_values_alone(gpu):
+    """Gate and up from elsewhere, without the four bits."""
+    t = draw(130, 72, 136)
+    pre = (torch.randn(130, 144, device="cuda") * 2).to(BF16)
+    got = gpu.glu_gated_linear_bwd(t["dh"], t["x"], t["w"], pre, bias=True, need_h=True)
+    same = gpu.glu_gated_linear_bwd(t["dh"], t["x"], t["w"], pre, torch.zeros(130, 72, dtype=torch.uint8, device="cuda"),
+                                    bias=True, need_h=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, same))
+    da, db = gpu.glu_bwd(pre[:, :72], pre[:, 72:], t["dh"])
+    dx, dw, _ = gpu.glu_linear_bwd(torch.cat([da, db], 1), t["x"], t["w"])
+    assert torch.equal(got[0], dx) and torch.equal(got[1], dw)
+    assert torch.equal(got[3], gpu.glu_fwd(pre[:, :72], pre[:, 72:]))
 
 
 def test_only_what_is_wanted(gpu):
