@@ -17,6 +17,7 @@ namespace glu {
 namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr uint32_t CODES = 128;   // codes a step, one line of an operand row and one block of scales
 
@@ -34,94 +35,154 @@ __device__ __forceinline__ v8i join16(u32x4 a, u32x4 b) {
   return (v8i){(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
+// What a workgroup works on: rows t.i0 .. of group `group`, columns j0 .. of a tile, steps s0 .. s1 - 1.
+struct Fp8Tile {
+  RowTile t;
+  bool none;                 // rows of no group: zeros
+  uint32_t part, s0, s1, rows, cols;
+  int64_t j0;
+};
+// Tile of this workgroup: contiguous runs per XCD, down GROUP_I row tiles before the next column tile.
+// False when there is none (the grid allows for more row tiles than groups may have).
+template <int BI, int BJ>
+__device__ __forceinline__ bool fp8_tile(Fp8Tile& o, const Fp8Args& a, uint32_t tiles_i, uint32_t tiles_j, uint32_t splits) {
+  if (a.offsets != nullptr) {
+    tiles_i = count_tiles(a.offsets, a.groups, a.I, BI);
+    if (blockIdx.x >= tiles_i * tiles_j) return false;
+  }
+  const uint32_t per = tiles_i * tiles_j;
+  uint32_t b = xcd_run(blockIdx.x, a.offsets != nullptr ? per : gridDim.x);
+  o.part = b / per;
+  b -= o.part * per;
+  const uint32_t in_group = GROUP_I * tiles_j, first_i = b / in_group * GROUP_I;
+  const uint32_t gi = min(tiles_i - first_i, GROUP_I);
+  o.t = find_tile(a.offsets, a.groups, a.I, first_i + b % in_group % gi, BI);
+  if (o.t.group < 0) return false;
+  o.none = o.t.group == a.groups;
+  o.s0 = 0;
+  o.s1 = o.none ? 0u : (uint32_t)a.blocks;
+  if (splits > 1) {
+    o.s0 = part_begin((uint32_t)a.blocks, o.part, splits);
+    o.s1 = part_begin((uint32_t)a.blocks, o.part + 1, splits);
+  }
+  o.j0 = (int64_t)(b % in_group / gi) * BJ;
+  o.rows = (uint32_t)(o.t.i1 - o.t.i0);
+  o.cols = (uint32_t)min((int64_t)BJ, a.J - o.j0);
+  return true;
+}
+
+// Copies of scales into LDS: one for each of SA rows of A (the tile's rows filled up to whole loads of
+// 64), then one for each column of the tile; every wave makes LOADS loads of 64.
+template <int W_SCALES, int BI, int BJ, int WAVES>
+struct Fp8Scales {
+  static constexpr uint32_t SA = BI < 64 ? 64 : BI, ROWS = SA + BJ;
+  static constexpr int LOADS = (ROWS / 64 + WAVES - 1) / WAVES;
+  static constexpr uint32_t BYTES = 256u * LOADS * WAVES;
+  uint32_t off[LOADS];
+  const float *xs, *ws;
+  int64_t x_step, w_step;    // from one block of the sum to the next
+  __device__ __forceinline__ void init(const Fp8Args& a, const Fp8Tile& o, uint32_t wave, uint32_t lane) {
+    const int64_t group = o.none ? 0 : o.t.group;
+    constexpr bool BLOCK = W_SCALES == FP8_W_BLOCK;
+    xs = a.xs + o.t.i0;
+    ws = BLOCK ? a.ws + (group * ((a.J + 127) / 128) + o.j0 / 128) * a.blocks : a.ws + group * a.blocks * a.J + o.j0;
+    x_step = a.I;
+    w_step = BLOCK ? 1 : a.J;
+#pragma unroll
+    for (int q = 0; q < LOADS; q++) {
+      const uint32_t at = 64u * (wave * LOADS + q) + lane, j = at - SA;
+      if (at < SA) off[q] = at < o.rows ? 4u * at : kOob;
+      else off[q] = j < o.cols ? 4u * (BLOCK ? (uint32_t)((o.j0 + j) / 128 - o.j0 / 128) * (uint32_t)a.blocks : j) : kOob;
+    }
+  }
+  // of block s of the sum, when there is one, to LDS at `to`
+  __device__ __forceinline__ void issue(uint32_t s, bool live, uint8_t* to, uint32_t wave) const {
+#pragma unroll
+    for (int q = 0; q < LOADS; q++) {
+      const uint32_t first = 64u * (wave * LOADS + q);
+      const float* base = first < SA ? xs + (live ? s : 0) * x_step : ws + (live ? s : 0) * w_step;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(uniform((const uint16_t*)base)), (lds_ptr)(to + 4u * first), 4,
+                                               live && first < ROWS ? off[q] : kOob, 0, 0, 0);
+    }
+  }
+};
+
+// Stores a wave's sums: `row tiles` of R rows by C columns, from its piece of LDS as eight consecutive
+// columns a lane, with bias and residual.  `put(i, piece)` writes row tile i, R rows PITCH floats apart.
+template <int R, int C, int TILES, typename Put>
+__device__ __forceinline__ void fp8_store(const Fp8Args& a, const Fp8Tile& o, uint32_t row0, uint32_t col0, uint32_t lane,
+                                          float* piece, Put&& put) {
+  constexpr uint32_t PITCH = C + 4, CH = C / 8, ROWS = 64 / CH, PASSES = R / ROWS;
+  const uint32_t cc = 8u * (lane % CH), lrow = lane / CH, col = col0 + cc;
+  const bool bias_of = !o.none && a.bias != nullptr, residual = !o.none && a.residual != nullptr;
+  const auto rc = rsrc(uniform(a.c + o.t.i0 * a.ld_c + o.j0));
+  const auto rr = rsrc(uniform(residual ? a.residual + o.t.i0 * a.ld_res + o.j0 : a.c));
+  float bias[8];
+  load_bf16(bias, bias_of && col < o.cols ? a.bias + o.t.group * a.J + o.j0 + col : nullptr);
+#pragma unroll
+  for (int i = 0; i < TILES; i++) {
+    put(i, piece);
+#pragma unroll
+    for (uint32_t p = 0; p < PASSES; p++) {
+      const float* q = piece + (ROWS * p + lrow) * PITCH + cc;
+      const v4f lo = *reinterpret_cast<const v4f*>(q), hi = *reinterpret_cast<const v4f*>(q + 4);
+      const uint32_t row = row0 + R * i + ROWS * p + lrow;
+      const bool ok = row < o.rows && col < o.cols;
+      u32x4 res = (u32x4)0u;
+      if (residual) res = __builtin_amdgcn_raw_buffer_load_b128(rr, ok ? 2u * (row * (uint32_t)a.ld_res + col) : kOob, 0, 0);
+      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+      for (int e = 0; e < 8; e++) v[e] = v[e] + bias[e] + (e % 2 == 0 ? bf_lo(res[e / 2]) : bf_hi(res[e / 2]));
+      put16(pack_row(v), rc, ok ? 2u * (row * (uint32_t)a.ld_c + col) : kOob);
+    }
+  }
+}
+
 // WI x WJ waves of TI x TJ tiles of 16 x 16 each, NS stages of one block of the sum in LDS, filled by
-// direct copies NS - 1 blocks ahead.  A stage ends with its scales: one for each row of A, then one for
-// each row of B.
+// direct copies NS - 1 blocks ahead.
 template <int W_SCALES, int WI, int WJ, int TI, int TJ, int NS>
 __global__ __launch_bounds__(64 * WI * WJ) void k_fp8_product(Fp8Args a, uint32_t tiles_i, uint32_t tiles_j,
                                                               uint32_t splits) {
   constexpr int BI = 16 * WI * TI, BJ = 16 * WJ * TJ, WAVES = WI * WJ;
   using OpA = Operand<false, BI, WAVES>;
   using OpB = Operand<false, BJ, WAVES>;
-  constexpr uint32_t SA = BI < 64 ? 64 : BI, SROWS = SA + BJ;                  // scales: whole loads of 64 rows
-  constexpr int SLOADS = (SROWS / 64 + WAVES - 1) / WAVES, LOADS = OpA::LOADS + OpB::LOADS + SLOADS;
-  constexpr uint32_t S_OFF = OpA::BYTES + OpB::BYTES, STAGE = S_OFF + 256u * SLOADS * WAVES;
+  using Scales = Fp8Scales<W_SCALES, BI, BJ, WAVES>;
+  constexpr int LOADS = OpA::LOADS + OpB::LOADS + Scales::LOADS;
+  constexpr uint32_t S_OFF = OpA::BYTES + OpB::BYTES, STAGE = S_OFF + Scales::BYTES;
   static_assert(NS * STAGE <= 160 * 1024);
   __shared__ __attribute__((aligned(16))) uint8_t smem[NS * STAGE];
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-
-  if (a.offsets != nullptr) {   // the grid allows for more row tiles than there are
-    tiles_i = count_tiles(a.offsets, a.groups, a.I, BI);
-    if (blockIdx.x >= tiles_i * tiles_j) return;
-  }
-  const uint32_t per = tiles_i * tiles_j;
-  uint32_t b = xcd_run(blockIdx.x, a.offsets != nullptr ? per : gridDim.x);
-  const uint32_t part = b / per;
-  b -= part * per;
-  const uint32_t in_group = GROUP_I * tiles_j, first_i = b / in_group * GROUP_I;
-  const uint32_t gi = min(tiles_i - first_i, GROUP_I);
-  const uint32_t ti = first_i + b % in_group % gi, tj = b % in_group / gi;
-  const RowTile t = find_tile(a.offsets, a.groups, a.I, ti, BI);
-  if (t.group < 0) return;
-  const int64_t group = t.group;
-  const bool none = group == a.groups;   // rows of no group
-  uint32_t s0 = 0, s1 = none ? 0u : (uint32_t)a.blocks;   // steps
-  if (splits > 1) {
-    s0 = part_begin((uint32_t)a.blocks, part, splits);
-    s1 = part_begin((uint32_t)a.blocks, part + 1, splits);
-  }
-  const uint32_t k1 = (uint32_t)a.K;
-  const int64_t j0 = (int64_t)tj * BJ, j1 = min(j0 + BJ, a.J);
+  Fp8Tile o;
+  if (!fp8_tile<BI, BJ>(o, a, tiles_i, tiles_j, splits)) return;
+  const uint32_t s0 = o.s0, s1 = o.s1, k1 = (uint32_t)a.K;
   const uint32_t wi = wave / WJ, wj = wave % WJ, g = lane >> 4, r = lane & 15u;
-  const uint32_t rows = (uint32_t)(t.i1 - t.i0), cols = (uint32_t)(j1 - j0);
 
   OpA oa;
   OpB ob;
-  oa.init(a.a, a.ld_a, t.i0, t.i1, wave, lane);
-  ob.init(none ? a.b : a.b + group * a.b_group, a.ld_b, j0, j1, wave, lane);
+  Scales os;
+  oa.init(a.a, a.ld_a, o.t.i0, o.t.i1, wave, lane);
+  ob.init(o.none ? a.b : a.b + o.t.group * a.b_group, a.ld_b, o.j0, o.j0 + o.cols, wave, lane);
+  os.init(a, o, wave, lane);
   Fragments<false, BI, WI, TI> fa;
   Fragments<false, BJ, WJ, TJ> fb;
   fa.init(wi, lane);
   fb.init(wj, lane);
-  // scale loads: load q of this wave is rows 64 (wave SLOADS + q) ..
-  const int64_t gb = none ? 0 : group;
-  const float* const wsb = W_SCALES == FP8_W_BLOCK ? a.ws + (gb * ((a.J + 127) / 128) + j0 / 128) * a.blocks
-                                                   : a.ws + gb * a.blocks * a.J + j0;
-  uint32_t so[SLOADS];
-#pragma unroll
-  for (int q = 0; q < SLOADS; q++) {
-    const uint32_t at = 64u * (wave * SLOADS + q) + lane;
-    if (at < SA) {
-      so[q] = at < rows ? 4u * at : kOob;
-    } else {
-      const uint32_t j = at - SA;
-      so[q] = j < cols ? 4u * (W_SCALES == FP8_W_BLOCK ? (uint32_t)((j0 + j) / 128 - j0 / 128) * (uint32_t)a.blocks : j) : kOob;
-    }
-  }
-  auto issue = [&](uint32_t s, uint32_t at) {   // of step s into the stage at byte `at`; past the end zeros
+  auto issue = [&](uint32_t s, uint8_t* to) {   // of step s; past the end zeros
     const bool live = s < s1;
     const uint32_t k = live ? s * (CODES / 2) : k1;
     if (k + BK <= k1) {
 #pragma unroll
-      for (int q = 0; q < OpA::LOADS; q++) oa.template issue<false>(q, k, k1, smem + at, wave, lane);
+      for (int q = 0; q < OpA::LOADS; q++) oa.template issue<false>(q, k, k1, to, wave, lane);
 #pragma unroll
-      for (int q = 0; q < OpB::LOADS; q++) ob.template issue<false>(q, k, k1, smem + at + OpA::BYTES, wave, lane);
+      for (int q = 0; q < OpB::LOADS; q++) ob.template issue<false>(q, k, k1, to + OpA::BYTES, wave, lane);
     } else {
 #pragma unroll
-      for (int q = 0; q < OpA::LOADS; q++) oa.template issue<true>(q, k, k1, smem + at, wave, lane);
+      for (int q = 0; q < OpA::LOADS; q++) oa.template issue<true>(q, k, k1, to, wave, lane);
 #pragma unroll
-      for (int q = 0; q < OpB::LOADS; q++) ob.template issue<true>(q, k, k1, smem + at + OpA::BYTES, wave, lane);
+      for (int q = 0; q < OpB::LOADS; q++) ob.template issue<true>(q, k, k1, to + OpA::BYTES, wave, lane);
     }
-#pragma unroll
-    for (int q = 0; q < SLOADS; q++) {
-      const uint32_t first = 64u * (wave * SLOADS + q);
-      const float* base = first < SA ? a.xs + (live ? s : 0) * a.I + t.i0
-                                     : wsb + (live ? s : 0) * (W_SCALES == FP8_W_BLOCK ? 1 : a.J);
-      const auto rs = rsrc(uniform((const uint16_t*)base));
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(smem + at + S_OFF + 4u * first), 4,
-                                               live && first < SROWS ? so[q] : kOob, 0, 0, 0);
-    }
+    os.issue(s, live, to + S_OFF, wave);
   };
 
   v4f acc[TI][TJ];
@@ -129,41 +190,38 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_fp8_product(Fp8Args a, uint32_
   for (int i = 0; i < TI; i++)
 #pragma unroll
     for (int j = 0; j < TJ; j++) acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+  auto frag = [&](const uint8_t* at, const uint32_t (&p)[2], int i) {
+    return join16(*reinterpret_cast<const u32x4*>(at + p[0] + 2048u * i), *reinterpret_cast<const u32x4*>(at + p[1] + 2048u * i));
+  };
 
   if (s0 < s1) {
 #pragma unroll
-    for (int q = 0; q < NS - 1; q++) issue(s0 + q, q * STAGE);
+    for (int q = 0; q < NS - 1; q++) issue(s0 + q, smem + q * STAGE);
     uint32_t now = 0;
     for (uint32_t s = s0; s < s1; s++) {
       wait_vm<(NS - 2) * LOADS>();
       lds_barrier();   // every wave's loads of this step have landed, and the step before has been read
-      issue(s + NS - 1, now == 0 ? (NS - 1) * STAGE : now - STAGE);
+      issue(s + NS - 1, smem + (now == 0 ? (NS - 1) * STAGE : now - STAGE));
       const uint8_t *const pa = smem + now, *const pb = pa + OpA::BYTES;
       const float* const sc = reinterpret_cast<const float*>(pa + S_OFF);
       v8i xb[TJ];
       v4f sw[TJ];
 #pragma unroll
-      for (int j = 0; j < TJ; j++)
-        xb[j] = join16(*reinterpret_cast<const u32x4*>(pb + fb.at[0] + 2048u * j), *reinterpret_cast<const u32x4*>(pb + fb.at[1] + 2048u * j));
-      if constexpr (W_SCALES == FP8_W_BLOCK) {
-        // a wave's columns are 16 TJ <= 64 of one block, j0 being a multiple of 64 or of the tile
-        sw[0] = (v4f)sc[SA + 16 * TJ * wj];
-      } else {
+      for (int j = 0; j < TJ; j++) xb[j] = frag(pb, fb.at, j);
+      // by blocks a wave's columns, 16 TJ <= 64, are of one block, j0 being a multiple of the tile
 #pragma unroll
-        for (int j = 0; j < TJ; j++) sw[j] = *reinterpret_cast<const v4f*>(sc + SA + 16 * (TJ * wj + j) + 4 * g);
-      }
+      for (int j = 0; j < TJ; j++)
+        sw[j] = W_SCALES == FP8_W_BLOCK ? (v4f)sc[Scales::SA + 16 * TJ * wj]
+                                        : *reinterpret_cast<const v4f*>(sc + Scales::SA + 16 * (TJ * wj + j) + 4 * g);
 #pragma unroll
       for (int i = 0; i < TI; i++) {
-        const v8i xa = join16(*reinterpret_cast<const u32x4*>(pa + fa.at[0] + 2048u * i), *reinterpret_cast<const u32x4*>(pa + fa.at[1] + 2048u * i));
+        const v8i xa = frag(pa, fa.at, i);
         const float sx = sc[16 * (TI * wi + i) + r];
 #pragma unroll
         for (int j = 0; j < TJ; j++) {
           const v4f p = product128(xb[j], xa);
 #pragma unroll
-          for (int e = 0; e < 4; e++) {
-            const float f = sx * (W_SCALES == FP8_W_BLOCK ? sw[0][0] : sw[j][e]);
-            acc[i][j][e] = __builtin_fmaf(p[e], f, acc[i][j][e]);
-          }
+          for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(p[e], sx * sw[j][e], acc[i][j][e]);
         }
       }
       now = now == (NS - 1) * STAGE ? 0u : now + STAGE;
@@ -173,44 +231,213 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_fp8_product(Fp8Args a, uint32_
   }
 
   if (splits > 1) {
-    const auto rw = rsrc(uniform((const uint16_t*)(a.work + ((int64_t)part * a.I + t.i0) * a.J + j0)));
+    const auto rw = rsrc(uniform((const uint16_t*)(a.work + ((int64_t)o.part * a.I + o.t.i0) * a.J + o.j0)));
 #pragma unroll
     for (int i = 0; i < TI; i++)
 #pragma unroll
       for (int j = 0; j < TJ; j++) {
         const uint32_t row = 16u * (TI * wi + i) + r, col = 16u * (TJ * wj + j) + 4u * g;
-        put16(__builtin_bit_cast(u32x4, acc[i][j]), rw, row < rows && col < cols ? 4u * (row * (uint32_t)a.J + col) : kOob);
+        put16(__builtin_bit_cast(u32x4, acc[i][j]), rw, row < o.rows && col < o.cols ? 4u * (row * (uint32_t)a.J + col) : kOob);
       }
     return;
   }
-  // a row tile's sums through the wave's piece of LDS into eight consecutive columns a lane
-  constexpr uint32_t PITCH = 16 * TJ + 4, CH = 2 * TJ, ROWS = 64 / CH, PASSES = 16 / ROWS;
+  constexpr uint32_t PITCH = 16 * TJ + 4;
   static_assert(WAVES * 16 * PITCH * 4 <= sizeof(smem));
-  float* const mine = reinterpret_cast<float*>(smem) + wave * (16 * PITCH);
-  const uint32_t cc = 8u * (lane % CH), lrow = lane / CH, col = 16u * TJ * wj + cc;
-  const auto rc = rsrc(uniform(a.c + t.i0 * a.ld_c + j0));
-  const auto rr = rsrc(uniform(a.residual != nullptr ? a.residual + t.i0 * a.ld_res + j0 : a.c));
-  float bias[8];
-  load_bf16(bias, !none && col < cols && a.bias != nullptr ? a.bias + group * a.J + j0 + col : nullptr);
+  fp8_store<16, 16 * TJ, TI>(a, o, 16u * TI * wi, 16u * TJ * wj, lane, reinterpret_cast<float*>(smem) + wave * (16 * PITCH),
+                             [&](int i, float* piece) {
 #pragma unroll
-  for (int i = 0; i < TI; i++) {
+    for (int j = 0; j < TJ; j++) *reinterpret_cast<v4f*>(piece + r * PITCH + 16 * j + 4 * g) = acc[i][j];
+  });
+}
+
+// The largest tile, 256 x 256, 8 waves of 128 x 64 as 4 x 2 tiles of 32 x 32.
+//
+// Waves 0 .. 3 (one a SIMD) read a step's fragments while waves 4 .. 7 multiply, and the other way round;
+// each turn ends with a barrier.  The first half reads step s in turn 2 s and multiplies in turn 2 s + 1, the
+// second half one turn later.  Starting loads takes a wave a while (the CU takes some 45 bytes a clock), so
+// that is done in the reading turns alone, and each half has two turns to see its loads landed:
+//   the first half starts in turn 2 s the loads of step s + 1 of its own rows of A and of the low columns
+//     of B (both halves have read step s - 1 of those by the end of turn 2 s - 1: two stages);
+//   the second half in turn 2 s + 1 those of step s + 1 of its own rows of A, which it reads in turn 2 s + 3,
+//     and of step s + 2 of the high columns of B, which the first half reads in turn 2 s + 4: three stages.
+// Registers hold B's fragments and half of A's; the others are read while multiplying.
+//
+// Beside a 16 x 16 x 128 product the vector unit has time for the four additions it needs, and little
+// else: the scales are read and multiplied in the reading turn.
+template <int W_SCALES>
+__global__ __launch_bounds__(512) void k_fp8_turns(Fp8Args a, uint32_t tiles_i, uint32_t tiles_j, uint32_t splits) {
+  constexpr int BI = 256, BJ = 256, WAVES = 8, TI = 8, TJ = 4;
+  constexpr bool BLOCK = W_SCALES == FP8_W_BLOCK;
+  using Op = Operand<false, 256, WAVES>;
+  using Scales = Fp8Scales<W_SCALES, BI, BJ, WAVES>;
+  static_assert(Op::LOADS == 4 && Scales::LOADS == 1);
+  // A: two stages of both halves' rows; B's low columns: two, high columns: three; the scales likewise
+  constexpr uint32_t HALF = Op::BYTES / 2, B_LOW = 4 * HALF, B_HIGH = 6 * HALF, S_ROWS = 9 * HALF, S_COLS = S_ROWS + 2048u;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[S_COLS + 3072u];
+  static_assert(sizeof(smem) <= 160 * 1024);
+  const uint32_t lane = threadIdx.x & 63u;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Fp8Tile o;
+  if (!fp8_tile<BI, BJ>(o, a, tiles_i, tiles_j, splits)) return;
+  const uint32_t s0 = o.s0, s1 = o.s1, k1 = (uint32_t)a.K;
+  const uint32_t wi = wave / 4u, wj = wave % 4u, r = lane & 15u, g = lane >> 4;
+
+  Op oa, ob;
+  Scales os;
+  oa.init(a.a, a.ld_a, o.t.i0, o.t.i1, wave, lane);
+  ob.init(o.none ? a.b : a.b + o.t.group * a.b_group, a.ld_b, o.j0, o.j0 + o.cols, wave, lane);
+  os.init(a, o, wave, lane);
+  auto third = [](uint32_t n) { return n - 3u * (n * 0xaaabu >> 17); };   // n % 3, n < 2^15
+  // The wave's loads of one operand for step s, four blocks of 1 KiB; past the end zeros.  No branch.
+  auto load = [&](const Op& op, uint32_t s, uint8_t* to) {
+    const uint32_t k = s < s1 ? s * (CODES / 2) : k1;
+    const auto from = rsrc(op.base + k);
+    const uint32_t mine = 8u * ((lane & 7u) ^ (lane >> 4));   // first pair of codes in even blocks; in odd ones ^ 32
+    const bool in[2] = {k + mine < k1, k + (mine ^ 32u) < k1};
 #pragma unroll
-    for (int j = 0; j < TJ; j++) *reinterpret_cast<v4f*>(mine + r * PITCH + 16 * j + 4 * g) = acc[i][j];
+    for (int q = 0; q < 4; q++)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr)(to + 4096u * (wave % 4u) + 1024u * q), 16,
+                                               in[q % 2] ? op.off[q] : kOob, 0, 0, 0);
+  };
+  auto load_a = [&](uint32_t s) { load(oa, s, smem + (s - s0) % 2u * (2 * HALF) + wave / 4u * HALF); };
+  auto load_low = [&](uint32_t s) {     // B and the rows' scales; waves 0 .. 3
+    load(ob, s, smem + B_LOW + (s - s0) % 2u * HALF);
+    os.issue(s, s < s1, smem + S_ROWS + (s - s0) % 2u * 1024u, wave);
+  };
+  auto load_high = [&](uint32_t s) {    // B and the columns' scales; waves 4 .. 7
+    load(ob, s, smem + B_HIGH + third(s - s0) * HALF);
+    os.issue(s, s < s1, smem + S_COLS + third(s - s0) * 1024u - 1024u, wave);
+  };
+
+  v4f acc[TI][TJ];
 #pragma unroll
-    for (uint32_t p = 0; p < PASSES; p++) {
-      const float* q = mine + (ROWS * p + lrow) * PITCH + cc;
-      const v4f lo = *reinterpret_cast<const v4f*>(q), hi = *reinterpret_cast<const v4f*>(q + 4);
-      const uint32_t row = 16u * (TI * wi + i) + ROWS * p + lrow;
-      const bool ok = row < rows && col < cols;
-      u32x4 res = (u32x4)0u;
-      if (a.residual != nullptr && !none)
-        res = __builtin_amdgcn_raw_buffer_load_b128(rr, ok ? 2u * (row * (uint32_t)a.ld_res + col) : kOob, 0, 0);
-      float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  for (int i = 0; i < TI; i++)
 #pragma unroll
-      for (int e = 0; e < 8; e++) v[e] = v[e] + bias[e] + (e % 2 == 0 ? bf_lo(res[e / 2]) : bf_hi(res[e / 2]));
-      put16(pack_row(v), rc, ok ? 2u * (row * (uint32_t)a.ld_c + col) : kOob);
+    for (int j = 0; j < TJ; j++) acc[i][j] = (v4f)0.0f;
+
+  // lane r + 16 g holds chunks g and g + 4 of row r of a fragment, kept at chunk ^ (row / 2 % 8)
+  uint32_t at[2];
+#pragma unroll
+  for (uint32_t c = 0; c < 2; c++) at[c] = 128u * r + 16u * ((4u * c + g) ^ ((r >> 1) & 7u));
+  auto frag = [&](const uint8_t* p, int tile) {
+    return join16(*reinterpret_cast<const u32x4*>(p + at[0] + 2048u * tile),
+                  *reinterpret_cast<const u32x4*>(p + at[1] + 2048u * tile));
+  };
+
+  if (s0 < s1) {
+    enum { G_VALU = 0x2, G_MFMA = 0x8, G_DS_READ = 0x100 };   // the scheduler's groups
+    load_a(s0);
+    if (wi == 0) {
+      load_low(s0);
+    } else {
+      load_high(s0);
+      load_high(s0 + 1);
     }
+    wait_vm<0>();
+    lds_barrier();
+    auto turns = [&](auto SECOND) {
+    constexpr bool second = decltype(SECOND)::value;
+    if (second) lds_barrier();
+    for (uint32_t s = s0; s < s1; s++) {
+      const uint32_t n = s - s0;
+      load_a(s + 1);
+      if (second) load_high(s + 2);
+      else load_low(s + 1);
+      const uint8_t *const pa = smem + n % 2u * (2 * HALF) + wi * HALF;
+      const uint8_t *const pb = smem + (wj < 2u ? B_LOW + n % 2u * HALF : B_HIGH + third(n) * HALF) + wj % 2u * 8192u;
+      const float* const sr = reinterpret_cast<const float*>(smem + S_ROWS + n % 2u * 1024u);
+      const float* const sc = reinterpret_cast<const float*>(smem + S_COLS + third(n) * 1024u);
+      v8i xa[4], xb[TJ];
+      float f[TI];             // row scales; by blocks times the columns'
+      v4f sw[BLOCK ? 1 : TJ];  // columns 16 j + 4 g .. + 3
+#pragma unroll
+      for (int i = 0; i < TI; i++) f[i] = sr[128u * wi + 16u * i + r];
+      if constexpr (BLOCK) {
+        const float w = sc[64u * wj];   // a wave's 64 columns are of one block
+#pragma unroll
+        for (int i = 0; i < TI; i++) f[i] *= w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < TJ; j++) sw[j] = *reinterpret_cast<const v4f*>(sc + 64u * wj + 16u * j + 4u * g);
+      }
+#pragma unroll
+      for (int j = 0; j < TJ; j++) xb[j] = frag(pb, j);
+#pragma unroll
+      for (int i = 0; i < 4; i++) xa[i] = frag(pa, i);
+#pragma unroll
+      for (int i = 0; i < TI; i++) asm volatile("" : "+v"(f[i]));   // read and multiplied in this turn
+      __builtin_amdgcn_sched_barrier(0);
+      lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int i = 0; i < TI; i++) {
+        const v8i x = xa[i % 4];
+#pragma unroll
+        for (int j = 0; j < TJ; j++) {
+          const v4f p = product128(xb[j], x);
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            acc[i][j][e] = __builtin_fmaf(p[e], BLOCK ? f[i] : f[i] * sw[BLOCK ? 0 : j][e], acc[i][j][e]);
+        }
+        if (i < 4) xa[i] = frag(pa, 4 + i);
+      }
+      // the additions stay in this turn
+#pragma unroll
+      for (int i = 0; i < TI; i++)
+        asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
+      constexpr int ADDS = BLOCK ? 4 : 8;
+      __builtin_amdgcn_sched_group_barrier(G_MFMA, 3, 0);
+#pragma unroll
+      for (int q = 0; q < 4; q++) {   // the fragments just done with give way to those of the high rows
+        __builtin_amdgcn_sched_group_barrier(G_VALU, ADDS, 0);
+        __builtin_amdgcn_sched_group_barrier(G_MFMA, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(G_DS_READ, 2, 0);
+#pragma unroll
+        for (int u = 0; u < 3; u++) {
+          __builtin_amdgcn_sched_group_barrier(G_VALU, ADDS, 0);
+          __builtin_amdgcn_sched_group_barrier(G_MFMA, 1, 0);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < TI * TJ - 19; q++) {
+        __builtin_amdgcn_sched_group_barrier(G_VALU, ADDS, 0);
+        __builtin_amdgcn_sched_group_barrier(G_MFMA, 1, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(G_VALU, 3 * ADDS, 0);
+      __builtin_amdgcn_s_setprio(0);
+      wait_vm<0>();
+      __builtin_amdgcn_sched_barrier(0);
+      lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (!second) lds_barrier();
+    };
+    if (wave >= WAVES / 2) turns(std::true_type{});
+    else turns(std::false_type{});
+    wait_vm<0>();
+    lds_barrier();   // the stages hold the sums next
   }
+
+  // acc[i][j][e] is row 16 i + r and column 16 j + 4 g + e of the wave's
+  if (splits > 1) {
+    const auto rw = rsrc(uniform((const uint16_t*)(a.work + ((int64_t)o.part * a.I + o.t.i0) * a.J + o.j0)));
+#pragma unroll
+    for (int i = 0; i < TI; i++)
+#pragma unroll
+      for (int j = 0; j < TJ; j++) {
+        const uint32_t row = 128u * wi + 16u * i + r, col = 64u * wj + 16u * j + 4u * g;
+        put16(__builtin_bit_cast(u32x4, acc[i][j]), rw, row < o.rows && col < o.cols ? 4u * (row * (uint32_t)a.J + col) : kOob);
+      }
+    return;
+  }
+  constexpr uint32_t PITCH = 64 + 4;
+  static_assert(WAVES * 16 * PITCH * 4 <= sizeof(smem));
+  fp8_store<16, 64, TI>(a, o, 128u * wi, 64u * wj, lane, reinterpret_cast<float*>(smem) + wave * (16 * PITCH),
+                        [&](int i, float* piece) {
+#pragma unroll
+    for (int j = 0; j < TJ; j++) *reinterpret_cast<v4f*>(piece + r * PITCH + 16 * j + 4 * g) = acc[i][j];
+  });
 }
 
 // ---- few rows --------------------------------------------------------------------------------
@@ -351,12 +578,13 @@ hipError_t launch_fp8_product(const Fp8Args& a, int64_t codes, hipStream_t s) {
                           : go(std::integral_constant<int, 8>{});
   }
   const unsigned n = (unsigned)(p.tiles_i * p.tiles_j * p.splits);
+  const uint32_t ti = (uint32_t)p.tiles_i, tj = (uint32_t)p.tiles_j, splits = (uint32_t)p.splits;
   auto go = [&](auto KIND) {
     constexpr TileShape t = kFp8Shape[decltype(KIND)::value];
-    return launch_kernel(k_fp8_product<W_SCALES, t.wi, t.wj, t.ti, t.tj, t.stages>, dim3(n), dim3(64 * t.wi * t.wj), s, a,
-                         (uint32_t)p.tiles_i, (uint32_t)p.tiles_j, (uint32_t)p.splits);
+    return launch_kernel(k_fp8_product<W_SCALES, t.wi, t.wj, t.ti, t.tj, t.stages>, dim3(n), dim3(64 * t.wi * t.wj), s, a, ti,
+                         tj, splits);
   };
-  const hipError_t e = p.kind == TILE_256       ? go(std::integral_constant<int, TILE_256>{})
+  const hipError_t e = p.kind == TILE_256       ? launch_kernel(k_fp8_turns<W_SCALES>, dim3(n), dim3(512), s, a, ti, tj, splits)
                        : p.kind == TILE_256_128 ? go(std::integral_constant<int, TILE_256_128>{})
                        : p.kind == TILE_128     ? go(std::integral_constant<int, TILE_128>{})
                                                 : go(std::integral_constant<int, TILE_32>{});
