@@ -340,22 +340,17 @@ __global__ __launch_bounds__(512) void k_fp8_turns(Fp8Args a, uint32_t tiles_i, 
     if (second) lds_barrier();
     for (uint32_t s = s0; s < s1; s++) {
       const uint32_t n = s - s0;
-      load_a(s + 1);
-      if (second) load_high(s + 2);
-      else load_low(s + 1);
       const uint8_t *const pa = smem + n % 2u * (2 * HALF) + wi * HALF;
       const uint8_t *const pb = smem + (wj < 2u ? B_LOW + n % 2u * HALF : B_HIGH + third(n) * HALF) + wj % 2u * 8192u;
       const float* const sr = reinterpret_cast<const float*>(smem + S_ROWS + n % 2u * 1024u);
       const float* const sc = reinterpret_cast<const float*>(smem + S_COLS + third(n) * 1024u);
       v8i xa[4], xb[TJ];
-      float f[TI];             // row scales; by blocks times the columns'
+      float f[TI], w = 1.0f;   // the rows' scales, and by blocks the columns'
       v4f sw[BLOCK ? 1 : TJ];  // columns 16 j + 4 g .. + 3
 #pragma unroll
       for (int i = 0; i < TI; i++) f[i] = sr[128u * wi + 16u * i + r];
       if constexpr (BLOCK) {
-        const float w = sc[64u * wj];   // a wave's 64 columns are of one block
-#pragma unroll
-        for (int i = 0; i < TI; i++) f[i] *= w;
+        w = sc[64u * wj];      // a wave's 64 columns are of one block
       } else {
 #pragma unroll
         for (int j = 0; j < TJ; j++) sw[j] = *reinterpret_cast<const v4f*>(sc + 64u * wj + 16u * j + 4u * g);
@@ -364,8 +359,15 @@ __global__ __launch_bounds__(512) void k_fp8_turns(Fp8Args a, uint32_t tiles_i, 
       for (int j = 0; j < TJ; j++) xb[j] = frag(pb, j);
 #pragma unroll
       for (int i = 0; i < 4; i++) xa[i] = frag(pa, i);
+      __builtin_amdgcn_sched_barrier(0);   // these reads come back while the loads are started
+      load_a(s + 1);
+      if (second) load_high(s + 2);
+      else load_low(s + 1);
 #pragma unroll
-      for (int i = 0; i < TI; i++) asm volatile("" : "+v"(f[i]));   // read and multiplied in this turn
+      for (int i = 0; i < TI; i++) {
+        if (BLOCK) f[i] *= w;
+        asm volatile("" : "+v"(f[i]));     // multiplied in this turn
+      }
       __builtin_amdgcn_sched_barrier(0);
       lds_barrier();
       __builtin_amdgcn_sched_barrier(0);
