@@ -201,7 +201,6 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_fp8_product(Fp8Args a, uint32_
     for (uint32_t s = s0; s < s1; s++) {
       wait_vm<(NS - 2) * LOADS>();
       lds_barrier();   // every wave's loads of this step have landed, and the step before has been read
-      issue(s + NS - 1, smem + (now == 0 ? (NS - 1) * STAGE : now - STAGE));
       const uint8_t *const pa = smem + now, *const pb = pa + OpA::BYTES;
       const float* const sc = reinterpret_cast<const float*>(pa + S_OFF);
       v8i xb[TJ];
@@ -213,17 +212,23 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_fp8_product(Fp8Args a, uint32_
       for (int j = 0; j < TJ; j++)
         sw[j] = W_SCALES == FP8_W_BLOCK ? (v4f)sc[Scales::SA + 16 * TJ * wj]
                                         : *reinterpret_cast<const v4f*>(sc + Scales::SA + 16 * (TJ * wj + j) + 4 * g);
+      v8i xa[TI];
+      float sx[TI];
 #pragma unroll
       for (int i = 0; i < TI; i++) {
-        const v8i xa = frag(pa, fa.at, i);
-        const float sx = sc[16 * (TI * wi + i) + r];
+        xa[i] = frag(pa, fa.at, i);
+        sx[i] = sc[16 * (TI * wi + i) + r];
+      }
+      __builtin_amdgcn_sched_barrier(0);   // these reads come back while the loads are started
+      issue(s + NS - 1, smem + (now == 0 ? (NS - 1) * STAGE : now - STAGE));
+#pragma unroll
+      for (int i = 0; i < TI; i++)
 #pragma unroll
         for (int j = 0; j < TJ; j++) {
-          const v4f p = product128(xb[j], xa);
+          const v4f p = product128(xb[j], xa[i]);
 #pragma unroll
-          for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(p[e], sx * sw[j][e], acc[i][j][e]);
+          for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_fmaf(p[e], sx[i] * sw[j][e], acc[i][j][e]);
         }
-      }
       now = now == (NS - 1) * STAGE ? 0u : now + STAGE;
     }
     wait_vm<0>();
@@ -452,7 +457,7 @@ __global__ __launch_bounds__(512) void k_fp8_turns(Fp8Args a, uint32_t tiles_i, 
 template <int W_SCALES, int KW>
 __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_fp8_few(Fp8Args a) {
   __shared__ v4f sums[FEW_WAVES][64];
-  constexpr int U = 4;              // pairs of blocks in flight
+  constexpr int U = 8;              // pairs of blocks in flight
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n0 = FEW_COLS * ((int64_t)blockIdx.x * (FEW_WAVES / KW) + wave / KW);
@@ -521,9 +526,17 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_fp8_few(Fp8Args a) {
 
 // ---- which kernel ----------------------------------------------------------------------------
 
+// What a tile takes, in microseconds a block of the sum and for its start and end, from calls of one to eight
+// rounds of workgroups, and what joining the parts of a split sum takes; the least total over the first
+// three sizes decides.  Measured for [I, J, K], 256x256 / 256x128 / 128x128 (parts of the sum):
+//   [ 1021, 1000, 2048]  30 / 20.7 / 15.0             [ 4096, 4096, 4096]  61.6 / 76.3 / 95.8
+//   [  968, 2048,16384]  50.5 (8) / 49.8 (4) / 54.4 (2)   [16384, 2048, 2048]  69.6 / 88.4 / 110
+//   [ 2048, 4096, 4096]  49.0 / 41.4 / 49.3           16 groups [8192, 4096, 2048]  102 / 122 / 139
 constexpr TileShape kFp8Shape[4] = {{2, 4, 8, 4, 2}, {4, 2, 4, 4, 3}, {2, 4, 4, 2, 3}, {1, 4, 2, 2, 4}};
-constexpr double kFp8StepUs[3] = {1.29, 0.85, 0.5}, kFp8TileUs[3] = {15.0, 5.0, 4.0};
+constexpr double kFp8StepUs[3] = {1.55, 1.05, 0.70}, kFp8TileUs[3] = {10.0, 6.0, 3.5}, kFp8JoinUs = 5.0;
 constexpr int64_t kFp8LeastPart = 8;   // blocks of a split sum's part
+
+int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 
 ProductPlan plan_fp8(int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped) {
   ProductPlan p{};
@@ -548,20 +561,18 @@ ProductPlan plan_fp8(int64_t I, int64_t J, int64_t K, int64_t groups, bool group
   for (int kind = TILE_256; kind <= TILE_128; kind++) {
     const int64_t ti = ceil_div(I, kFp8Shape[kind].rows()), tj = ceil_div(J, kFp8Shape[kind].cols());
     const int64_t tiles = (ti + (grouped ? groups / 2 : 0)) * tj;
-    int64_t splits = 1;
-    if (!grouped && kind != TILE_256) {
-      const int64_t most = blocks / kFp8LeastPart, want = kUnits / tiles;
-      splits = want < most ? want : most;
-      if (splits < 1) splits = 1;
-    }
-    double us = (kFp8TileUs[kind] + kFp8StepUs[kind] * ceil_div(blocks, splits)) * ceil_div(tiles * splits, kUnits);
-    if (splits > 1) us += kJoinUs + 8e-6 / kJoinTBps * splits * I * J;
-    if (best == 0.0 || us < best) {
-      best = us;
-      p.kind = kind;
-      p.tiles_i = ti + (grouped ? groups + 1 : 0);
-      p.tiles_j = tj;
-      p.splits = splits;
+    const int64_t most = grouped ? 1 : min64(kUnits / tiles, blocks / kFp8LeastPart);
+    for (int q = 0; q < (most > 1 ? 2 : 1); q++) {   // one part, or the most
+      const int64_t splits = q == 0 ? 1 : most;
+      double us = (kFp8TileUs[kind] + kFp8StepUs[kind] * ceil_div(blocks, splits)) * ceil_div(tiles * splits, kUnits);
+      if (splits > 1) us += kFp8JoinUs + 8e-6 / kJoinTBps * splits * I * J;
+      if (best == 0.0 || us < best) {
+        best = us;
+        p.kind = kind;
+        p.tiles_i = ti + (grouped ? groups + 1 : 0);
+        p.tiles_j = tj;
+        p.splits = splits;
+      }
     }
   }
   return p;
