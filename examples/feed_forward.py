@@ -8,6 +8,8 @@ steps and one decoding step on synthetic data.
 and with experts, between the norm and the next block,
   rows, offsets = sort of the router's choices          moe_sort
   z = glu(permute(h) W13[e]^T),  y' = combine(z W2[e]^T, weights)
+With `save` the projections and the GLU between them are one op, feed_forward, which keeps gate and up for
+the backward as BF16 with four more bits ("bf16") or as 8-bit codes ("mxfp8") and forms z again.
 
 `torch.ops.glu_mx` carries the gradients.  Run on a GPU: python examples/feed_forward.py
 """
@@ -40,12 +42,15 @@ def make_params(width, inner, experts=0, seed=0, device="cuda"):
     return p
 
 
-def feed_forward(x, y, p, choices=0):
+def feed_forward(x, y, p, choices=0, save=None):
     """One block on the residual stream x [M, width] and the previous block's output y: the new
-    stream x' and this block's output.  choices > 0 takes that many experts a token."""
+    stream x' and this block's output.  choices > 0 takes that many experts a token; save says what
+    the projections keep for the backward (None: the projections and the GLU one by one)."""
     x_out, h, _ = ops.block_norm(x, y, p["gate"], p["w_pre"], None, p["w_post"], True)
     inner = p["w13"].shape[-2] // 2
     if not choices:
+        if save is not None:
+            return x_out, ops.feed_forward(h, p["w13"], p["w2"], None, p["b2"], None, "swiglu", "split", save)[0]
         a, _ = ops.linear(h, p["w13"])
         z = ops.glu(a[:, :inner], a[:, inner:], "swiglu", "split")
         out, _ = ops.linear(z, p["w2"], p["b2"])
@@ -55,20 +60,23 @@ def feed_forward(x, y, p, choices=0):
     weights = torch.softmax(top, dim=1)
     rows, offsets = ops.moe_sort(ids, p["router"].shape[0])
     xs = ops.moe_permute(h, rows, offsets)
+    if save is not None:
+        ys, _, _ = ops.feed_forward(xs, p["w13"], p["w2"], None, p["b2"], offsets, "swiglu", "split", save)
+        return x_out, ops.moe_combine(ys, rows, offsets, weights)
     a, _ = ops.linear(xs, p["w13"], None, None, offsets)
     z = ops.glu(a[:, :inner], a[:, inner:], "swiglu", "split")
     ys, _ = ops.linear(z, p["w2"], p["b2"], None, offsets)
     return x_out, ops.moe_combine(ys, rows, offsets, weights)
 
 
-def train(tokens=512, width=256, inner=512, experts=0, choices=0, steps=8, lr=0.2, seed=0):
+def train(tokens=512, width=256, inner=512, experts=0, choices=0, steps=8, lr=0.2, seed=0, save=None):
     """Fits the block's output to a fixed target by plain gradient descent; returns the losses."""
     g = torch.Generator(device="cuda").manual_seed(seed + 1)
     x, y, target = (torch.randn((tokens, width), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3))
     p = make_params(width, inner, experts, seed)
     losses = []
     for _ in range(steps):
-        x_out, out = feed_forward(x, y, p, choices)
+        x_out, out = feed_forward(x, y, p, choices, save)
         loss = (x_out.float() + out.float() - target.float()).square().mean()
         grads = torch.autograd.grad(loss * tokens, list(p.values()))
         with torch.no_grad():
@@ -79,13 +87,15 @@ def train(tokens=512, width=256, inner=512, experts=0, choices=0, steps=8, lr=0.
 
 
 def main():
-    for name, kw in (("dense", {}), ("8 experts, 2 a token", dict(experts=8, choices=2))):
+    experts = dict(experts=8, choices=2)
+    for name, kw in (("dense", {}), ("8 experts, 2 a token", experts), ("dense, 8-bit checkpoints", dict(save="mxfp8")),
+                     ("8 experts, 8-bit checkpoints", dict(experts, save="mxfp8"))):
         losses = train(**kw)
         print(f"{name}: loss " + " ".join(f"{v:.4f}" for v in losses))
         with torch.no_grad():   # one new token
             p = make_params(256, 512, kw.get("experts", 0))
             one = torch.randn(1, 256, device="cuda").to(torch.bfloat16)
-            x_out, out = feed_forward(one, one, p, kw.get("choices", 0))
+            x_out, out = feed_forward(one, one, p, kw.get("choices", 0), kw.get("save") and "none")
             print(f"{name}: one token -> {tuple(out.shape)}, mean square {float(out.float().square().mean()):.4f}")
 
 

@@ -28,14 +28,30 @@ that torch.compile keeps whole; these ops do the same for the MI355X kernels:
   torch.ops.glu_mx.moe_permute(x, rows, offsets)                       -> xs
   torch.ops.glu_mx.moe_combine(y, rows, offsets, weights, residual)    -> out
   torch.ops.glu_mx.moe_combine_backward(dout, y, rows, weights, offsets) -> (dy, dweights)
+  torch.ops.glu_mx.gated_linear(x, w, bias, offsets, act, w_layout, save) -> (h, pre, extra)
+  torch.ops.glu_mx.gated_linear_backward(dh, x, w, pre, extra, offsets, act, w_layout, bias, need_dx,
+                                         need_dw)          -> (dx, dw, db)
+  torch.ops.glu_mx.glu_ckpt(gate, up, act, layout)                     -> (h, q, s)
+  torch.ops.glu_mx.glu_ckpt_backward(q, s, dh, act, layout, need_h)    -> (d, h)
+  torch.ops.glu_mx.feed_forward(x, w13, w2, b13, b2, offsets, act, w_layout, save) -> (y, pre, extra)
+  torch.ops.glu_mx.feed_forward_backward(dy, x, w13, w2, pre, extra, offsets, act, w_layout, bias13, bias2)
+                                                                       -> (dx, dw13, dw2, db13, db2)
+  torch.ops.glu_mx.quant_fp8(x, rowwise, colwise)                      -> (q_row, q_col, s_row, s_col)
+  torch.ops.glu_mx.glu_fp8(gate, up, act, layout, rowwise, colwise)    -> the same of act(gate) * up
+  torch.ops.glu_mx.quant_fp8_weight(w, transpose)                      -> (q, s, qt, st)
+  torch.ops.glu_mx.product_fp8(xq, xs, wq, ws, bias, residual, offsets, w_scales) -> y
+  torch.ops.glu_mx.linear_fp8(x, w, bias, residual)                    -> (y, xq, xs, wq, ws)
+  torch.ops.glu_mx.linear_fp8_backward(dy, xq, xs, wq, ws, need_dx, need_dw, bias) -> (dx, dw, db)
 
 Each real implementation is the binding function of the same name (argument marshalling;
 the HIP kernels compute everything).  Each fake implementation gives the output shapes and
 dtypes without touching a GPU, so FakeTensor tracing and torch.compile(fullgraph=True)
 capture the ops as single graph nodes.  `glu` is differentiable: its backward is the
 `glu_backward` op (the fused BF16 backward kernel); so are block_norm, linear, moe_permute (of
-BF16 rows) and moe_combine, through the backward ops beside them.  The quantized ops are not
-differentiable.  In the split layout `up` is the second operand; in the paired layout pass
+BF16 rows), moe_combine, gated_linear, glu_ckpt, feed_forward and linear_fp8, through the backward
+ops beside them.  glu_ckpt keeps gate and up for its backward in 8 bits, feed_forward what its `save`
+says (and forms the GLU's result again instead of keeping it), linear_fp8 x and w as 8-bit codes.  The
+other quantized ops are not differentiable.  In the split layout `up` is the second operand; in the paired layout pass
 an empty `up` (a 0-element tensor), since a custom op cannot take None for a tensor that
 other layouts need.
 """
@@ -52,6 +68,9 @@ from . import (glu_amax as _amax, glu_bwd as _bwd, glu_bwd_mxfp8 as _bwd_mx,
 from . import (glu_block_norm as _norm, glu_block_norm_bwd as _norm_bwd, glu_linear as _linear,
                glu_linear_bwd as _linear_bwd, glu_moe_combine as _combine,
                glu_moe_combine_bwd as _combine_bwd, glu_moe_permute as _permute, glu_moe_sort as _sort)
+from . import (glu_bwd_ckpt as _bwd_ckpt, glu_fwd_ckpt as _fwd_ckpt, glu_fwd_fp8 as _fwd_fp8,
+               glu_gated_linear as _gated, glu_gated_linear_bwd as _gated_bwd, glu_linear_fp8 as _product_fp8,
+               glu_quant_fp8 as _quant_fp8, glu_quant_fp8_weight as _quant_weight)
 
 _LIB = "glu_mx"
 
@@ -462,3 +481,284 @@ def _combine_grad(ctx, dout):
 
 moe_permute.register_autograd(_permute_grad, setup_context=_permute_setup)
 moe_combine.register_autograd(_combine_grad, setup_context=_combine_setup)
+
+
+# ---- gated projections, differentiable --------------------------------------------------
+# pre and extra are what the backward needs of gate and up, zero-sized with save="none" (which has no
+# gradient).  They have no gradient of their own.
+
+def _kept_fake(x, N, save):
+    M = x.shape[0]
+    if save == "none":
+        return x.new_empty((0,)), x.new_empty((0,), dtype=torch.uint8)
+    if save == "bf16":
+        return x.new_empty((M, 2 * N)), x.new_empty((M, N), dtype=torch.uint8)
+    return (x.new_empty((M, 2 * N), dtype=torch.uint8),
+            x.new_empty((M, 2 * ((N + 31) // 32)), dtype=torch.uint8))
+
+
+def _no_save(save):
+    if save == "none":
+        raise RuntimeError('called with save="none": what the gradients need was not kept')
+
+
+@torch.library.custom_op(f"{_LIB}::gated_linear", mutates_args=())
+def gated_linear(x: Tensor, w: Tensor, bias: Optional[Tensor] = None, offsets: Optional[Tensor] = None,
+                 act: str = "swiglu", w_layout: str = "split", save: str = "bf16") -> Tuple[Tensor, Tensor, Tensor]:
+    if save == "none":
+        return (_gated(x, w, bias, act=act, w_layout=w_layout, offsets=offsets), x.new_empty((0,)),
+                x.new_empty((0,), dtype=torch.uint8))
+    return _gated(x, w, bias, act=act, w_layout=w_layout, offsets=offsets, save=save)
+
+
+@gated_linear.register_fake
+def _(x, w, bias=None, offsets=None, act="swiglu", w_layout="split", save="bf16"):
+    N = w.shape[-2] // 2
+    return (x.new_empty((x.shape[0], N)), *_kept_fake(x, N, save))
+
+
+@torch.library.custom_op(f"{_LIB}::gated_linear_backward", mutates_args=())
+def gated_linear_backward(dh: Tensor, x: Tensor, w: Tensor, pre: Tensor, extra: Tensor, offsets: Optional[Tensor],
+                          act: str, w_layout: str, bias: bool, need_dx: bool = True,
+                          need_dw: bool = True) -> Tuple[Tensor, Tensor, Tensor]:
+    return _gated_bwd(dh, x, w, pre, extra, act=act, w_layout=w_layout, offsets=offsets, bias=bias, need_dx=need_dx,
+                      need_dw=need_dw)[:3]
+
+
+@gated_linear_backward.register_fake
+def _(dh, x, w, pre, extra, offsets, act, w_layout, bias, need_dx=True, need_dw=True):
+    return (x.new_empty(x.shape if need_dx else (0,)), w.new_empty(w.shape if need_dw else (0,)),
+            w.new_empty(w.shape[:-1] if bias else (0,)))
+
+
+def _gated_setup(ctx, inputs, output):
+    x, w, _, offsets, ctx.act, ctx.w_layout, ctx.save = inputs
+    ctx.save_for_backward(x, w, offsets, output[1], output[2])
+    ctx.mark_non_differentiable(output[1], output[2])
+
+
+def _gated_grad(ctx, dh, *_):
+    _no_save(ctx.save)
+    x, w, offsets, pre, extra = ctx.saved_tensors
+    need = (tuple(ctx.needs_input_grad) + (False,) * 3)[:3]
+    dx, dw, db = gated_linear_backward(_incoming(dh), x, w, pre, extra, offsets, ctx.act, ctx.w_layout, need[2], need[0],
+                                       need[1])
+    return (*(g if n else None for g, n in zip((dx, dw, db), need)), None, None, None, None)
+
+
+gated_linear.register_autograd(_gated_grad, setup_context=_gated_setup)
+
+
+# ---- the GLU with 8-bit checkpoints, differentiable ---------------------------------------
+
+@torch.library.custom_op(f"{_LIB}::glu_ckpt", mutates_args=())
+def glu_ckpt(gate: Tensor, up: Tensor, act: str = "swiglu", layout: str = "split") -> Tuple[Tensor, Tensor, Tensor]:
+    return _fwd_ckpt(gate, _up(up, layout), act=act, layout=layout)
+
+
+@glu_ckpt.register_fake
+def _(gate, up, act="swiglu", layout="split"):
+    M, N = gate.shape[0], _width(gate, layout)
+    return (gate.new_empty((M, N)), gate.new_empty((M, 2 * N), dtype=torch.uint8),
+            gate.new_empty((M, 2 * ((N + 31) // 32)), dtype=torch.uint8))
+
+
+@torch.library.custom_op(f"{_LIB}::glu_ckpt_backward", mutates_args=())
+def glu_ckpt_backward(q: Tensor, s: Tensor, dh: Tensor, act: str = "swiglu", layout: str = "split",
+                      need_h: bool = False) -> Tuple[Tensor, Tensor]:
+    """d is [dGate | dUp] (split) or the interleaved gradient (paired)."""
+    return _bwd_ckpt(q, s, dh, act=act, layout=layout, need_h=need_h)
+
+
+@glu_ckpt_backward.register_fake
+def _(q, s, dh, act="swiglu", layout="split", need_h=False):
+    return dh.new_empty(q.shape), dh.new_empty(dh.shape if need_h else (0,))
+
+
+def _ckpt_setup(ctx, inputs, output):
+    ctx.act, ctx.layout = inputs[2:]
+    ctx.save_for_backward(output[1], output[2])
+    ctx.mark_non_differentiable(output[1], output[2])
+
+
+def _ckpt_grad(ctx, dh, *_):
+    q, s = ctx.saved_tensors
+    d, _ = glu_ckpt_backward(q, s, _incoming(dh), ctx.act, ctx.layout)
+    if ctx.layout == "paired":
+        return d, None, None, None
+    N = d.shape[1] // 2
+    return d[:, :N], d[:, N:], None, None
+
+
+glu_ckpt.register_autograd(_ckpt_grad, setup_context=_ckpt_setup)
+
+
+# ---- a gated feed-forward block, differentiable --------------------------------------------
+# y = (act(x Wg^T + bg) * (x Wu^T + bu)) W2^T + b2.  The GLU's result is not kept: the backward forms it
+# again from gate and up as kept (save "bf16" or "mxfp8"), in the pass that forms their gradients.
+
+@torch.library.custom_op(f"{_LIB}::feed_forward", mutates_args=())
+def feed_forward(x: Tensor, w13: Tensor, w2: Tensor, b13: Optional[Tensor] = None, b2: Optional[Tensor] = None,
+                 offsets: Optional[Tensor] = None, act: str = "swiglu", w_layout: str = "split",
+                 save: str = "mxfp8") -> Tuple[Tensor, Tensor, Tensor]:
+    h, pre, extra = gated_linear(x, w13, b13, offsets, act, w_layout, save)
+    return _linear(h, w2, b2, offsets=offsets), pre, extra
+
+
+@feed_forward.register_fake
+def _(x, w13, w2, b13=None, b2=None, offsets=None, act="swiglu", w_layout="split", save="mxfp8"):
+    return (x.new_empty((x.shape[0], w2.shape[-2])), *_kept_fake(x, w13.shape[-2] // 2, save))
+
+
+@torch.library.custom_op(f"{_LIB}::feed_forward_backward", mutates_args=())
+def feed_forward_backward(dy: Tensor, x: Tensor, w13: Tensor, w2: Tensor, pre: Tensor, extra: Tensor,
+                          offsets: Optional[Tensor], act: str, w_layout: str, bias13: bool,
+                          bias2: bool) -> Tuple[Tensor, Tensor, Tensor, Tensor, Tensor]:
+    # the first call reads no h: its gradient needs dy and w2 alone
+    dh = _linear_bwd(dy, x.new_empty((x.shape[0], w2.shape[-1])), w2, offsets=offsets, need_dw=False)[0]
+    dx, dw13, db13, h = _gated_bwd(dh, x, w13, pre, extra, act=act, w_layout=w_layout, offsets=offsets, bias=bias13,
+                                   need_h=True)
+    _, dw2, db2 = _linear_bwd(dy, h, w2, offsets=offsets, bias=bias2, need_dx=False)
+    return dx, dw13, dw2, db13, db2
+
+
+@feed_forward_backward.register_fake
+def _(dy, x, w13, w2, pre, extra, offsets, act, w_layout, bias13, bias2):
+    return (x.new_empty(x.shape), w13.new_empty(w13.shape), w2.new_empty(w2.shape),
+            w13.new_empty(w13.shape[:-1] if bias13 else (0,)), w2.new_empty(w2.shape[:-1] if bias2 else (0,)))
+
+
+def _ffn_setup(ctx, inputs, output):
+    x, w13, w2, b13, b2, offsets, ctx.act, ctx.w_layout, ctx.save = inputs
+    ctx.has_bias = b13 is not None, b2 is not None
+    ctx.save_for_backward(x, w13, w2, offsets, output[1], output[2])
+    ctx.mark_non_differentiable(output[1], output[2])
+
+
+def _ffn_grad(ctx, dy, *_):
+    _no_save(ctx.save)
+    x, w13, w2, offsets, pre, extra = ctx.saved_tensors
+    dx, dw13, dw2, db13, db2 = feed_forward_backward(_incoming(dy), x, w13, w2, pre, extra, offsets, ctx.act, ctx.w_layout,
+                                                     *ctx.has_bias)
+    return (dx, dw13, dw2, db13 if ctx.has_bias[0] else None, db2 if ctx.has_bias[1] else None, None, None, None, None)
+
+
+feed_forward.register_autograd(_ffn_grad, setup_context=_ffn_setup)
+
+
+# ---- 8-bit floating point with a scale for each 128 -----------------------------------------
+
+def _fp8_fake(ref, M, N, rowwise, colwise):
+    def pair(on, rows, cols):
+        if not on:
+            return ref.new_empty((0,), dtype=torch.uint8), ref.new_empty((0,), dtype=torch.float32)
+        return (ref.new_empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8),
+                ref.new_empty(((cols + 127) // 128, rows), dtype=torch.float32))
+    (q_row, s_row), (q_col, s_col) = pair(rowwise, M, N), pair(colwise, N, M)
+    return q_row, q_col, s_row, s_col
+
+
+@torch.library.custom_op(f"{_LIB}::quant_fp8", mutates_args=())
+def quant_fp8(x: Tensor, rowwise: bool = True, colwise: bool = False) -> Tuple[Tensor, Tensor, Tensor, Tensor]:
+    return _quant_fp8(x, rowwise=rowwise, colwise=colwise)
+
+
+@quant_fp8.register_fake
+def _(x, rowwise=True, colwise=False):
+    return _fp8_fake(x, x.shape[0], x.shape[1], rowwise, colwise)
+
+
+@torch.library.custom_op(f"{_LIB}::glu_fp8", mutates_args=())
+def glu_fp8(gate: Tensor, up: Tensor, act: str = "swiglu", layout: str = "split", rowwise: bool = True,
+            colwise: bool = False) -> Tuple[Tensor, Tensor, Tensor, Tensor]:
+    return _fwd_fp8(gate, _up(up, layout), act=act, layout=layout, rowwise=rowwise, colwise=colwise)
+
+
+@glu_fp8.register_fake
+def _(gate, up, act="swiglu", layout="split", rowwise=True, colwise=False):
+    return _fp8_fake(gate, gate.shape[0], _width(gate, layout), rowwise, colwise)
+
+
+def _weight_fake(w, n, k):
+    lead = w.shape[:-2]
+    return (w.new_empty((*lead, n, (k + 15) // 16 * 16), dtype=torch.uint8),
+            w.new_empty((*lead, (n + 127) // 128, (k + 127) // 128), dtype=torch.float32))
+
+
+@torch.library.custom_op(f"{_LIB}::quant_fp8_weight", mutates_args=())
+def quant_fp8_weight(w: Tensor, transpose: bool = False) -> Tuple[Tensor, Tensor, Tensor, Tensor]:
+    return _quant_weight(w, transpose=transpose)
+
+
+@quant_fp8_weight.register_fake
+def _(w, transpose=False):
+    n, k = w.shape[-2:]
+    none = (w.new_empty((0,), dtype=torch.uint8), w.new_empty((0,), dtype=torch.float32))
+    return (*_weight_fake(w, n, k), *(_weight_fake(w, k, n) if transpose else none))
+
+
+@torch.library.custom_op(f"{_LIB}::product_fp8", mutates_args=())
+def product_fp8(xq: Tensor, xs: Tensor, wq: Tensor, ws: Tensor, bias: Optional[Tensor] = None,
+                residual: Optional[Tensor] = None, offsets: Optional[Tensor] = None, w_scales: str = "block") -> Tensor:
+    return _product_fp8(xq, xs, wq, ws, bias, residual, w_scales=w_scales, offsets=offsets)
+
+
+@product_fp8.register_fake
+def _(xq, xs, wq, ws, bias=None, residual=None, offsets=None, w_scales="block"):
+    return xq.new_empty((xq.shape[0], wq.shape[-2]), dtype=torch.bfloat16)
+
+
+# A linear layer whose three products run in 8 bits.  For the backward it keeps x quantized along its rows'
+# number (colwise) and W transposed, both as codes.  The gradients are those of the product at what the
+# codes of x and W stand for, with dy quantized too; the bias's is the sum of dy, the residual's dy itself.
+
+@torch.library.custom_op(f"{_LIB}::linear_fp8", mutates_args=())
+def linear_fp8(x: Tensor, w: Tensor, bias: Optional[Tensor] = None,
+               residual: Optional[Tensor] = None) -> Tuple[Tensor, Tensor, Tensor, Tensor, Tensor]:
+    q_row, q_col, s_row, s_col = _quant_fp8(x, rowwise=True, colwise=True)
+    wq, ws, wt, wts = _quant_weight(w, transpose=True)
+    return _product_fp8(q_row, s_row, wq, ws, bias, residual), q_col, s_col, wt, wts
+
+
+@linear_fp8.register_fake
+def _(x, w, bias=None, residual=None):
+    _, q_col, _, s_col = _fp8_fake(x, x.shape[0], x.shape[1], False, True)
+    return (x.new_empty((x.shape[0], w.shape[0])), q_col, s_col, *_weight_fake(w, w.shape[1], w.shape[0]))
+
+
+@torch.library.custom_op(f"{_LIB}::linear_fp8_backward", mutates_args=())
+def linear_fp8_backward(dy: Tensor, xq: Tensor, xs: Tensor, wq: Tensor, ws: Tensor, need_dx: bool = True,
+                        need_dw: bool = True, bias: bool = False) -> Tuple[Tensor, Tensor, Tensor]:
+    dx, dw, db = dy.new_empty((0,)), dy.new_empty((0,)), dy.new_empty((0,))
+    if need_dx or need_dw:
+        q_row, q_col, s_row, s_col = _quant_fp8(dy, rowwise=need_dx, colwise=need_dw)
+        if need_dx:
+            dx = _product_fp8(q_row, s_row, wq, ws)
+        if need_dw:
+            dw = _product_fp8(q_col, s_col, xq, xs, w_scales="row")
+    if bias:   # the column sums alone, of a product without terms
+        db = _linear_bwd(dy, dy.new_empty((dy.shape[0], 0)), dy.new_empty((dy.shape[1], 0)), bias=True, need_dx=False,
+                         need_dw=False)[2]
+    return dx, dw, db
+
+
+@linear_fp8_backward.register_fake
+def _(dy, xq, xs, wq, ws, need_dx=True, need_dw=True, bias=False):
+    return (dy.new_empty((dy.shape[0], wq.shape[0]) if need_dx else (0,)),
+            dy.new_empty((dy.shape[1], xq.shape[0]) if need_dw else (0,)),
+            dy.new_empty((dy.shape[1],) if bias else (0,)))
+
+
+def _fp8_setup(ctx, inputs, output):
+    ctx.save_for_backward(*output[1:])
+    ctx.mark_non_differentiable(*output[1:])
+
+
+def _fp8_grad(ctx, dy, *_):
+    need = (tuple(ctx.needs_input_grad) + (False,) * 4)[:4]
+    dy = _incoming(dy)
+    grads = linear_fp8_backward(dy, *ctx.saved_tensors, *need[:3])
+    return (*(g if n else None for g, n in zip(grads, need)), dy if need[3] else None)
+
+
+linear_fp8.register_autograd(_fp8_grad, setup_context=_fp8_setup)
