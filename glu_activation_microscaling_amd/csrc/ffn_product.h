@@ -511,21 +511,35 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, int64_t group
 
 // WI x WJ waves of TI x TJ tiles of 16 x 16 each: a tile of 16 WI TI rows by 16 WJ TJ columns.
 //
-// NS LDS stages, each a step of BK elements.  A step's matrix work runs in two halves of 32
-// elements.  While the first half multiplies, the second half's fragments are read; then one
-// barrier says both that every wave has read the stage and that the next stage has landed;
-// the loads of the step NS further on go into the stage just freed and the next stage's first
-// fragments are read while the second half multiplies.  A load so has NS - 1 steps to arrive.
+// The smaller tiles keep NS LDS stages, each a step of BK elements.  A step's matrix work runs in two
+// halves of 32 elements.  While the first half multiplies, the second half's fragments are read;
+// then one barrier says both that every wave has read the stage and that the next stage has
+// landed; the loads of the step NS further on go into the stage just freed and the next stage's
+// first fragments are read while the second half multiplies.  A load so has NS - 1 steps to arrive.
+//
+// In the largest tile (NS = 2, eight waves) waves 0 .. 3, one a SIMD, read a step's fragments and start
+// loads while waves 4 .. 7 multiply, and the other way round; each turn ends with a barrier.  With all
+// eight in step, every wave waited for its fragments and for its loads to be taken at the same time (the
+// times below 7 % longer, 2 % for the gradient of W).
+// The first half reads step s in turn 2 s and multiplies in turn 2 s + 1, the second half one turn later.
+// Each half has two turns to see its loads landed:
+//   the first half starts in turn 2 s the loads of step s + 1 of its own rows of A and of the low columns
+//     of B (both halves have read step s - 1 of those by the end of turn 2 s - 1: two stages);
+//   the second half in turn 2 s + 1 those of step s + 1 of its own rows of A, which it reads in turn 2 s + 3,
+//     and of step s + 2 of the high columns of B, which the first half reads in turn 2 s + 4: three stages.
+// Registers hold B's fragments and half of A's; the others are read while multiplying.
 //
 // Bound by the matrix cores at large sizes; what is lost there is the start and the end of a tile,
 // which nothing overlaps (one workgroup fills a compute unit's LDS).  Measured on an MI355X:
-//   256x256  [16384, 7168, 2048] (I, J, K) alone 364 to 373 us (1.3 PFLOP/s), with bias, GELU, residual
-//            and saved pre-activation 488 to 506; gradient of x 377 to 388, of W 408 to 410
-//            16 groups, 16384 rows, [4096, 2048]: 290 to 323, gradients 296 to 329 and 296 to 326
+//   256x256  [16384, 7168, 2048] (I, J, K) alone 346 to 354 us (1.4 PFLOP/s), with bias, GELU, residual
+//            and saved pre-activation 434; gradient of x 329, of W 357; 8192^3 711 (1.55 PFLOP/s; 601 on zeros)
+//            16 groups, 16384 rows, [4096, 2048]: 267, gradients 266 and 274
+//            gated, [16384, 2 x 7168, 2048]: 800 with gate and up kept; 16 groups, 16384 rows, [2 x 2048, 2048]:
+//            290 with them kept as MXFP8; [968, 2 x 16384, 2048] 111 to 133
 //   256x128  [968, 2048, 16384] in four parts 59 us (1.1 PFLOP/s), and 7 to join them
 //   128x128  [1021, 1000, 2056] in four parts 14.9 us, and 5.6 to join them
 //   32x128   32 groups, 256 rows, [2048, 2048], W from memory: 49 us (5.5 TB/s)
-// Tried and slower at [16384, 7168, 2048] (forward with epilogue, 500 to 540 us at the time): 128x128 tiles 637;
+// Tried and slower at [16384, 7168, 2048] (forward with epilogue, eight waves in step, 500 to 540 us): 128x128 tiles 637;
 // 4 waves of 128x128 798; four stages of 32 elements 558; two workgroups of 256x128 and three
 // stages of 32 a compute unit 581; workgroups that stay and load the next tile during the
 // epilogue 560.
@@ -535,11 +549,13 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
   static_assert(GATED == 3);
   constexpr bool TA = MODE == WGRAD, TB = MODE == DGRAD || MODE == WGRAD;
   constexpr int BI = 16 * WI * TI, BJ = 16 * WJ * TJ, WAVES = WI * WJ;
-  using OpA = Operand<TA, BI, WAVES>;
-  using OpB = std::conditional_t<MODE == GATED, GatedOperand<BJ, WAVES>, Operand<TB, BJ, WAVES>>;
-  // both stages of A, then both of B: every fragment read's place is within the 16-bit offset
-  // of a read instruction from the lane's base
-  __shared__ __attribute__((aligned(16))) uint8_t smem[NS * (OpA::BYTES + OpB::BYTES)];
+  constexpr bool TURNS = NS == 2;
+  static_assert(!TURNS || (WI == 2 && WJ % 2 == 0 && TI % 2 == 0));
+  constexpr int PARTS = TURNS ? 2 : 1;   // of the waves, and of the rows and columns they load
+  using OpA = Operand<TA, BI / PARTS, WAVES / PARTS>;
+  using OpB = std::conditional_t<MODE == GATED, GatedOperand<BJ / PARTS, WAVES / PARTS>, Operand<TB, BJ / PARTS, WAVES / PARTS>>;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[TURNS ? 4 * OpA::BYTES + 5 * OpB::BYTES
+                                                             : NS * (OpA::BYTES + OpB::BYTES)];
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -592,20 +608,30 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
 
   OpA oa;
   OpB ob;
-  oa.init(a.a, a.ld_a, t.i0, t.i1, wave, lane);
+  const uint32_t half = TURNS ? wave / (WAVES / 2) : 0u, mate = TURNS ? wave % (WAVES / 2) : wave;
+  oa.init(a.a, a.ld_a, t.i0 + half * (BI / 2), t.i1, mate, lane);
   const bool none = MODE != WGRAD && group == a.groups;   // rows of no group
   if constexpr (MODE == GATED) {
-    ob.init(none ? a.b : a.b + group * a.b_group, a.ld_b, a.J, a.paired != 0, j0 / 2, wave, lane);
+    ob.init(none ? a.b : a.b + group * a.b_group, a.ld_b, a.J, a.paired != 0, j0 / 2 + half * (BJ / 4), mate, lane);
   } else {
-    ob.init(a.b + group * a.b_group, a.ld_b, j0, j1, wave, lane);
+    ob.init(a.b + group * a.b_group, a.ld_b, j0 + half * (BJ / 2), j1, mate, lane);
     if (none) ob.base = a.b;
   }
-  using FrA = Fragments<TA, BI, WI, TI>;
-  using FrB = Fragments<TB, BJ, WJ, TJ>;
+  using FrA = Fragments<TA, BI / PARTS, WI / PARTS, TI>;
+  using FrB = Fragments<TB, BJ / PARTS, WJ / PARTS, TJ>;
   FrA fa;
   FrB fb;
-  fa.init(wi, lane);
-  fb.init(wj, lane);
+  fa.init(TURNS ? 0 : wi, lane);
+  fb.init(TURNS ? wj % (WJ / PARTS) : wj, lane);
+  // row tile i and column tile j of a wave in the workgroup's tile
+  struct Rows {
+    static __device__ __forceinline__ uint32_t tile(uint32_t w, int i) { return TURNS ? TI * w + i : FrA::tile(w, i); }
+  };
+  struct Cols {
+    static __device__ __forceinline__ uint32_t tile(uint32_t w, int j) {
+      return TURNS ? w / (WJ / PARTS) * (BJ / 32) + FrB::tile(w % (WJ / PARTS), j) : FrB::tile(w, j);
+    }
+  };
 
   v4f acc[TI][TJ];
 #pragma unroll
@@ -613,30 +639,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
 #pragma unroll
     for (int j = 0; j < TJ; j++) acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 
-  uint8_t *const sa = smem, *const sb = smem + 2 * OpA::BYTES;
-  auto issue = [&](uint32_t k, int stage) {
-#pragma unroll
-    for (int q = 0; q < OpA::LOADS; q++) oa.template issue<false>(q, k, k1, sa + stage * OpA::BYTES, wave, lane);
-#pragma unroll
-    for (int q = 0; q < OpB::LOADS; q++) ob.template issue<false>(q, k, k1, sb + stage * OpB::BYTES, wave, lane);
-  };
-  auto issue_tail = [&](uint32_t k, int stage) {
-#pragma unroll
-    for (int q = 0; q < OpA::LOADS; q++) oa.template issue<true>(q, k, k1, sa + stage * OpA::BYTES, wave, lane);
-#pragma unroll
-    for (int q = 0; q < OpB::LOADS; q++) ob.template issue<true>(q, k, k1, sb + stage * OpB::BYTES, wave, lane);
-  };
-  auto start = [&](uint32_t k, int stage) {   // the loads of the step at k, if there is one
-    if (k + BK <= k1) issue(k, stage);
-    else if (k < k1) issue_tail(k, stage);
-  };
   v8bf xa[2][TI], xb[2][TJ];
-  auto read = [&](int stage, int h) {
-#pragma unroll
-    for (int i = 0; i < TI; i++) xa[h][i] = fa.read(sa + stage * OpA::BYTES, i, h);
-#pragma unroll
-    for (int j = 0; j < TJ; j++) xb[h][j] = fb.read(sb + stage * OpB::BYTES, j, h);
-  };
   auto multiply = [&](int h) {
 #pragma unroll
     for (int i = 0; i < TI; i++)
@@ -649,42 +652,8 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
   constexpr int READS = TI * (TA ? 2 : 1) + TJ * (TB ? 2 : 1), PRODUCTS = TI * TJ;
   constexpr int LOADS = OpA::LOADS + OpB::LOADS;
   enum { G_MFMA = 0x8, G_VMEM = 0x10, G_DS_READ = 0x100 };
-  auto step = [&](uint32_t k, int stage, auto FULL) {
-    read(stage, 1);
-    multiply(0);
-#pragma unroll
-    for (int q = 0; q < READS; q++) {
-      __builtin_amdgcn_sched_group_barrier(G_DS_READ, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(G_MFMA, PRODUCTS / READS, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);   // the products above are not to sink below the wait
-    wait_vm<0>();
-    lds_barrier();
-    if constexpr (decltype(FULL)::value) {   // at least two whole steps follow: no branches
-      issue(k + 2 * BK, stage);
-      read(1 - stage, 0);
-      multiply(1);
-#pragma unroll
-      for (int q = 0; q < LOADS; q++) {
-        __builtin_amdgcn_sched_group_barrier(G_VMEM, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(G_MFMA, 1, 0);
-      }
-#pragma unroll
-      for (int q = 0; q < READS; q++) {
-        __builtin_amdgcn_sched_group_barrier(G_DS_READ, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(G_MFMA, (PRODUCTS - LOADS) / READS > 1 ? (PRODUCTS - LOADS) / READS : 1, 0);
-      }
-    } else {
-      start(k + 2 * BK, stage);
-      if (k + BK < k1) read(1 - stage, 0);
-      multiply(1);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    wait_lds();   // long since arrived; said here so that the loop's head waits for no more
-  };
-
-  // More stages: a ring, whose present stage starts at byte `now`.  Every step starts the loads of
-  // one step, real or not, so that the count of loads under way is known.
+  // A ring of stages, whose present one starts at byte `now`.  Every step starts the loads of one
+  // step, real or not, so that the count of loads under way is known.
   constexpr uint32_t STAGE = OpA::BYTES + OpB::BYTES;
   uint32_t now = 0;
   auto issue_at = [&](uint32_t k, uint32_t at, auto TAIL) {
@@ -766,22 +735,93 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
       lds_barrier();
     }
   } else if (k0 < k1) {
-    start(k0, 0);
-    start(k0 + BK, 1);
-    if (k0 + 2 * BK <= k1) wait_vm<LOADS>();   // of the second step's
-    else wait_vm<0>();
+    // A: two stages of both halves' rows; B's low columns: two, high columns: three
+    constexpr uint32_t B_LOW = 4 * OpA::BYTES, B_HIGH = B_LOW + 2 * OpB::BYTES;
+    auto load = [&](const auto& op, uint32_t k, uint8_t* to, auto TAIL) {
+#pragma unroll
+      for (int q = 0; q < std::decay_t<decltype(op)>::LOADS; q++)
+        op.template issue<decltype(TAIL)::value>(q, k, k1, to, mate, lane);
+    };
+    constexpr std::true_type any{};
+    constexpr std::false_type whole{};
+    load(oa, k0, smem + half * OpA::BYTES, any);
+    if (half == 0) {
+      load(ob, k0, smem + B_LOW, any);
+    } else {
+      load(ob, k0, smem + B_HIGH, any);
+      load(ob, min(k0 + BK, k1), smem + B_HIGH + OpB::BYTES, any);
+    }
+    wait_vm<0>();
     lds_barrier();
-    read(0, 0);
-    wait_lds();
-    uint32_t k = k0;
-    for (; k + 4 * BK <= k1; k += 2 * BK) {
-      step(k, 0, std::true_type{});
-      step(k + BK, 1, std::true_type{});
-    }
-    for (; k < k1; k += 2 * BK) {
-      step(k, 0, std::false_type{});
-      if (k + BK < k1) step(k + BK, 1, std::false_type{});
-    }
+    auto turns = [&](auto SECOND) {
+      constexpr bool second = decltype(SECOND)::value;
+      if (second) lds_barrier();
+      uint32_t third = 0;   // the step's stage of B's high columns
+      auto step = [&](uint32_t k, uint32_t odd, auto TAIL) {
+        const uint8_t *const pa = smem + odd * (2 * OpA::BYTES) + half * OpA::BYTES;
+        const uint8_t *const pb = smem + (wj < WJ / 2 ? B_LOW + odd * OpB::BYTES : B_HIGH + third * OpB::BYTES);
+        v8bf ya[2][TI / 2], yb[2][TJ];
+#pragma unroll
+        for (int j = 0; j < TJ; j++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) yb[h][j] = fb.read(pb, j, h);
+#pragma unroll
+        for (int i = 0; i < TI / 2; i++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) ya[h][i] = fa.read(pa, i, h);
+        __builtin_amdgcn_sched_barrier(0);   // these reads come back while the loads are started
+        const uint32_t k_a = min(k + BK, k1), k_b = second ? min(k + 2 * BK, k1) : k_a;   // of the loads
+        uint8_t* const to_a = smem + (odd ^ 1u) * (2 * OpA::BYTES) + half * OpA::BYTES;
+        uint8_t* const to_b =
+            smem + (second ? B_HIGH + (third == 0 ? 2u : third - 1u) * OpB::BYTES : B_LOW + (odd ^ 1u) * OpB::BYTES);
+        load(oa, k_a, to_a, TAIL);
+        load(ob, k_b, to_b, TAIL);
+        __builtin_amdgcn_sched_barrier(0);
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int i = 0; i < TI; i++) {
+#pragma unroll
+          for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int j = 0; j < TJ; j++)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(yb[h][j], ya[h][i % (TI / 2)], acc[i][j], 0, 0, 0);
+          if (i < TI / 2) {
+#pragma unroll
+            for (int h = 0; h < 2; h++) ya[h][i] = fa.read(pa, TI / 2 + i, h);
+          }
+        }
+        // the products stay in this turn
+#pragma unroll
+        for (int i = 0; i < TI; i++)
+#pragma unroll
+          for (int j = 0; j < TJ; j++) asm volatile("" : "+v"(acc[i][j]));
+#pragma unroll
+        for (int i = 0; i < TI / 2; i++) {   // the fragments just done with give way to those of the high rows
+          __builtin_amdgcn_sched_group_barrier(G_MFMA, 2 * TJ, 0);
+          __builtin_amdgcn_sched_group_barrier(G_DS_READ, TA ? 4 : 2, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(G_MFMA, TI * TJ, 0);
+        __builtin_amdgcn_s_setprio(0);
+        wait_vm<0>();
+        __builtin_amdgcn_sched_barrier(0);
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        third = third == 2 ? 0u : third + 1u;
+      };
+      uint32_t k = k0;
+      for (; k + 4 * BK <= k1; k += 2 * BK) {
+        step(k, 0, whole);
+        step(k + BK, 1, whole);
+      }
+      for (uint32_t odd = 0; k < k1; k += BK, odd ^= 1u) step(k, odd, any);
+      if (!second) lds_barrier();
+    };
+    if (half != 0) turns(std::true_type{});
+    else turns(std::false_type{});
+    wait_vm<0>();   // the stages hold the sums next
+    lds_barrier();
   }
 
   // acc[i][j][e] is C at row r of its row tile and column 4 g + e of its column tile.  Rows and
@@ -793,10 +833,10 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
     const auto rw = rsrc(uniform((const uint16_t*)(a.work + at * width + j0)));
 #pragma unroll
     for (int i = 0; i < TI; i++) {
-      const uint32_t first = 16u * FrA::tile(wi, i);
+      const uint32_t first = 16u * Rows::tile(wi, i);
 #pragma unroll
       for (int j = 0; j < TJ; j++) {
-        const uint32_t col = 16u * FrB::tile(wj, j) + 4u * g;
+        const uint32_t col = 16u * Cols::tile(wj, j) + 4u * g;
         const uint32_t o = first + r < rows && col < cols ? 4u * ((first + r) * (uint32_t)width + col) : kOob;
         put16(__builtin_bit_cast(u32x4, acc[i][j]), rw, o);
       }
@@ -805,7 +845,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
   }
   if constexpr (MODE == GATED) {
     static_assert(WAVES * GATED_LDS <= sizeof(smem));
-    gated_epilogue<ACT, TI, TJ, FrA>(a, group, t, j0 / 2, wi, wj, lane, smem + wave * GATED_LDS, acc);
+    gated_epilogue<ACT, TI, TJ, Rows>(a, group, t, j0 / 2, wi, wj, lane, smem + wave * GATED_LDS, acc);
     return;
   }
   // A row tile's 16 x (16 TJ) sums go through the wave's own piece of LDS, so that a lane gets 8
@@ -815,11 +855,11 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
   static_assert(WAVES * 16 * PITCH * 4 <= sizeof(smem));
   float* const mine = reinterpret_cast<float*>(smem) + wave * (16 * PITCH);
   const uint32_t cc = 8u * (lane % CH), lrow = lane / CH;
-  const uint32_t col = 16u * FrB::tile(wj, cc / 16) + cc % 16u;
+  const uint32_t col = 16u * Cols::tile(wj, cc / 16) + cc % 16u;
   const uint32_t left = col < cols ? rows - min(rows, lrow) : 0u;   // of the lane's rows lrow + 16 tile + ROWS p
   // the place of pass p of row tile i in a matrix whose rows are ld apart
   auto place = [&](uint32_t ld, int i, uint32_t p) {
-    const uint32_t first = 16u * FrA::tile(wi, i) + ROWS * p;
+    const uint32_t first = 16u * Rows::tile(wi, i) + ROWS * p;
     return first < left ? 2u * (lrow * ld + col) + 2u * first * ld : kOob;
   };
   const uint32_t ld_c = (uint32_t)a.ld_c, J = (uint32_t)a.J;
@@ -995,12 +1035,13 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // one round of workgroups (2048 to 8192 rows, sums of 1024 to 8192 elements), and what joining the
 // parts of a split sum takes.  The least total over the first three sizes decides.  Measured for
 // [I, J, K], 256x256 / 256x128 / 128x128:
-//   [ 1000, 1000, 1000]  24.8 / 15.8 / 11.2      [ 4096, 4096, 1024]  33.2 /  41.6 /  45.7
-//   [  968, 2048,16384]   278 / 65.8 / 72.0      [ 4096, 4096, 4096]  99.2 / 113.7 / 136.3
-//   [ 2048, 4096, 4096]  87.6 / 58.2 / 69.1      [16384, 2048, 2048]   107 /   126 /   151
-// (of 33 such shapes the rule takes the fastest of the three on 32 and is 0.5% behind on one).
+//   [ 1000, 1000, 1000]  22   / 15.8 / 11.2      [ 4096, 4096, 1024]  29.8 /  41.6 /  45.7
+//   [  968, 2048,16384]   278 / 65.8 / 72.0      [ 4096, 4096, 4096]  92.6 / 113.7 / 136.3
+//   [ 2048, 4096, 4096]  75   / 58.2 / 69.1      [16384, 2048, 2048]  98.6 /   126 /   151
+// (of 33 such shapes, with the largest tile's step at 1.29 us, the rule took the fastest of the three on 32
+// and was 0.5% behind on one).
 constexpr int64_t kUnits = 256;
-constexpr double kStepUs[3] = {1.29, 0.85, 0.5}, kTileUs[3] = {15.0, 5.0, 4.0}, kJoinUs = 2.5, kJoinTBps = 8.0;
+constexpr double kStepUs[3] = {1.22, 0.85, 0.5}, kTileUs[3] = {15.0, 5.0, 4.0}, kJoinUs = 2.5, kJoinTBps = 8.0;
 constexpr int64_t kLeastPart = 512;   // elements of a split sum's part: 256 costs up to 5 us more, and gains 0.5
 
 // A rule on extents alone, so that the scratch memory of split sums can be sized before the
