@@ -292,26 +292,26 @@ __global__ __launch_bounds__(512) void k_fp8_turns(Fp8Args a, uint32_t tiles_i, 
   oa.init(a.a, a.ld_a, o.t.i0, o.t.i1, wave, lane);
   ob.init(o.none ? a.b : a.b + o.t.group * a.b_group, a.ld_b, o.j0, o.j0 + o.cols, wave, lane);
   os.init(a, o, wave, lane);
-  auto third = [](uint32_t n) { return n - 3u * (n * 0xaaabu >> 17); };   // n % 3, n < 2^15
-  // The wave's loads of one operand for step s, four blocks of 1 KiB; past the end zeros.  No branch.
-  auto load = [&](const Op& op, uint32_t s, uint8_t* to) {
-    const uint32_t k = s < s1 ? s * (CODES / 2) : k1;
+  // The wave's loads of one operand for step s, four blocks of 1 KiB.  TAIL: past the end zeros.
+  auto load = [&](const Op& op, uint32_t s, uint8_t* to, auto TAIL) {
+    constexpr bool tail = decltype(TAIL)::value;
+    const uint32_t k = !tail || s < s1 ? s * (CODES / 2) : k1;
     const auto from = rsrc(op.base + k);
     const uint32_t mine = 8u * ((lane & 7u) ^ (lane >> 4));   // first pair of codes in even blocks; in odd ones ^ 32
     const bool in[2] = {k + mine < k1, k + (mine ^ 32u) < k1};
 #pragma unroll
     for (int q = 0; q < 4; q++)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr)(to + 4096u * (wave % 4u) + 1024u * q), 16,
-                                               in[q % 2] ? op.off[q] : kOob, 0, 0, 0);
+                                               !tail || in[q % 2] ? op.off[q] : kOob, 0, 0, 0);
   };
-  auto load_a = [&](uint32_t s) { load(oa, s, smem + (s - s0) % 2u * (2 * HALF) + wave / 4u * HALF); };
-  auto load_low = [&](uint32_t s) {     // B and the rows' scales; waves 0 .. 3
-    load(ob, s, smem + B_LOW + (s - s0) % 2u * HALF);
-    os.issue(s, s < s1, smem + S_ROWS + (s - s0) % 2u * 1024u, wave);
+  auto load_a = [&](uint32_t s, uint32_t odd, auto TAIL) { load(oa, s, smem + odd * (2 * HALF) + wave / 4u * HALF, TAIL); };
+  auto load_low = [&](uint32_t s, uint32_t odd, auto TAIL) {     // B and the rows' scales; waves 0 .. 3
+    load(ob, s, smem + B_LOW + odd * HALF, TAIL);
+    os.issue(s, !decltype(TAIL)::value || s < s1, smem + S_ROWS + odd * 1024u, wave);
   };
-  auto load_high = [&](uint32_t s) {    // B and the columns' scales; waves 4 .. 7
-    load(ob, s, smem + B_HIGH + third(s - s0) * HALF);
-    os.issue(s, s < s1, smem + S_COLS + third(s - s0) * 1024u - 1024u, wave);
+  auto load_high = [&](uint32_t s, uint32_t third, auto TAIL) {    // B and the columns' scales; waves 4 .. 7
+    load(ob, s, smem + B_HIGH + third * HALF, TAIL);
+    os.issue(s, !decltype(TAIL)::value || s < s1, smem + S_COLS + third * 1024u - 1024u, wave);
   };
 
   v4f acc[TI][TJ];
@@ -331,24 +331,27 @@ __global__ __launch_bounds__(512) void k_fp8_turns(Fp8Args a, uint32_t tiles_i, 
 
   if (s0 < s1) {
     enum { G_VALU = 0x2, G_MFMA = 0x8, G_DS_READ = 0x100 };   // the scheduler's groups
-    load_a(s0);
+    constexpr std::true_type any{};
+    constexpr std::false_type whole{};
+    const uint32_t full = min(s1, k1 / (CODES / 2));   // steps before it have all their codes
+    load_a(s0, 0, any);
     if (wi == 0) {
-      load_low(s0);
+      load_low(s0, 0, any);
     } else {
-      load_high(s0);
-      load_high(s0 + 1);
+      load_high(s0, 0, any);
+      load_high(s0 + 1, 1, any);
     }
     wait_vm<0>();
     lds_barrier();
     auto turns = [&](auto SECOND) {
     constexpr bool second = decltype(SECOND)::value;
     if (second) lds_barrier();
-    for (uint32_t s = s0; s < s1; s++) {
-      const uint32_t n = s - s0;
-      const uint8_t *const pa = smem + n % 2u * (2 * HALF) + wi * HALF;
-      const uint8_t *const pb = smem + (wj < 2u ? B_LOW + n % 2u * HALF : B_HIGH + third(n) * HALF) + wj % 2u * 8192u;
-      const float* const sr = reinterpret_cast<const float*>(smem + S_ROWS + n % 2u * 1024u);
-      const float* const sc = reinterpret_cast<const float*>(smem + S_COLS + third(n) * 1024u);
+    uint32_t third = 0;
+    auto step = [&](uint32_t s, uint32_t odd, auto TAIL) {
+      const uint8_t *const pa = smem + odd * (2 * HALF) + wi * HALF;
+      const uint8_t *const pb = smem + (wj < 2u ? B_LOW + odd * HALF : B_HIGH + third * HALF) + wj % 2u * 8192u;
+      const float* const sr = reinterpret_cast<const float*>(smem + S_ROWS + odd * 1024u);
+      const float* const sc = reinterpret_cast<const float*>(smem + S_COLS + third * 1024u);
       v8i xa[4], xb[TJ];
       float f[TI], w = 1.0f;   // the rows' scales, and by blocks the columns'
       v4f sw[BLOCK ? 1 : TJ];  // columns 16 j + 4 g .. + 3
@@ -365,9 +368,9 @@ __global__ __launch_bounds__(512) void k_fp8_turns(Fp8Args a, uint32_t tiles_i, 
 #pragma unroll
       for (int i = 0; i < 4; i++) xa[i] = frag(pa, i);
       __builtin_amdgcn_sched_barrier(0);   // these reads come back while the loads are started
-      load_a(s + 1);
-      if (second) load_high(s + 2);
-      else load_low(s + 1);
+      load_a(s + 1, odd ^ 1u, TAIL);
+      if (second) load_high(s + 2, third == 0 ? 2u : third - 1u, TAIL);
+      else load_low(s + 1, odd ^ 1u, TAIL);
 #pragma unroll
       for (int i = 0; i < TI; i++) {
         if (BLOCK) f[i] *= w;
@@ -417,7 +420,14 @@ __global__ __launch_bounds__(512) void k_fp8_turns(Fp8Args a, uint32_t tiles_i, 
       __builtin_amdgcn_sched_barrier(0);
       lds_barrier();
       __builtin_amdgcn_sched_barrier(0);
+      third = third == 2 ? 0u : third + 1u;
+    };
+    uint32_t s = s0;
+    for (; s + 4 <= full; s += 2) {
+      step(s, 0, whole);
+      step(s + 1, 1, whole);
     }
+    for (uint32_t odd = 0; s < s1; s++, odd ^= 1u) step(s, odd, any);
     if (!second) lds_barrier();
     };
     if (wave >= WAVES / 2) turns(std::true_type{});
