@@ -98,7 +98,7 @@ def _empty(t, shape, dtype):
 def _like(t, name, dtype, shape):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if not t.is_cuda or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous GPU tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
