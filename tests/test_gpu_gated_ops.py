@@ -166,3 +166,77 @@ def test_the_example_runs(gpu):
     for kw in (dict(save="bf16"), dict(save="mxfp8"), dict(save="mxfp8", experts=4, choices=2)):
         losses = example.train(tokens=64, width=64, inner=72, steps=2, **kw)
         assert len(losses) == 2 and all(v == v and v < float("inf") for v in losses)
+
+
+def test_no_rows(gpu):
+    x, w, w2 = leaf(0, 136), leaf(144, 136, seed=1), leaf(200, 72, seed=2)
+    b, r = leaf(200, seed=3), leaf(0, 200, seed=4)
+    for save in ("bf16", "mxfp8"):
+        h = ops.gated_linear(x, w, None, None, "swiglu", "split", save)[0]
+        y = ops.feed_forward(x, w, w2, None, b, None, "swiglu", "split", save)[0]
+        assert h.shape == (0, 72) and y.shape == (0, 200)
+        for a, z in zip(torch.autograd.grad(h.sum() + y.sum(), (x, w, w2, b)), (x, w, w2, b)):
+            assert a.shape == z.shape and (a == 0).all()
+    z = ops.linear_fp8(h.detach().requires_grad_(True), w2, b, r)[0]
+    for a, t in zip(torch.autograd.grad(z.sum(), (w2, b, r)), (w2, b, r)):
+        assert a.shape == t.shape and (a == 0).all()
+    assert ops.glu_ckpt(leaf(0, 72), leaf(0, 72))[0].shape == (0, 72)
+
+
+def test_expanded_gradients_and_halves_of_one_tensor(gpu):
+    """The gradient of a sum has no strides; gate and up may be the halves of one projection."""
+    both, w, x = leaf(40, 144), leaf(144, 136, seed=1, scale=0.1), leaf(40, 136, seed=2)
+    ones = torch.ones(40, 72, device="cuda", dtype=BF16)
+    h = ops.glu_ckpt(*both.chunk(2, 1))[0]
+    assert torch.equal(torch.autograd.grad(h.sum(), both)[0], torch.autograd.grad(ops.glu_ckpt(*both.chunk(2, 1))[0], both, ones)[0])
+    for f in (lambda: ops.gated_linear(x, w)[0], lambda: ops.linear_fp8(x, w[:72])[0]):
+        for a, b in zip(torch.autograd.grad(f().sum(), (x, w)), torch.autograd.grad(f(), (x, w), ones)):
+            assert torch.equal(a, b)
+
+
+def test_offsets_out_of_range_are_taken_into_it(gpu):
+    x, w = n(40, 136), n(2, 144, 136, seed=1, scale=0.1)
+    far = torch.tensor([-7, 20, 10 ** 9], dtype=torch.int32, device="cuda")
+    near = torch.tensor([0, 20, 40], dtype=torch.int32, device="cuda")
+    dh = n(40, 72, seed=2)
+    q, _, s, _ = gpu.glu_quant_fp8(x)
+    wq, ws, _, _ = gpu.glu_quant_fp8_weight(w)
+    for save in ("bf16", "mxfp8"):
+        got, want = [], []
+        for out, off in ((got, far), (want, near)):
+            h, pre, extra = gpu.glu_gated_linear(x, w, offsets=off, save=save)
+            out += [h, pre, extra, *gpu.glu_gated_linear_bwd(dh, x, w, pre, extra, offsets=off, bias=True, need_h=True),
+                    gpu.glu_linear_fp8(q, s, wq, ws, offsets=off)]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("save", ["bf16", "mxfp8"])
+def test_a_captured_training_step(gpu, save):
+    """Forward and backward in one graph, replayed between eager work; the leaves have no eager graph."""
+    x, w13, w2 = leaf(150, 136), leaf(656, 136, seed=1, scale=0.1), leaf(136, 328, seed=2, scale=0.1)
+    w8, b8, d = leaf(136, 136, seed=3, scale=0.1), leaf(136, seed=4), n(150, 136, seed=5)
+    leaves = (x, w13, w2, w8, b8)
+
+    def step():
+        y = ops.feed_forward(x, w13, w2, None, None, None, "geglu", "paired", save)[0]
+        z = ops.linear_fp8(y, w8, b8, x)[0]
+        return (z.detach(), *torch.autograd.grad(z, leaves, d))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(2):
+            want = [t.clone() for t in step()]
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(3):
+        for o in out:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        n(300, 300) @ n(300, 300, seed=1)
+        torch.cuda.synchronize()
