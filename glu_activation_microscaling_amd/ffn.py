@@ -67,6 +67,27 @@ def _launch(t, name, *args):
         return _call(name, *args, _stream(t))
 
 
+# Makes a tensor on the current GPU; what compiled graphs make theirs with (0.8 us where new_empty takes 1.4).
+_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
+def _contiguous(shape, dtype):
+    if len(shape) == 2:
+        m, n = shape
+        return _strided((m, n), (n or 1, 1), dtype)   # tuples alone will do
+    stride = [1] * len(shape)
+    for i in range(len(shape) - 1, 0, -1):
+        stride[i - 1] = stride[i] * (shape[i] or 1)
+    return _strided(tuple(shape), tuple(stride), dtype)
+
+
+def _allocator(t):
+    """new(shape, dtype): uninitialised contiguous tensors on GPU tensor t's device."""
+    if _strided is None or _device is None or _device() != t.get_device():
+        return lambda shape, dtype: t.new_empty(shape, dtype=dtype)
+    return _contiguous
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr() or None   # an empty tensor's pointer is 0
 

@@ -9,11 +9,9 @@ include/glu_mx.h); every function is also a name of the package:
 Codes are uint8 (E4M3), scales float32.  Code rows are filled up with zero codes to a multiple of 16, so
 that each is the K of a product.  What is disabled comes back zero-sized (fixed arity).
 """
-import torch
-
-from . import ACT, LAYOUT, _flags, _operands
-from .ffn import _BF16, _F32, _I32, _launch, _like, _matrix, _one_row, _ptr, _same_device, _size
-from .gated import _U8, _choice
+from . import ACT, LAYOUT, _flags
+from .ffn import _BF16, _F32, _I32, _allocator, _launch, _like, _matrix, _ptr, _same_device, _size
+from .gated import _U8, _choice, _glu_operands
 
 W_SCALES = {"block": 0, "row": 1}
 
@@ -27,10 +25,12 @@ def _blocks(n):
 
 
 def _directions(t, M, N, rowwise, colwise):
+    new = _allocator(t)
+
     def pair(on, rows, cols):
         if not on:
-            return t.new_empty((0,), dtype=_U8), t.new_empty((0,), dtype=_F32)
-        return t.new_empty((rows, _padded(cols)), dtype=_U8), t.new_empty((_blocks(cols), rows), dtype=_F32)
+            return new((0,), _U8), new((0,), _F32)
+        return new((rows, _padded(cols)), _U8), new((_blocks(cols), rows), _F32)
     (q_row, s_row), (q_col, s_col) = pair(rowwise, M, N), pair(colwise, N, M)
     return q_row, q_col, s_row, s_col
 
@@ -51,10 +51,8 @@ def glu_quant_fp8(x, *, rowwise=True, colwise=False):
 def glu_fwd_fp8(gate, up=None, *, act="swiglu", layout="split", rowwise=True, colwise=False):
     """glu_quant_fp8 of h = bf16(act(gate) * up) without writing h: (q_row, q_col, s_row, s_col)."""
     a, lay, flags = _choice(act, ACT, "act"), _choice(layout, LAYOUT, "layout"), _flags(rowwise, colwise)
-    M, N, ld = _operands(gate, up, layout)
+    M, N, ld = _glu_operands(gate, up, layout)
     _same_device(gate, up)
-    if M == 1:
-        ld = _one_row(gate.shape[1])
     out = _directions(gate, M, N, rowwise, colwise)
     q_row, q_col, s_row, s_col = (_ptr(t) for t in out)
     _launch(gate, "glu_fwd_fp8", a, lay, flags, M, N, _ptr(gate), _ptr(up), ld, q_row, s_row, q_col, s_col)
@@ -68,12 +66,12 @@ def glu_quant_fp8_weight(w, *, transpose=False):
     if w.dim() not in (2, 3):
         raise ValueError("w must be [N, K] or [groups, N, K]")
     _like(w, "w", _BF16, w.shape)
-    lead, (N, K) = w.shape[:-2], w.shape[-2:]
+    lead, (N, K), new = w.shape[:-2], w.shape[-2:], _allocator(w)
 
     def pair(on, n, k):
         if not on:
-            return w.new_empty((0,), dtype=_U8), w.new_empty((0,), dtype=_F32)
-        return w.new_empty((*lead, n, _padded(k)), dtype=_U8), w.new_empty((*lead, _blocks(n), _blocks(k)), dtype=_F32)
+            return new((0,), _U8), new((0,), _F32)
+        return new((*lead, n, _padded(k)), _U8), new((*lead, _blocks(n), _blocks(k)), _F32)
     (q, s), (qt, st) = pair(True, N, K), pair(transpose, K, N)
     _launch(w, "glu_quant_fp8_weight", lead[0] if lead else 1, N, K, _ptr(w), _ptr(q), _ptr(s), _ptr(qt), _ptr(st))
     return q, s, qt, st
@@ -103,12 +101,13 @@ def glu_linear_fp8(xq, xs, wq, ws, bias=None, residual=None, *, w_scales="block"
         _like(offsets, "offsets", _I32, (groups + 1,))
     _same_device(xq, xs, wq, ws, bias, residual, offsets, out)
     ld_res = 0 if residual is None else _matrix(residual, "residual", _BF16, M, N)
+    new = _allocator(xq)
     if out is None:
-        y, ld_y = xq.new_empty((M, N), dtype=_BF16), N
+        y, ld_y = new((M, N), _BF16), N
     else:
         y, ld_y = out, _matrix(out, "out", _BF16, M, N)
     nbytes = _size("glu_linear_fp8_work_bytes", M, N, K, groups, int(offsets is not None))
-    work = xq.new_empty((nbytes,), dtype=_U8) if nbytes > 0 else None
+    work = new((nbytes,), _U8) if nbytes > 0 else None
     _launch(xq, "glu_linear_fp8", mode, M, N, K, groups, _ptr(offsets), _ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(bias),
             _ptr(residual), ld_res, _ptr(y), ld_y, _ptr(work), nbytes)
     return y

@@ -12,7 +12,7 @@ the call, on the current stream.
 import torch
 
 from . import ACT, LAYOUT, W_LAYOUT, _operands
-from .ffn import _BF16, _I32, _empty, _launch, _like, _matrix, _one_row, _ptr, _same_device, _size
+from .ffn import _BF16, _I32, _allocator, _launch, _like, _matrix, _ptr, _same_device, _size
 
 SAVE = {"none": 0, "bf16": 1, "mxfp8": 2}
 _U8 = torch.uint8
@@ -22,6 +22,20 @@ def _choice(value, table, name):
     if value not in table:
         raise ValueError(f"{name} must be one of {sorted(table)}")
     return table[value]
+
+
+def _glu_operands(gate, up, layout):
+    """(M, N, row stride) of the GLU's operands."""
+    ld = _matrix(gate, "gate", _BF16)
+    M, C = gate.shape
+    if layout == "paired":
+        if up is not None or C % 2:
+            _operands(gate, up, layout)   # says what is wrong
+        return M, C // 2, ld
+    if up is None or _matrix(up, "up", _BF16) != ld or up.shape != gate.shape:
+        _operands(gate, up, layout)
+        raise ValueError("gate and up must share a row stride")
+    return M, C, ld
 
 
 def _gated_setup(x, w, bias, offsets, act, w_layout):
@@ -55,16 +69,17 @@ def glu_gated_linear(x, w, bias=None, *, act="swiglu", w_layout="split", offsets
     a, layout, M, N, K, groups, ld_x = _gated_setup(x, w, bias, offsets, act, w_layout)
     keep = _choice(save, SAVE, "save")
     _same_device(x, w, bias, offsets, out)
+    new = _allocator(x)
     if out is None:
-        h, ld_h = x.new_empty((M, N)), N
+        h, ld_h = new((M, N), _BF16), N
     else:
         h, ld_h = out, _matrix(out, "out", _BF16, M, N)
     pre = extra = None
     if keep:
-        pre = x.new_empty((M, 2 * N), dtype=_BF16 if keep == 1 else _U8)
-        extra = x.new_empty((M, N if keep == 1 else _scale_columns(N)), dtype=_U8)
+        pre = new((M, 2 * N), _BF16 if keep == 1 else _U8)
+        extra = new((M, N if keep == 1 else _scale_columns(N)), _U8)
     nbytes = _size("glu_gated_linear_work_bytes", keep, M, N, K, groups, int(offsets is not None))
-    work = x.new_empty((nbytes,), dtype=_U8) if nbytes > 0 else None
+    work = new((nbytes,), _U8) if nbytes > 0 else None
     _launch(x, "glu_gated_linear", a, layout, keep, M, N, K, groups, _ptr(offsets), _ptr(x), ld_x, _ptr(w), _ptr(bias),
           _ptr(h), ld_h, _ptr(pre), _ptr(extra), _ptr(work), nbytes)
     return (h, pre, extra) if keep else h
@@ -86,12 +101,13 @@ def glu_gated_linear_bwd(dh, x, w, pre, extra=None, *, act="swiglu", w_layout="s
         raise ValueError("codes need their scales")
     _like(pre, "pre", _U8 if keep == 2 else _BF16, (M, 2 * N))
     _same_device(x, w, dh, pre, extra, offsets)
-    dx = _empty(x, (M, K), _BF16) if need_dx else x.new_empty((0,))
-    dw = torch.empty_like(w) if need_dw else x.new_empty((0,))
-    db = x.new_empty(w.shape[:-1] if bias else (0,))
-    h = x.new_empty((M, N) if need_h else (0,))
+    new = _allocator(x)
+    dx = new((M, K) if need_dx else (0,), _BF16)
+    dw = new(w.shape if need_dw else (0,), _BF16)
+    db = new(w.shape[:-1] if bias else (0,), _BF16)
+    h = new((M, N) if need_h else (0,), _BF16)
     nbytes = _size("glu_gated_linear_bwd_work_bytes", M, N, K, groups, int(offsets is not None), int(bias))
-    work = x.new_empty((nbytes,), dtype=_U8) if nbytes > 0 else None
+    work = new((nbytes,), _U8) if nbytes > 0 else None
     _launch(x, "glu_gated_linear_bwd", a, layout, keep, M, N, K, groups, _ptr(offsets), _ptr(dh), ld_dh, _ptr(x), ld_x,
           _ptr(w), _ptr(pre), _ptr(extra), _ptr(dx) if need_dx else None, K, _ptr(dw) if need_dw else None,
           _ptr(db) if bias else None, _ptr(h) if need_h else None, N, _ptr(work), nbytes)
@@ -103,19 +119,18 @@ def glu_fwd_ckpt(gate, up=None, *, act="swiglu", layout="split", need_h=True, ou
     and scales of [gate | up] that glu_bwd_ckpt takes in place of gate and up.  need_h=False leaves h
     zero-sized."""
     a, lay = _choice(act, ACT, "act"), _choice(layout, LAYOUT, "layout")
-    M, N, ld = _operands(gate, up, layout)
+    M, N, ld = _glu_operands(gate, up, layout)
     _same_device(gate, up, out)
-    if M == 1:
-        ld = _one_row(gate.shape[1])
+    new = _allocator(gate)
     if not need_h:
         if out is not None:
             raise ValueError("out is for h (need_h=True)")
-        h, ld_h = gate.new_empty((0,)), 0
+        h, ld_h = new((0,), _BF16), 0
     elif out is None:
-        h, ld_h = gate.new_empty((M, N)), N
+        h, ld_h = new((M, N), _BF16), N
     else:
         h, ld_h = out, _matrix(out, "out", _BF16, M, N)
-    q, s = gate.new_empty((M, 2 * N), dtype=_U8), gate.new_empty((M, _scale_columns(N)), dtype=_U8)
+    q, s = new((M, 2 * N), _U8), new((M, _scale_columns(N)), _U8)
     _launch(gate, "glu_fwd_ckpt", a, lay, M, N, _ptr(gate), _ptr(up), ld, _ptr(h) if need_h else None, ld_h, _ptr(q), _ptr(s))
     return h, q, s
 
@@ -130,10 +145,11 @@ def glu_bwd_ckpt(q, s, dh, *, act="swiglu", layout="split", need_h=False, out=No
     _like(q, "q", _U8, (M, 2 * N))
     _like(s, "s", _U8, (M, _scale_columns(N)))
     _same_device(dh, q, s, out)
+    new = _allocator(dh)
     if out is None:
-        d, ld_d = dh.new_empty((M, 2 * N)), 2 * N
+        d, ld_d = new((M, 2 * N), _BF16), 2 * N
     else:
         d, ld_d = out, _matrix(out, "out", _BF16, M, 2 * N)
-    h = dh.new_empty((M, N) if need_h else (0,))
+    h = new((M, N) if need_h else (0,), _BF16)
     _launch(dh, "glu_bwd_ckpt", a, lay, M, N, _ptr(q), _ptr(s), _ptr(dh), ld_dh, _ptr(d), ld_d, _ptr(h) if need_h else None, N)
     return d, h

@@ -249,3 +249,26 @@ def test_the_call_is_made_on_its_operands_device(monkeypatch):
     monkeypatch.setattr(ffn, "_device", lambda: 3)
     ffn._launch(Operand(), "f", 1, 2)
     assert log == [("f", (1, 2, ("stream", 3)))]
+
+
+def test_outputs_are_made_contiguous_and_on_their_operands_device(monkeypatch):
+    monkeypatch.setattr(ffn, "_strided", lambda *args: args)
+    for shape in ((0,), (5,), (0, 7), (7, 0), (3, 8), (2, 0, 4), (2, 3, 4), (0, 3, 0)):
+        for s in (shape, torch.Size(shape)):
+            got = ffn._contiguous(s, torch.uint8)
+            assert got == (shape, torch.empty(shape).stride(), torch.uint8) and type(got[0]) is type(got[1]) is tuple
+
+    class Operand:
+        def get_device(self):
+            return 3
+
+        def new_empty(self, shape, dtype):
+            return "its own", shape, dtype
+
+    monkeypatch.setattr(ffn, "_device", lambda: 3)
+    assert ffn._allocator(Operand()) is ffn._contiguous
+    monkeypatch.setattr(ffn, "_device", lambda: 0)
+    assert ffn._allocator(Operand())((4, 8), torch.uint8) == ("its own", (4, 8), torch.uint8)
+    monkeypatch.setattr(ffn, "_device", lambda: 3)
+    monkeypatch.setattr(ffn, "_strided", None)
+    assert ffn._allocator(Operand())((4, 8), torch.uint8) == ("its own", (4, 8), torch.uint8)
