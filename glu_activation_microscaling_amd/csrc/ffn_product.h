@@ -531,18 +531,20 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, int64_t group
 //
 // Bound by the matrix cores at large sizes; what is lost there is the start and the end of a tile,
 // which nothing overlaps (one workgroup fills a compute unit's LDS).  Measured on an MI355X:
-//   256x256  [16384, 7168, 2048] (I, J, K) alone 346 to 354 us (1.4 PFLOP/s), with bias, GELU, residual
-//            and saved pre-activation 434; gradient of x 329, of W 357; 8192^3 711 (1.55 PFLOP/s; 601 on zeros)
-//            16 groups, 16384 rows, [4096, 2048]: 267, gradients 266 and 274
-//            gated, [16384, 2 x 7168, 2048]: 800 with gate and up kept; 16 groups, 16384 rows, [2 x 2048, 2048]:
-//            290 with them kept as MXFP8; [968, 2 x 16384, 2048] 111 to 133
+//   256x256  [16384, 7168, 2048] (I, J, K) alone 343 to 354 us (1.4 PFLOP/s), with bias, GELU, residual
+//            and saved pre-activation 434 to 456; gradient of x 329 to 343, of W 357 to 378
+//            8192^3 711 (1.55 PFLOP/s; 601 on zeros)
+//            16 groups, 16384 rows, [4096, 2048]: 257 to 270, gradients 266 to 291 and 274 to 294
+//            gated, [16384, 2 x 7168, 2048]: 800 to 835 with gate and up kept (716 for the product alone); 16
+//            groups, 16384 rows, [2 x 2048, 2048]: 290 to 317 with them kept as MXFP8; [968, 2 x 16384, 2048] 110
 //   256x128  [968, 2048, 16384] in four parts 59 us (1.1 PFLOP/s), and 7 to join them
 //   128x128  [1021, 1000, 2056] in four parts 14.9 us, and 5.6 to join them
 //   32x128   32 groups, 256 rows, [2048, 2048], W from memory: 49 us (5.5 TB/s)
 // Tried and slower at [16384, 7168, 2048] (forward with epilogue, eight waves in step, 500 to 540 us): 128x128 tiles 637;
 // 4 waves of 128x128 798; four stages of 32 elements 558; two workgroups of 256x128 and three
 // stages of 32 a compute unit 581; workgroups that stay and load the next tile during the
-// epilogue 560.
+// epilogue 560.  With turns, workgroups that stay and start the next tile's loads before the epilogue
+// gain 1 to 4% over 14 rounds of the chip and lose 1 to 2% over 7 or fewer.
 template <int MODE, int ACT, int WI, int WJ, int TI, int TJ, int NS>
 __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE == 3>::type a,
                                                           uint32_t tiles_i, uint32_t tiles_j, uint32_t splits) {
@@ -1035,11 +1037,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // one round of workgroups (2048 to 8192 rows, sums of 1024 to 8192 elements), and what joining the
 // parts of a split sum takes.  The least total over the first three sizes decides.  Measured for
 // [I, J, K], 256x256 / 256x128 / 128x128:
-//   [ 1000, 1000, 1000]  22   / 15.8 / 11.2      [ 4096, 4096, 1024]  29.8 /  41.6 /  45.7
-//   [  968, 2048,16384]   278 / 65.8 / 72.0      [ 4096, 4096, 4096]  92.6 / 113.7 / 136.3
-//   [ 2048, 4096, 4096]  75   / 58.2 / 69.1      [16384, 2048, 2048]  98.6 /   126 /   151
-// (of 33 such shapes, with the largest tile's step at 1.29 us, the rule took the fastest of the three on 32
-// and was 0.5% behind on one).
+//   [ 1000, 1000, 1000]  22.5 / 15.8 / 11.2      [ 4096, 4096, 1024]  31.5 /  41.6 /  45.7
+//   [  968, 2048,16384]   237 / 65.8 / 72.0      [ 4096, 4096, 4096]  95.7 / 113.7 / 136.3
+//   [ 2048, 4096, 4096]  72.9 / 58.2 / 69.1      [16384, 2048, 2048]   102 /   126 /   151
+// (of 33 such shapes the rule takes the fastest of the three on 31 and is 0.5% and 6% behind on the others).
 constexpr int64_t kUnits = 256;
 constexpr double kStepUs[3] = {1.22, 0.85, 0.5}, kTileUs[3] = {15.0, 5.0, 4.0}, kJoinUs = 2.5, kJoinTBps = 8.0;
 constexpr int64_t kLeastPart = 512;   // elements of a split sum's part: 256 costs up to 5 us more, and gains 0.5

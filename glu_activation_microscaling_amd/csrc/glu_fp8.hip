@@ -83,7 +83,8 @@ __device__ __forceinline__ uint32_t row_top(uint32_t m) {
   return pkmax(m, dpp<0x121>(m));
 }
 
-// Rowwise alone.  grid: (256 columns, row blocks)
+// Rowwise alone.  Of the GLU of [8192, 2048] 16 us (84 MB, 5.2 TB/s), of [968, 16384] paired with tanh-GELU 16
+// (79 MB, 4.9 TB/s).  grid: (256 columns, row blocks)
 template <int SRC, int LAYOUT>
 __global__ __launch_bounds__(256) void k_fp8_row(Fp8QuantArgs a) {
   const int64_t col = 256 * (int64_t)blockIdx.x + 8 * (threadIdx.x & 31), ld_q = (a.N + 15) / 16 * 16;
@@ -100,6 +101,8 @@ __global__ __launch_bounds__(256) void k_fp8_row(Fp8QuantArgs a) {
 // A tile of 128 x 128: thread (lr, lc) has rows 8 lr .. + 7 and columns 8 lc .. + 7.
 //   ROW  codes of each row under the row's scale;  COL  of each column, transposed
 //   BLOCK  one scale for the tile, codes as they are and, with COL, transposed
+// Rows and columns of [16384, 7168] 109 to 114 us (477 MB, 4.3 TB/s: the tile is loaded, turned and stored one after
+// the other, and other workgroups fill the gaps), of [16384, 2048] 35 to 38, weights [7168, 2048] both ways 16 to 17.
 struct TileArgs {
   int64_t M, N, ld_in;
   const uint16_t* gate;

@@ -8,8 +8,8 @@
 // (ffn_product.h) with gate and up rows of W interleaved by 16 in LDS, so that a lane gets the
 // gate and the up value of the same outputs and the pre-activation need not reach memory.  For the
 // gradient it is kept as BF16, the type the GLU takes its operands in, with four more bits of each
-// value beside it, or as MXFP8 codes of BF16 values; the gradient is that of the GLU at the values kept.  dp is rounded to BF16 for the matrix
-// cores; dbias sums it unrounded.
+// value beside it, or as MXFP8 codes of BF16 values; the gradient is that of the GLU at the values
+// kept.  dp is rounded to BF16 for the matrix cores; dbias sums it unrounded.
 #include "ffn_product.h"
 #include "gated_launch.h"
 
@@ -61,7 +61,7 @@ __device__ __forceinline__ void finish_gated(const GatedArgs& a, int64_t group, 
 }
 
 // Joins the parts of split sums: eight outputs a thread, a row's chunks counted in whole fours, so that
-// four neighbouring lanes hold one block of 32.
+// four neighbouring lanes hold one block of 32.  Bound by its start: [1021, 1000] in two parts with codes 6.0 us.
 template <int ACT>
 __global__ __launch_bounds__(256) void k_gated_join(GatedArgs a, uint32_t splits) {
   const int64_t V = gated_columns(a.J), CP = (a.J + 31) / 32 * 4, all = a.I * CP;
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(256) void k_gated_join(GatedArgs a, uint32_t splits
 // Up to 8 rows of one group: a pass over W at memory speed, as the linear products' (k_few_rows): a wave
 // takes 8 rows of W of one kind straight from memory into 16 x 16 x 32 tiles whose other halves are
 // the same rows 32 elements on.  Of 2 KW waves that share 8 outputs, KW take the gates and KW the ups,
-// each kind cutting the sum among them; they meet in LDS.
+// each kind cutting the sum among them; they meet in LDS.  [1, 2 x 16384, 2048]: 26.5 us (134 MB, 5.1 TB/s).
 // grid: tiles of 8 outputs for 2 KW waves
 template <int ACT, int KW>
 __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_gated_few(GatedArgs a) {
@@ -175,7 +175,9 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_gated_few(GatedArgs a) {
 
 // ---- which kernel ----------------------------------------------------------------------------
 
-// The tile sizes of the linear products, each with waves of 64 columns of the sums (32 outputs).
+// The tile sizes of the linear products, each with waves of 64 columns of the sums (32 outputs).  The rule
+// counts the time of the products' loops, the same here ([1021, 2 x 1000, 2056] in two parts of 128 x 128: 18 us
+// and 6 to join them); the epilogue adds up to 6 us a 256 x 256 tile where gate and up are kept.
 constexpr TileShape kGatedShape[4] = {{2, 4, 8, 4, 2}, {4, 2, 4, 4, 3}, {4, 2, 2, 4, 3}, {2, 2, 1, 4, 4}};
 
 // Codes need whole blocks of 32 outputs, which the few rows' kernel does not have.

@@ -19,7 +19,7 @@ def exact(a, b):
     return a.to(F32) @ b.to(F32).t()
 
 
-# 256 x 256 tiles are taken for [4096, 4096] from 640 elements of the sum on
+# 256 x 256 tiles are taken for [4096, 4096] beyond 640 elements of the sum
 SUMS = [640, 648, 696, 704, 712, 768, 776, 832, 888, 896, 960, 1032]
 
 
