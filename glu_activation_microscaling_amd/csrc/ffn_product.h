@@ -445,66 +445,81 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, int64_t group
     for (int q = 0; q < 2; q++) *reinterpret_cast<u32x2*>(at + r * GATED_PITCH + 32 * q + 8 * g) = (u32x2){p[q][0], p[q][1]};
     return *reinterpret_cast<const u32x4*>(at + lrow * GATED_PITCH + 16 * (lane & 3u));
   };
+  // a loop for each kind of what is kept: instructions are what the epilogue takes its time for ([16384, 2 x 7168,
+  // 2048] with choices inside the loop 805 us, with a loop each 786)
+  auto finish_rows = [&](auto KEEP) {
+    constexpr bool has_pre = decltype(KEEP)::value == 1, has_codes = decltype(KEEP)::value == 2;
 #pragma unroll
-  for (int i = 0; i < TI; i++) {
-    const uint32_t first = 16u * FrA::tile(wi, i), row = first + lrow;
-    const bool ok = in && row < rows;
-    uint32_t H[2][2], G[2][2], U[2][2], ng[2], nu[2];
-#pragma unroll
-    for (int q = 0; q < 2; q++) {
-      float gate[4], up[4], h[4];
-#pragma unroll
-      for (int e = 0; e < 4; e++) {
-        gate[e] = acc[i][2 * q][e] + bg[q][e];
-        up[e] = acc[i][2 * q + 1][e] + bu[q][e];
-      }
-      glu_of<ACT>(h, gate, up);
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        H[q][e] = pack_bf16(h[2 * e], h[2 * e + 1]);
-        G[q][e] = has_pre ? wide_pair(gate[2 * e], gate[2 * e + 1]) : pack_bf16(gate[2 * e], gate[2 * e + 1]);
-        U[q][e] = has_pre ? wide_pair(up[2 * e], up[2 * e + 1]) : pack_bf16(up[2 * e], up[2 * e + 1]);
-      }
-      ng[q] = wide_rests(gate[0], gate[1], gate[2], gate[3]);
-      nu[q] = wide_rests(up[0], up[1], up[2], up[3]);
-    }
-    put16(through(mine, H), rh, ok ? 2u * (row * ld + col) : kOob);
-    if (has_pre) {
-      put16(through(mine + 16 * GATED_PITCH, G), rp, ok ? 2u * (row * 2u * N + col) : kOob);
-      put16(through(mine + 32 * GATED_PITCH, U), rp, ok ? 2u * (row * 2u * N + N + col) : kOob);
-      uint8_t* at = mine + 48 * GATED_PITCH;
+    for (int i = 0; i < TI; i++) {
+      const uint32_t first = 16u * FrA::tile(wi, i), row = first + lrow;
+      const bool ok = in && row < rows;
+      uint32_t H[2][2], G[2][2] = {}, U[2][2] = {}, ng[2], nu[2];
 #pragma unroll
       for (int q = 0; q < 2; q++) {
-        *reinterpret_cast<uint16_t*>(at + r * REST_PITCH + 8 * q + 2 * g) = (uint16_t)ng[q];
-        *reinterpret_cast<uint16_t*>(at + (16 + r) * REST_PITCH + 8 * q + 2 * g) = (uint16_t)nu[q];
-      }
-      // (read as vectors, which may alias the 16-bit stores)
-      const uint32_t wg = as_u32(*reinterpret_cast<const u16x2*>(at + lrow * REST_PITCH + 4 * (lane & 3u)));
-      const uint32_t wu = as_u32(*reinterpret_cast<const u16x2*>(at + (16 + lrow) * REST_PITCH + 4 * (lane & 3u)));
-      __builtin_amdgcn_raw_buffer_store_b32(wg, rn, ok ? row * N + col / 2u : kOob, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b32(wu, rn, ok ? row * N + N / 2u + col / 2u : kOob, 0, 0);
-    }
-    if (has_codes) {
-      const uint32_t g4[4] = {G[0][0], G[0][1], G[1][0], G[1][1]}, u4[4] = {U[0][0], U[0][1], U[1][0], U[1][1]};
-      uint32_t m = top_of(g4) | top_of(u4) << 16;   // over the row's four lanes
-      m = pkmax(m, swz_xor16(m));
-      m = pkmax(m, (uint32_t)__builtin_amdgcn_ds_bpermute((int)(4u * (lane ^ 32u)), (int)m));
-      const uint32_t sg = block_scale(lo16(m)), su = block_scale(hi16(m));
-      uint8_t* at = mine + 16 * GATED_PITCH;
+        float gate[4], up[4], h[4];
 #pragma unroll
-      for (int q = 0; q < 2; q++) {
-        *reinterpret_cast<uint32_t*>(at + r * 40 + 16 * q + 4 * g) = block_codes(G[q][0], G[q][1], sg);
-        *reinterpret_cast<uint32_t*>(at + 640 + r * 40 + 16 * q + 4 * g) = block_codes(U[q][0], U[q][1], su);
+        for (int e = 0; e < 4; e++) {
+          gate[e] = acc[i][2 * q][e] + bg[q][e];
+          up[e] = acc[i][2 * q + 1][e] + bu[q][e];
+        }
+        glu_of<ACT>(h, gate, up);
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          H[q][e] = pack_bf16(h[2 * e], h[2 * e + 1]);
+          if constexpr (has_pre) {
+            G[q][e] = wide_pair(gate[2 * e], gate[2 * e + 1]);
+            U[q][e] = wide_pair(up[2 * e], up[2 * e + 1]);
+          } else if constexpr (has_codes) {
+            G[q][e] = pack_bf16(gate[2 * e], gate[2 * e + 1]);
+            U[q][e] = pack_bf16(up[2 * e], up[2 * e + 1]);
+          }
+        }
+        if constexpr (has_pre) {
+          ng[q] = wide_rests(gate[0], gate[1], gate[2], gate[3]);
+          nu[q] = wide_rests(up[0], up[1], up[2], up[3]);
+        }
       }
-      const u32x2 cg = *reinterpret_cast<const u32x2*>(at + lrow * 40 + 8 * (lane & 3u));
-      const u32x2 cu = *reinterpret_cast<const u32x2*>(at + 640 + lrow * 40 + 8 * (lane & 3u));
-      __builtin_amdgcn_raw_buffer_store_b64(cg, rq, ok ? row * 2u * N + col : kOob, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b64(cu, rq, ok ? row * 2u * N + N + col : kOob, 0, 0);
-      const uint32_t at_s = any && g == 0 && first + r < rows ? (first + r) * 2u * NB + c0 / 32u : kOob;
-      __builtin_amdgcn_raw_buffer_store_b8((uint8_t)sg, rs, at_s, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b8((uint8_t)su, rs, at_s == kOob ? kOob : at_s + NB, 0, 0);
+      put16(through(mine, H), rh, ok ? 2u * (row * ld + col) : kOob);
+      if constexpr (has_pre) {
+        put16(through(mine + 16 * GATED_PITCH, G), rp, ok ? 2u * (row * 2u * N + col) : kOob);
+        put16(through(mine + 32 * GATED_PITCH, U), rp, ok ? 2u * (row * 2u * N + N + col) : kOob);
+        uint8_t* at = mine + 48 * GATED_PITCH;
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+          *reinterpret_cast<uint16_t*>(at + r * REST_PITCH + 8 * q + 2 * g) = (uint16_t)ng[q];
+          *reinterpret_cast<uint16_t*>(at + (16 + r) * REST_PITCH + 8 * q + 2 * g) = (uint16_t)nu[q];
+        }
+        // (read as vectors, which may alias the 16-bit stores)
+        const uint32_t wg = as_u32(*reinterpret_cast<const u16x2*>(at + lrow * REST_PITCH + 4 * (lane & 3u)));
+        const uint32_t wu = as_u32(*reinterpret_cast<const u16x2*>(at + (16 + lrow) * REST_PITCH + 4 * (lane & 3u)));
+        __builtin_amdgcn_raw_buffer_store_b32(wg, rn, ok ? row * N + col / 2u : kOob, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(wu, rn, ok ? row * N + N / 2u + col / 2u : kOob, 0, 0);
+      }
+      if constexpr (has_codes) {
+        const uint32_t g4[4] = {G[0][0], G[0][1], G[1][0], G[1][1]}, u4[4] = {U[0][0], U[0][1], U[1][0], U[1][1]};
+        uint32_t m = top_of(g4) | top_of(u4) << 16;   // over the row's four lanes
+        m = pkmax(m, swz_xor16(m));
+        m = pkmax(m, (uint32_t)__builtin_amdgcn_ds_bpermute((int)(4u * (lane ^ 32u)), (int)m));
+        const uint32_t sg = block_scale(lo16(m)), su = block_scale(hi16(m));
+        uint8_t* at = mine + 16 * GATED_PITCH;
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+          *reinterpret_cast<uint32_t*>(at + r * 40 + 16 * q + 4 * g) = block_codes(G[q][0], G[q][1], sg);
+          *reinterpret_cast<uint32_t*>(at + 640 + r * 40 + 16 * q + 4 * g) = block_codes(U[q][0], U[q][1], su);
+        }
+        const u32x2 cg = *reinterpret_cast<const u32x2*>(at + lrow * 40 + 8 * (lane & 3u));
+        const u32x2 cu = *reinterpret_cast<const u32x2*>(at + 640 + lrow * 40 + 8 * (lane & 3u));
+        __builtin_amdgcn_raw_buffer_store_b64(cg, rq, ok ? row * 2u * N + col : kOob, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(cu, rq, ok ? row * 2u * N + N + col : kOob, 0, 0);
+        const uint32_t at_s = any && g == 0 && first + r < rows ? (first + r) * 2u * NB + c0 / 32u : kOob;
+        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)sg, rs, at_s, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)su, rs, at_s == kOob ? kOob : at_s + NB, 0, 0);
+      }
     }
-  }
+  };
+  if (has_pre) finish_rows(std::integral_constant<int, 1>{});
+  else if (has_codes) finish_rows(std::integral_constant<int, 2>{});
+  else finish_rows(std::integral_constant<int, 0>{});
 }
 
 // ---- the tiled product -----------------------------------------------------------------------
@@ -535,8 +550,8 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, int64_t group
 //            and saved pre-activation 434 to 456; gradient of x 329 to 343, of W 357 to 378
 //            8192^3 711 (1.55 PFLOP/s; 601 on zeros)
 //            16 groups, 16384 rows, [4096, 2048]: 257 to 270, gradients 266 to 291 and 274 to 294
-//            gated, [16384, 2 x 7168, 2048]: 800 to 835 with gate and up kept (716 for the product alone); 16
-//            groups, 16384 rows, [2 x 2048, 2048]: 290 to 317 with them kept as MXFP8; [968, 2 x 16384, 2048] 110
+//            gated, [16384, 2 x 7168, 2048]: 770 to 786 with gate and up kept (716 for the product alone); 16
+//            groups, 16384 rows, [2 x 2048, 2048]: 268 to 285 with them kept as MXFP8; [968, 2 x 16384, 2048] 104
 //   256x128  [968, 2048, 16384] in four parts 59 us (1.1 PFLOP/s), and 7 to join them
 //   128x128  [1021, 1000, 2056] in four parts 14.9 us, and 5.6 to join them
 //   32x128   32 groups, 256 rows, [2048, 2048], W from memory: 49 us (5.5 TB/s)

@@ -177,7 +177,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_gated_few(GatedArgs a) {
 
 // The tile sizes of the linear products, each with waves of 64 columns of the sums (32 outputs).  The rule
 // counts the time of the products' loops, the same here ([1021, 2 x 1000, 2056] in two parts of 128 x 128: 18 us
-// and 6 to join them); the epilogue adds up to 6 us a 256 x 256 tile where gate and up are kept.
+// and 6 to join them); the epilogue adds up to 5 us a 256 x 256 tile where gate and up are kept.
 constexpr TileShape kGatedShape[4] = {{2, 4, 8, 4, 2}, {4, 2, 4, 4, 3}, {4, 2, 2, 4, 3}, {2, 2, 1, 4, 4}};
 
 // Codes need whole blocks of 32 outputs, which the few rows' kernel does not have.

@@ -28,10 +28,10 @@ __device__ __forceinline__ void glu_of(float (&h)[N], const float (&g)[N], const
 __device__ __forceinline__ uint32_t wide_pair(float a, float b) {   // two BF16
   return __builtin_amdgcn_perm(__float_as_uint(b) + 0x8800u, __float_as_uint(a) + 0x8800u, 0x07060302u);
 }
-__device__ __forceinline__ uint32_t wide_rest(float v) { return (__float_as_uint(v) + 0x800u) >> 12 & 15u; }   // a nibble
-// Four nibbles, the first lowest.
+// Four nibbles, the first lowest: bits 15 .. 12 of each value, moved to their places.
 __device__ __forceinline__ uint32_t wide_rests(float a, float b, float c, float d) {
-  return wide_rest(a) | wide_rest(b) << 4 | wide_rest(c) << 8 | wide_rest(d) << 12;
+  auto bits = [](float v) { return __float_as_uint(v) + 0x800u; };
+  return (bits(a) >> 12 & 0xfu) | (bits(b) >> 8 & 0xf0u) | (bits(c) >> 4 & 0xf00u) | (bits(d) & 0xf000u);
 }
 // The value of BF16 `hi` (in the upper half of a word whose lower half is zero) and nibble I of `rest`.
 template <int I>
