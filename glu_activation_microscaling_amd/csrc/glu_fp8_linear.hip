@@ -284,7 +284,7 @@ __global__ __launch_bounds__(512) void k_fp8_turns(Fp8Args a, uint32_t tiles_i, 
   static_assert(Op::LOADS == 4 && Scales::LOADS == 1);
   // A: two stages of both halves' rows; B's low columns: two, high columns: three; the scales likewise
   constexpr uint32_t HALF = Op::BYTES / 2, B_LOW = 4 * HALF, B_HIGH = 6 * HALF, S_ROWS = 9 * HALF, S_COLS = S_ROWS + 2048u;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[S_COLS + 3072u];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[S_COLS + 3 * 1024u];
   static_assert(sizeof(smem) <= 160 * 1024);
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
