@@ -560,10 +560,13 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, int64_t group
 // stages of 32 a compute unit 581; workgroups that stay and load the next tile during the
 // epilogue 560.  With turns, workgroups that stay and start the next tile's loads before the epilogue
 // gain 1 to 4% over 14 rounds of the chip and lose 1 to 2% over 7 or fewer.
+//
+// `block` of `blocks` is the workgroup's number among those of the product.
+template <int BI, int BJ, int NS>
+constexpr uint32_t kProductLds = (NS == 2 ? 2 * BI + BJ * 5 / 2 : NS * (BI + BJ)) * BK * 2;   // bytes
 template <int MODE, int ACT, int WI, int WJ, int TI, int TJ, int NS>
-__global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE == 3>::type a,
-                                                          uint32_t tiles_i, uint32_t tiles_j, uint32_t splits) {
-  static_assert(GATED == 3);
+__device__ __forceinline__ void product_tile(const typename ArgsOf<MODE == 3>::type& a, uint32_t tiles_i, uint32_t tiles_j,
+                                             uint32_t splits, uint32_t block, uint32_t blocks, uint8_t* smem) {
   constexpr bool TA = MODE == WGRAD, TB = MODE == DGRAD || MODE == WGRAD;
   constexpr int BI = 16 * WI * TI, BJ = 16 * WJ * TJ, WAVES = WI * WJ;
   constexpr bool TURNS = NS == 2;
@@ -571,8 +574,8 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
   constexpr int PARTS = TURNS ? 2 : 1;   // of the waves, and of the rows and columns they load
   using OpA = Operand<TA, BI / PARTS, WAVES / PARTS>;
   using OpB = std::conditional_t<MODE == GATED, GatedOperand<BJ / PARTS, WAVES / PARTS>, Operand<TB, BJ / PARTS, WAVES / PARTS>>;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[TURNS ? 4 * OpA::BYTES + 5 * OpB::BYTES
-                                                             : NS * (OpA::BYTES + OpB::BYTES)];
+  constexpr uint32_t LDS = kProductLds<BI, BJ, NS>;
+  static_assert(LDS == (TURNS ? 4 * OpA::BYTES + 5 * OpB::BYTES : NS * (OpA::BYTES + OpB::BYTES)));
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -580,13 +583,13 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
   // next column tile, so that the workgroups of one XCD share operands in its L2
   if (MODE != WGRAD && a.offsets != nullptr) {   // the grid allows for more row tiles than there are
     tiles_i = count_tiles(a.offsets, a.groups, a.I, BI);
-    if (blockIdx.x >= tiles_i * tiles_j) return;
+    if (block >= tiles_i * tiles_j) return;
   }
   const uint32_t per = tiles_i * tiles_j;
   // WGRAD of groups: their sums differ in length, so each XCD gets a share of every group's tiles
   const bool each = MODE == WGRAD && a.offsets != nullptr;
-  uint32_t b = blockIdx.x, outer = each ? b / per : 0u;   // WGRAD: group; with splits: part of the sum
-  b = xcd_run(b - outer * per, each ? per : MODE != WGRAD && a.offsets != nullptr ? per : gridDim.x);
+  uint32_t b = block, outer = each ? b / per : 0u;   // WGRAD: group; with splits: part of the sum
+  b = xcd_run(b - outer * per, each ? per : MODE != WGRAD && a.offsets != nullptr ? per : blocks);
   if (!each) {
     outer = b / per;
     b -= outer * per;
@@ -725,7 +728,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
       // partial step is the last one, unless every step may be partial (ANY).
       constexpr bool ANY = BI <= 32;
       const uint32_t steps = (k1 - k0 + BK - 1) / BK, whole = (k1 - k0) / BK;
-      const uint32_t turn = ANY || whole == steps ? (3u * (blockIdx.x % 8u) + (uint32_t)group) % steps : 0u;
+      const uint32_t turn = ANY || whole == steps ? (3u * (block % 8u) + (uint32_t)group) % steps : 0u;
       uint32_t k = k0 + turn * BK, left = steps;
       auto advance = [&] { k = k + BK < k1 ? k + BK : k0; };
       auto feed = [&](uint32_t at) {
@@ -861,7 +864,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
     return;
   }
   if constexpr (MODE == GATED) {
-    static_assert(WAVES * GATED_LDS <= sizeof(smem));
+    static_assert(WAVES * GATED_LDS <= LDS);
     gated_epilogue<ACT, TI, TJ, Rows>(a, group, t, j0 / 2, wi, wj, lane, smem + wave * GATED_LDS, acc);
     return;
   }
@@ -869,7 +872,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
   // consecutive columns of a row: 16-byte loads and stores.  (No wave reads the stages any
   // more: the last step's barrier comes after its last read.)
   constexpr uint32_t PITCH = 16 * TJ + 4, CH = 2 * TJ, ROWS = 64 / CH, PASSES = 16 / ROWS;   // floats; lanes a row
-  static_assert(WAVES * 16 * PITCH * 4 <= sizeof(smem));
+  static_assert(WAVES * 16 * PITCH * 4 <= LDS);
   float* const mine = reinterpret_cast<float*>(smem) + wave * (16 * PITCH);
   const uint32_t cc = 8u * (lane % CH), lrow = lane / CH;
   const uint32_t col = 16u * Cols::tile(wj, cc / 16) + cc % 16u;
@@ -932,6 +935,27 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
       put16(pack_row(v), rc, place(ld_c, i, p));
     }
   }
+}
+
+template <int MODE, int ACT, int WI, int WJ, int TI, int TJ, int NS>
+__global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE == 3>::type a,
+                                                          uint32_t tiles_i, uint32_t tiles_j, uint32_t splits) {
+  static_assert(GATED == 3);
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kProductLds<16 * WI * TI, 16 * WJ * TJ, NS>];
+  product_tile<MODE, ACT, WI, WJ, TI, TJ, NS>(a, tiles_i, tiles_j, splits, blockIdx.x, gridDim.x, smem);
+}
+
+// Both gradients of a product without groups, each whole in its own workgroups: dx = dp W in the first ones, filled
+// up to a multiple of 8 so that the rest, dW = dp^T x, start on the first XCD too.
+template <int WI, int WJ, int TI, int TJ, int NS>
+__global__ __launch_bounds__(64 * WI * WJ) void k_gradients(ProductArgs d, uint32_t d_i, uint32_t d_j, ProductArgs w,
+                                                            uint32_t w_i, uint32_t w_j) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kProductLds<16 * WI * TI, 16 * WJ * TJ, NS>];
+  const uint32_t nd = d_i * d_j, first = (nd + 7u) / 8u * 8u;
+  if (blockIdx.x >= first)
+    product_tile<WGRAD, LIN_NONE, WI, WJ, TI, TJ, NS>(w, w_i, w_j, 1, blockIdx.x - first, w_i * w_j, smem);
+  else if (blockIdx.x < nd)
+    product_tile<DGRAD, LIN_NONE, WI, WJ, TI, TJ, NS>(d, d_i, d_j, 1, blockIdx.x, nd, smem);
 }
 
 // Joins the parts of split sums and finishes them: eight columns a thread, the parts in order.
@@ -1044,6 +1068,7 @@ struct ProductPlan {
   int kind;
   int64_t share;             // FEW: waves sharing a sum
   int64_t tiles_i, tiles_j, splits;
+  double us;                 // the rule's estimate, of the tiled ones
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1110,7 +1135,40 @@ ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t grou
       p.splits = splits;
     }
   }
+  p.us = best;
   return p;
+}
+
+// Both gradients in one launch, for x [M, K] and dp [M, N] without groups: when all tiles of both run at once and
+// that is estimated to take less than one product after the other.  The tiles' kind, or -1.  Measured for [M, N, K], in
+// a graph, one after the other / together: [256, 512, 512] 12.1 / 6.7 us, [1000, 1000, 1000] 21.2 / 11.7, [2048, 1024,
+// 1024] 40.5 / 19.0, [1021, 2000, 2056] 38.5 / 31.3, [3000, 1000, 1000] 31.6 / 27.1; of 17 such shapes none was
+// slower together where the rule said so.
+constexpr double kLaunchUs = 2.0;
+int plan_gradients(int64_t M, int64_t N, int64_t K) {
+  if (M == 0 || N == 0 || K == 0) return -1;
+  double best = plan_product(DGRAD, M, K, N, 1, false).us + plan_product(WGRAD, N, K, M, 1, false).us + kLaunchUs;
+  int kind = -1;
+  for (int k = TILE_256_128; k <= TILE_128; k++) {
+    const int64_t rows = kShape[k].rows(), j = ceil_div(K, kShape[k].cols());
+    if (ceil_div(M, rows) * j + ceil_div(N, rows) * j > kUnits) continue;
+    const double us = kTileUs[k] + kStepUs[k] * ceil_div(M > N ? M : N, BK);
+    if (us < best) {
+      best = us;
+      kind = k;
+    }
+  }
+  return kind;
+}
+
+hipError_t launch_gradients(int kind, const ProductArgs& d, const ProductArgs& w, hipStream_t s) {
+  auto go = [&](auto KIND) {
+    constexpr TileShape t = kShape[decltype(KIND)::value];
+    const int64_t j = ceil_div(d.J, t.cols()), di = ceil_div(d.I, t.rows()), wi = ceil_div(w.I, t.rows());
+    return launch_kernel(k_gradients<t.wi, t.wj, t.ti, t.tj, t.stages>, dim3((unsigned)((di * j + 7) / 8 * 8 + wi * j)),
+                         dim3(64 * t.wi * t.wj), s, d, (uint32_t)di, (uint32_t)j, w, (uint32_t)wi, (uint32_t)j);
+  };
+  return kind == TILE_128 ? go(std::integral_constant<int, TILE_128>{}) : go(std::integral_constant<int, TILE_256_128>{});
 }
 
 int64_t product_work_bytes(int mode, int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped) {

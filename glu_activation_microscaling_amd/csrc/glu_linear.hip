@@ -138,16 +138,16 @@ hipError_t launch_linear_bwd(const LinearBwdArgs& a, hipStream_t s) {
     }
   }
   float* split = (float*)(a.work + w.dp + w.sums);
-  if (st == hipSuccess && a.dx != nullptr) {
-    const ProductArgs p{a.M, a.K, a.N, a.groups, a.offsets, dp, ld_dp, a.w, a.K, a.N * a.K, a.dx, a.ld_dx, 0,
-                        nullptr, nullptr, 0, nullptr, split};
-    st = launch_product<DGRAD, LIN_NONE>(p, s);
+  const ProductArgs to_dx{a.M, a.K, a.N, a.groups, a.offsets, dp, ld_dp, a.w, a.K, a.N * a.K, a.dx, a.ld_dx, 0,
+                          nullptr, nullptr, 0, nullptr, split};
+  const ProductArgs to_dw{a.N, a.K, a.M, a.groups, a.offsets, dp, ld_dp, a.x, a.ld_x, 0, a.dw, a.K, a.N * a.K,
+                          nullptr, nullptr, 0, nullptr, split};
+  if (st == hipSuccess && a.dx != nullptr && a.dw != nullptr && a.offsets == nullptr) {
+    const int kind = plan_gradients(a.M, a.N, a.K);
+    if (kind >= 0) return launch_gradients(kind, to_dx, to_dw, s);
   }
-  if (st == hipSuccess && a.dw != nullptr) {
-    const ProductArgs p{a.N, a.K, a.M, a.groups, a.offsets, dp, ld_dp, a.x, a.ld_x, 0, a.dw, a.K, a.N * a.K,
-                        nullptr, nullptr, 0, nullptr, split};
-    st = launch_product<WGRAD, LIN_NONE>(p, s);
-  }
+  if (st == hipSuccess && a.dx != nullptr) st = launch_product<DGRAD, LIN_NONE>(to_dx, s);
+  if (st == hipSuccess && a.dw != nullptr) st = launch_product<WGRAD, LIN_NONE>(to_dw, s);
   return st;
 }
 

@@ -34,6 +34,22 @@ def test_linear(gpu, K):
     assert torch.equal(dw, exact(a, b).to(BF16))
 
 
+# both gradients in one launch, of either tile size, their tiles not a multiple of 8 and ending anywhere, sums of a
+# few elements to thirty-two steps; the last two take a launch each
+@pytest.mark.parametrize("M,N,K", [(8, 8, 8), (1, 64, 128), (40, 1000, 264), (129, 72, 1032), (500, 520, 640), (1000, 712, 904),
+                                   (1021, 1000, 2056), (1021, 2000, 2056), (704, 704, 2800), (2048, 1024, 1024), (2000, 2000, 2000),
+                                   (4096, 512, 512), (300, 4096, 512)])
+def test_both_gradients(gpu, M, N, K):
+    dy, x, w = ints(M, N, seed=1), ints(M, K, seed=2), ints(N, K, seed=3)
+    db = dy.to(F32).sum(0).to(BF16)
+    dx, dw, got = gpu.glu_linear_bwd(dy, x, w, bias=True)
+    assert torch.equal(dx, exact(dy, w.t()).to(BF16)) and torch.equal(dw, exact(dy.t(), x.t()).to(BF16))
+    assert torch.equal(got, db)
+    one, _, _ = gpu.glu_linear_bwd(dy, x, w, need_dw=False)
+    _, other, _ = gpu.glu_linear_bwd(dy, x, w, need_dx=False)
+    assert torch.equal(dx, one) and torch.equal(dw, other)
+
+
 @pytest.mark.parametrize("K", SUMS)
 @pytest.mark.parametrize("layout", ["split", "paired"])
 def test_gated(gpu, K, layout):
