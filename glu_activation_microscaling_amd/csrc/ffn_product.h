@@ -1082,8 +1082,31 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //   [ 2048, 4096, 4096]  72.9 / 58.2 / 69.1      [16384, 2048, 2048]   102 /   126 /   151
 // (of 33 such shapes the rule takes the fastest of the three on 31 and is 0.5% and 6% behind on the others).
 constexpr int64_t kUnits = 256;
-constexpr double kStepUs[3] = {1.22, 0.85, 0.5}, kTileUs[3] = {15.0, 5.0, 4.0}, kJoinUs = 2.5, kJoinTBps = 8.0;
+constexpr double kStepUs[3] = {1.22, 0.85, 0.5}, kTileUs[3] = {15.0, 5.0, 4.0}, kJoinUs = 2.5, kJoinTBps = 5.0;
+constexpr double kStepFewUs[3] = {1.22, 0.85, 0.41};   // of a step while at most half the chip works
 constexpr int64_t kLeastPart = 512;   // elements of a split sum's part: 256 costs up to 5 us more, and gains 0.5
+
+// The number of parts of a sum that takes the least time by these figures: one, a power of two or the most, at
+// least kLeastPart elements each and one round of workgroups in all.  Measured in a graph, 128 x 128 tiles, the most
+// parts / the rule's: [2048, 1024, 1024] 20.2 (2) / 10.6 us (1), [512, 2048, 2048] 20.4 (4) / 17.7 (2; 16.0 whole),
+// [968, 2048, 2048] 20.3 (2) / 16.8 (1), [1021, 1000, 2056] 20.2 (4) / 18.6 (2; 22.9 whole), [1024, 1024, 4096] 20.0 (4)
+// / the same (26 whole).
+struct Parts {
+  int64_t splits;
+  double us;
+};
+Parts best_parts(int kind, int64_t tiles, int64_t K, int64_t steps, int64_t outputs, bool whole) {
+  const int64_t fit = whole ? 1 : K / kLeastPart < kUnits / tiles ? K / kLeastPart : kUnits / tiles, most = fit < 1 ? 1 : fit;
+  Parts best{0, 0.0};
+  for (int64_t splits = 1;;) {
+    const double step = tiles * splits <= kUnits / 2 ? kStepFewUs[kind] : kStepUs[kind];
+    double us = (kTileUs[kind] + step * ceil_div(steps, splits)) * ceil_div(tiles * splits, kUnits);
+    if (splits > 1) us += kJoinUs + 8e-6 / kJoinTBps * splits * outputs;
+    if (best.splits == 0 || us < best.us) best = {splits, us};
+    if (splits == most) return best;
+    splits = 2 * splits < most ? 2 * splits : most;
+  }
+}
 
 // A rule on extents alone, so that the scratch memory of split sums can be sized before the
 // launch.
@@ -1118,21 +1141,13 @@ ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t grou
   for (int kind = TILE_256; kind <= TILE_128; kind++) {
     const int64_t ti = ceil_div(I, kShape[kind].rows()), tj = ceil_div(J, kShape[kind].cols());
     const int64_t tiles = (ti + (cut ? groups / 2 : 0)) * tj * outer;
-    int64_t splits = 1;
-    if (!grouped && kind != TILE_256) {
-      const int64_t most = K / kLeastPart, want = kUnits / tiles;
-      splits = want < most ? want : most;
-      if (splits < 1) splits = 1;
-    }
-    const double round = kTileUs[kind] + kStepUs[kind] * ceil_div(steps, splits);
-    double us = round * ceil_div(tiles * splits, kUnits);
-    if (splits > 1) us += kJoinUs + 8e-6 / kJoinTBps * splits * I * J;
-    if (best == 0.0 || us < best) {
-      best = us;
+    const Parts parts = best_parts(kind, tiles, K, steps, I * J, grouped || kind == TILE_256);
+    if (best == 0.0 || parts.us < best) {
+      best = parts.us;
       p.kind = kind;
       p.tiles_i = ti + extra;
       p.tiles_j = tj;
-      p.splits = splits;
+      p.splits = parts.splits;
     }
   }
   p.us = best;
@@ -1141,18 +1156,19 @@ ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t grou
 
 // Both gradients in one launch, for x [M, K] and dp [M, N] without groups: when all tiles of both run at once and
 // that is estimated to take less than one product after the other.  The tiles' kind, or -1.  Measured for [M, N, K], in
-// a graph, one after the other / together: [256, 512, 512] 12.1 / 6.7 us, [1000, 1000, 1000] 21.2 / 11.7, [2048, 1024,
-// 1024] 40.5 / 19.0, [1021, 2000, 2056] 38.5 / 31.3, [3000, 1000, 1000] 31.6 / 27.1; of 17 such shapes none was
+// a graph, one after the other / together: [256, 512, 512] 12.1 / 6.7 us, [1000, 1000, 1000] 21.2 / 11.7, [1024, 2048,
+// 2048] 30.4 / 26.8, [1021, 2000, 2056] 38.5 / 31.3, [3000, 1000, 1000] 31.6 / 27.1; of 17 such shapes none was
 // slower together where the rule said so.
-constexpr double kLaunchUs = 2.0;
+constexpr double kLaunchUs = 3.5;   // a launch and the gap before it
 int plan_gradients(int64_t M, int64_t N, int64_t K) {
   if (M == 0 || N == 0 || K == 0) return -1;
   double best = plan_product(DGRAD, M, K, N, 1, false).us + plan_product(WGRAD, N, K, M, 1, false).us + kLaunchUs;
   int kind = -1;
   for (int k = TILE_256_128; k <= TILE_128; k++) {
     const int64_t rows = kShape[k].rows(), j = ceil_div(K, kShape[k].cols());
-    if (ceil_div(M, rows) * j + ceil_div(N, rows) * j > kUnits) continue;
-    const double us = kTileUs[k] + kStepUs[k] * ceil_div(M > N ? M : N, BK);
+    const int64_t tiles = ceil_div(M, rows) * j + ceil_div(N, rows) * j;
+    if (tiles > kUnits) continue;
+    const double us = kTileUs[k] + (tiles <= kUnits / 2 ? kStepFewUs[k] : kStepUs[k]) * ceil_div(M > N ? M : N, BK);
     if (us < best) {
       best = us;
       kind = k;

@@ -550,7 +550,8 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_fp8_few(Fp8Args a) {
 //   [  968, 2048,16384]  50.5 (8) / 49.8 (4) / 54.4 (2)   [16384, 2048, 2048]  69.6 / 88.4 / 110
 //   [ 2048, 4096, 4096]  49.0 / 41.4 / 49.3           16 groups [8192, 4096, 2048]  102 / 122 / 139
 constexpr TileShape kFp8Shape[4] = {{2, 4, 8, 4, 2}, {4, 2, 4, 4, 3}, {2, 4, 4, 2, 3}, {1, 4, 2, 2, 4}};
-constexpr double kFp8StepUs[3] = {1.55, 1.05, 0.70}, kFp8TileUs[3] = {10.0, 6.0, 3.5}, kFp8JoinUs = 5.0;
+constexpr double kFp8StepUs[3] = {1.55, 1.05, 0.70}, kFp8TileUs[3] = {10.0, 6.0, 3.5}, kFp8JoinUs = 5.0,
+                 kFp8JoinTBps = 8.0;
 constexpr int64_t kFp8LeastPart = 8;   // blocks of a split sum's part
 
 int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -582,7 +583,7 @@ ProductPlan plan_fp8(int64_t I, int64_t J, int64_t K, int64_t groups, bool group
     for (int q = 0; q < (most > 1 ? 2 : 1); q++) {   // one part, or the most
       const int64_t splits = q == 0 ? 1 : most;
       double us = (kFp8TileUs[kind] + kFp8StepUs[kind] * ceil_div(blocks, splits)) * ceil_div(tiles * splits, kUnits);
-      if (splits > 1) us += kFp8JoinUs + 8e-6 / kJoinTBps * splits * I * J;
+      if (splits > 1) us += kFp8JoinUs + 8e-6 / kFp8JoinTBps * splits * I * J;
       if (best == 0.0 || us < best) {
         best = us;
         p.kind = kind;

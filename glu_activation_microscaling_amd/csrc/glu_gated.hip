@@ -205,20 +205,13 @@ ProductPlan plan_gated(int save, int64_t I, int64_t N, int64_t K, int64_t groups
   for (int kind = TILE_256; kind <= TILE_128; kind++) {
     const int64_t ti = ceil_div(I, kGatedShape[kind].rows()), tj = ceil_div(J, kGatedShape[kind].cols());
     const int64_t tiles = (ti + (grouped ? groups / 2 : 0)) * tj;
-    int64_t splits = 1;
-    if (!grouped && kind != TILE_256) {
-      const int64_t most = K / kLeastPart, want = kUnits / tiles;
-      splits = want < most ? want : most;
-      if (splits < 1) splits = 1;
-    }
-    double us = (kTileUs[kind] + kStepUs[kind] * ceil_div(steps, splits)) * ceil_div(tiles * splits, kUnits);
-    if (splits > 1) us += kJoinUs + 8e-6 / kJoinTBps * splits * I * J;
-    if (best == 0.0 || us < best) {
-      best = us;
+    const Parts parts = best_parts(kind, tiles, K, steps, I * J, grouped || kind == TILE_256);
+    if (best == 0.0 || parts.us < best) {
+      best = parts.us;
       p.kind = kind;
       p.tiles_i = ti + extra;
       p.tiles_j = tj;
-      p.splits = splits;
+      p.splits = parts.splits;
     }
   }
   return p;
