@@ -553,7 +553,8 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, int64_t group
 //            gated, [16384, 2 x 7168, 2048]: 770 to 786 with gate and up kept (716 for the product alone); 16
 //            groups, 16384 rows, [2 x 2048, 2048]: 268 to 285 with them kept as MXFP8; [968, 2 x 16384, 2048] 104
 //   256x128  [968, 2048, 16384] in four parts 59 us (1.1 PFLOP/s), and 7 to join them
-//   128x128  [1021, 1000, 2056] in four parts 14.9 us, and 5.6 to join them
+//   128x128  [1021, 1000, 2056] in two parts 16.0 us, and 4.4 to join them
+//   both gradients of it in one launch of 256x128 tiles 20.5 us (one after the other 14.6 and 13.8)
 //   32x128   32 groups, 256 rows, [2048, 2048], W from memory: 49 us (5.5 TB/s)
 // Tried and slower at [16384, 7168, 2048] (forward with epilogue, eight waves in step, 500 to 540 us): 128x128 tiles 637;
 // 4 waves of 128x128 798; four stages of 32 elements 558; two workgroups of 256x128 and three

@@ -61,7 +61,8 @@ __device__ __forceinline__ void finish_gated(const GatedArgs& a, int64_t group, 
 }
 
 // Joins the parts of split sums: eight outputs a thread, a row's chunks counted in whole fours, so that
-// four neighbouring lanes hold one block of 32.  Bound by its start: [1021, 1000] in two parts with codes 6.0 us.
+// four neighbouring lanes hold one block of 32.  Bound by its start and
+// the parts, which are in the caches: [1021, 1000] in two parts with codes 6.0 us.
 template <int ACT>
 __global__ __launch_bounds__(256) void k_gated_join(GatedArgs a, uint32_t splits) {
   const int64_t V = gated_columns(a.J), CP = (a.J + 31) / 32 * 4, all = a.I * CP;
@@ -176,8 +177,8 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_gated_few(GatedArgs a) {
 // ---- which kernel ----------------------------------------------------------------------------
 
 // The tile sizes of the linear products, each with waves of 64 columns of the sums (32 outputs).  The rule
-// counts the time of the products' loops, the same here ([1021, 2 x 1000, 2056] in two parts of 128 x 128: 18 us
-// and 6 to join them); the epilogue adds up to 5 us a 256 x 256 tile where gate and up are kept.
+// counts the time of the products' loops, the same here ([1021, 2 x 1000, 2056] 128 x 128 in one piece 26 us, in two
+// parts 18 and 6 to join them); the epilogue adds up to 5 us a 256 x 256 tile where gate and up are kept.
 constexpr TileShape kGatedShape[4] = {{2, 4, 8, 4, 2}, {4, 2, 4, 4, 3}, {4, 2, 2, 4, 3}, {2, 2, 1, 4, 4}};
 
 // Codes need whole blocks of 32 outputs, which the few rows' kernel does not have.
