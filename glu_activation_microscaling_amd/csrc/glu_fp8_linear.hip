@@ -17,7 +17,6 @@ namespace glu {
 namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr uint32_t CODES = 128;   // codes a step, one line of an operand row and one block of scales
 
