@@ -21,7 +21,9 @@ using glu::status_of;
 
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
 constexpr int64_t kMaxQuantWidth = (int64_t)1 << 28;   // one workgroup per 256 columns
-constexpr int64_t kMaxWidth = (int64_t)1 << 20;        // N and K of a product
+constexpr int64_t kMaxWidth = (int64_t)1 << 20;        // N of a product, and K where W is quantized by blocks
+constexpr int64_t kMaxRowSum = (int64_t)1 << 22;       // K by rows, the rows of x in W's gradient: 256 code rows stay
+                                                       // within 32-bit offsets
 
 // Outputs of a quantizer: the pointers that go with the flags.
 glu_status check_directions(int flags, const uint8_t* q_row, const float* s_row, const uint8_t* q_col, const float* s_col) {
@@ -55,7 +57,8 @@ glu_status check_quant(bool glu_of, bool paired, int flags, int64_t M, int64_t N
 glu_status check_fp8_shape(int w_scales, int64_t M, int64_t N, int64_t K, int64_t groups, bool grouped) {
   if (w_scales != GLU_FP8_W_BLOCK && w_scales != GLU_FP8_W_ROW) return GLU_ERR_ARG;
   if (M < 0 || N < 0 || K < 0 || groups < 1 || M > kMaxRows || groups > glu::kMaxExperts) return GLU_ERR_SHAPE;
-  if (N % 8 != 0 || K % 16 != 0 || N > kMaxWidth || K > kMaxWidth) return GLU_ERR_SHAPE;
+  if (N % 8 != 0 || K % 16 != 0 || N > kMaxWidth) return GLU_ERR_SHAPE;
+  if (K > (w_scales == GLU_FP8_W_BLOCK ? kMaxWidth : kMaxRowSum)) return GLU_ERR_SHAPE;
   return grouped || groups == 1 ? GLU_OK : GLU_ERR_NULL;
 }
 
@@ -121,7 +124,7 @@ glu_status glu_quant_fp8_weight(int64_t groups, int64_t N, int64_t K, const uint
 }
 
 int64_t glu_linear_fp8_work_bytes(int64_t M, int64_t N, int64_t K, int64_t groups, int grouped) {
-  if (check_fp8_shape(GLU_FP8_W_BLOCK, M, N, K, groups, grouped != 0) != GLU_OK) return -1;
+  if (check_fp8_shape(GLU_FP8_W_ROW, M, N, K, groups, grouped != 0) != GLU_OK) return -1;
   return glu::fp8_linear_work_bytes(M, N, K, groups, grouped != 0);
 }
 

@@ -711,6 +711,11 @@ def _(xq, xs, wq, ws, bias=None, residual=None, offsets=None, w_scales="block"):
 # A linear layer whose three products run in 8 bits.  For the backward it keeps x quantized along its rows'
 # number (colwise) and W transposed, both as codes.  The gradients are those of the product at what the
 # codes of x and W stand for, with dy quantized too; the bias's is the sum of dy, the residual's dy itself.
+# W's gradient sums over the rows of x, of which the product takes _MAX_ROW_SUM: a call that will want it of
+# more rows is refused when it is made, not in its backward.
+
+_MAX_ROW_SUM = 1 << 22
+
 
 @torch.library.custom_op(f"{_LIB}::linear_fp8", mutates_args=())
 def linear_fp8(x: Tensor, w: Tensor, bias: Optional[Tensor] = None,
@@ -750,6 +755,8 @@ def _(dy, xq, xs, wq, ws, need_dx=True, need_dw=True, bias=False):
 
 
 def _fp8_setup(ctx, inputs, output):
+    if ctx.needs_input_grad[1] and inputs[0].shape[0] > _MAX_ROW_SUM:
+        raise ValueError(f"x must have at most {_MAX_ROW_SUM} rows for the gradient of w, got {inputs[0].shape[0]}")
     ctx.save_for_backward(*output[1:])
     ctx.mark_non_differentiable(*output[1:])
 

@@ -532,7 +532,8 @@ glu_status glu_quant_fp8_weight(int64_t groups, int64_t N, int64_t K, const uint
  * xq [M, K], xs [K/128, M]; wq [groups, N, K]; ws [groups, N/128, K/128] (GLU_FP8_W_BLOCK) or [groups,
  * K/128, N] (GLU_FP8_W_ROW: W was quantized along the sum); bias [groups, N] or NULL, residual [M, N] or
  * NULL, BF16; offsets and groups as for glu_linear.  K, the length of a code row, is a multiple of 16 up
- * to 2^20, N a multiple of 8 up to 2^20; row strides of y and residual multiples of 8 up to 2^21.
+ * to 2^20 (GLU_FP8_W_ROW: up to 2^22, for dW of that many rows), N a multiple of 8 up to 2^20; row strides of
+ * y and residual multiples of 8 up to 2^21.
  * The gradients are products of the same kind: dx of dy (rowwise) and wt, dW of dy and x (both colwise,
  * GLU_FP8_W_ROW). */
 enum { GLU_FP8_W_BLOCK = 0, GLU_FP8_W_ROW = 1 };
