@@ -726,10 +726,13 @@ __device__ __forceinline__ void product_tile(const typename ArgsOf<MODE == 3>::t
       // read the same columns of many rows meet in few memory channels when the rows are a power of
       // two apart; each XCD and group starts elsewhere (within an XCD the workgroups stay together,
       // for what they share in its L2).  32 groups of [8, 2048] x [2048, 2048]: 65 -> 50 us.  A
-      // partial step is the last one, unless every step may be partial (ANY).
+      // partial step is the last one, unless every step may be partial (ANY).  Gradients without groups
+      // begin at the beginning, so that their bits do not depend on the tile size, which in turn may depend on
+      // whether the other gradient is formed too; of 26 shapes none took longer so.
       constexpr bool ANY = BI <= 32;
       const uint32_t steps = (k1 - k0 + BK - 1) / BK, whole = (k1 - k0) / BK;
-      const uint32_t turn = ANY || whole == steps ? (3u * (block % 8u) + (uint32_t)group) % steps : 0u;
+      const bool turned = (ANY || whole == steps) && ((MODE != DGRAD && MODE != WGRAD) || a.offsets != nullptr);
+      const uint32_t turn = turned ? (3u * (block % 8u) + (uint32_t)group) % steps : 0u;
       uint32_t k = k0 + turn * BK, left = steps;
       auto advance = [&] { k = k + BK < k1 ? k + BK : k0; };
       auto feed = [&](uint32_t at) {
@@ -1110,8 +1113,8 @@ Parts best_parts(int kind, int64_t tiles, int64_t K, int64_t steps, int64_t outp
 }
 
 // A rule on extents alone, so that the scratch memory of split sums can be sized before the
-// launch.
-ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped) {
+// launch.  whole: sums are not cut.
+ProductPlan plan_one(int mode, int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped, bool whole) {
   ProductPlan p{};
   p.splits = 1;
   if (I == 0 || J == 0) return p;   // nothing to launch
@@ -1142,7 +1145,7 @@ ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t grou
   for (int kind = TILE_256; kind <= TILE_128; kind++) {
     const int64_t ti = ceil_div(I, kShape[kind].rows()), tj = ceil_div(J, kShape[kind].cols());
     const int64_t tiles = (ti + (cut ? groups / 2 : 0)) * tj * outer;
-    const Parts parts = best_parts(kind, tiles, K, steps, I * J, grouped || kind == TILE_256);
+    const Parts parts = best_parts(kind, tiles, K, steps, I * J, whole || grouped || kind == TILE_256);
     if (best == 0.0 || parts.us < best) {
       best = parts.us;
       p.kind = kind;
@@ -1155,15 +1158,20 @@ ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t grou
   return p;
 }
 
-// Both gradients in one launch, for x [M, K] and dp [M, N] without groups: when all tiles of both run at once and
-// that is estimated to take less than one product after the other.  The tiles' kind, or -1.  Measured for [M, N, K], in
-// a graph, one after the other / together: [256, 512, 512] 12.1 / 6.7 us, [1000, 1000, 1000] 21.2 / 11.7, [1024, 2048,
-// 2048] 30.4 / 26.8, [1021, 2000, 2056] 38.5 / 31.3, [3000, 1000, 1000] 31.6 / 27.1; of 17 such shapes none was
-// slower together where the rule said so.
+// Both gradients in one launch, for x [M, K] and dp [M, N] without groups, every sum in one piece: when all tiles of
+// both run at once and that is estimated to take less than one product after the other.  The parts of a sum must not
+// depend on whether the other gradient is formed (they show in the last bits), so a gradient formed alone is not cut
+// either where this is taken, and what the two gain together has to be more than what they lose alone.  The
+// tiles' kind, or -1.  Measured for [M, N, K], in a graph, one after the other / together: [256, 512, 512] 12.1 / 6.7
+// us, [1000, 1000, 1000] 21.2 / 11.7, [1024, 2048, 2048] 30.4 / 26.8, [1021, 2000, 2056] 38.5 / 31.3; where one alone would
+// be cut, and it alone cut / whole: [3000, 1000, 1000] 33.3 / 26.2, dW 20.5 / 25.2; [2000, 512, 512] 20.7 / 18.0, dW 13.4 /
+// 17.5 (the rule takes the gain for 5.9); not taken [512, 2048, 512], 19.9 / 16.1, dx 12.4 / 17.
 constexpr double kLaunchUs = 3.5;   // a launch and the gap before it
 int plan_gradients(int64_t M, int64_t N, int64_t K) {
   if (M == 0 || N == 0 || K == 0) return -1;
-  double best = plan_product(DGRAD, M, K, N, 1, false).us + plan_product(WGRAD, N, K, M, 1, false).us + kLaunchUs;
+  const double apart = plan_one(DGRAD, M, K, N, 1, false, false).us + plan_one(WGRAD, N, K, M, 1, false, false).us;
+  const double uncut = plan_one(DGRAD, M, K, N, 1, false, true).us + plan_one(WGRAD, N, K, M, 1, false, true).us;
+  double best = apart + kLaunchUs - (uncut - apart);
   int kind = -1;
   for (int k = TILE_256_128; k <= TILE_128; k++) {
     const int64_t rows = kShape[k].rows(), j = ceil_div(K, kShape[k].cols());
@@ -1176,6 +1184,13 @@ int plan_gradients(int64_t M, int64_t N, int64_t K) {
     }
   }
   return kind;
+}
+
+ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped) {
+  const ProductPlan p = plan_one(mode, I, J, K, groups, grouped, false);
+  if (p.splits == 1 || (mode != DGRAD && mode != WGRAD)) return p;
+  const int joint = mode == DGRAD ? plan_gradients(I, K, J) : plan_gradients(K, I, J);
+  return joint < 0 ? p : plan_one(mode, I, J, K, groups, grouped, true);
 }
 
 hipError_t launch_gradients(int kind, const ProductArgs& d, const ProductArgs& w, hipStream_t s) {
