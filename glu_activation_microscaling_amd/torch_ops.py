@@ -34,8 +34,8 @@ that torch.compile keeps whole; these ops do the same for the MI355X kernels:
   torch.ops.glu_mx.glu_ckpt(gate, up, act, layout)                     -> (h, q, s)
   torch.ops.glu_mx.glu_ckpt_backward(q, s, dh, act, layout, need_h)    -> (d, h)
   torch.ops.glu_mx.feed_forward(x, w13, w2, b13, b2, offsets, act, w_layout, save) -> (y, pre, extra)
-  torch.ops.glu_mx.feed_forward_backward(dy, x, w13, w2, pre, extra, offsets, act, w_layout, bias13, bias2)
-                                                                       -> (dx, dw13, dw2, db13, db2)
+  torch.ops.glu_mx.feed_forward_backward(dy, x, w13, w2, pre, extra, offsets, act, w_layout, bias13, bias2,
+                                         need_dx, need_dw13, need_dw2) -> (dx, dw13, dw2, db13, db2)
   torch.ops.glu_mx.quant_fp8(x, rowwise, colwise)                      -> (q_row, q_col, s_row, s_col)
   torch.ops.glu_mx.glu_fp8(gate, up, act, layout, rowwise, colwise)    -> the same of act(gate) * up
   torch.ops.glu_mx.quant_fp8_weight(w, transpose)                      -> (q, s, qt, st)
@@ -612,25 +612,34 @@ def _(x, w13, w2, b13=None, b2=None, offsets=None, act="swiglu", w_layout="split
 
 @torch.library.custom_op(f"{_LIB}::feed_forward_backward", mutates_args=())
 def feed_forward_backward(dy: Tensor, x: Tensor, w13: Tensor, w2: Tensor, pre: Tensor, extra: Tensor,
-                          offsets: Optional[Tensor], act: str, w_layout: str, bias13: bool,
-                          bias2: bool) -> Tuple[Tensor, Tensor, Tensor, Tensor, Tensor]:
-    # the first call reads no h: its gradient needs dy and w2 alone
-    dh = _linear_bwd(dy, x.new_empty((x.shape[0], w2.shape[-1])), w2, offsets=offsets, need_dw=False)[0]
-    dx, dw13, db13, h = _gated_bwd(dh, x, w13, pre, extra, act=act, w_layout=w_layout, offsets=offsets, bias=bias13,
-                                   need_h=True)
-    _, dw2, db2 = _linear_bwd(dy, h, w2, offsets=offsets, bias=bias2, need_dx=False)
+                          offsets: Optional[Tensor], act: str, w_layout: str, bias13: bool, bias2: bool,
+                          need_dx: bool = True, need_dw13: bool = True,
+                          need_dw2: bool = True) -> Tuple[Tensor, Tensor, Tensor, Tensor, Tensor]:
+    dx, dw13, dw2, db13, db2 = (x.new_empty((0,)) for _ in range(5))
+    first = need_dx or need_dw13 or bias13   # gradients of the projections
+    M, N = x.shape[0], w2.shape[-1]
+    # the calls for dh and db2 read no h
+    dh = h = x.new_empty((M, N))
+    if first:
+        dh = _linear_bwd(dy, h, w2, offsets=offsets, need_dw=False)[0]
+    if first or need_dw2:
+        dx, dw13, db13, h = _gated_bwd(dh, x, w13, pre, extra, act=act, w_layout=w_layout, offsets=offsets, bias=bias13,
+                                       need_dx=need_dx, need_dw=need_dw13, need_h=need_dw2)
+    if need_dw2 or bias2:
+        _, dw2, db2 = _linear_bwd(dy, h if need_dw2 else dh, w2, offsets=offsets, bias=bias2, need_dx=False, need_dw=need_dw2)
     return dx, dw13, dw2, db13, db2
 
 
 @feed_forward_backward.register_fake
-def _(dy, x, w13, w2, pre, extra, offsets, act, w_layout, bias13, bias2):
-    return (x.new_empty(x.shape), w13.new_empty(w13.shape), w2.new_empty(w2.shape),
-            w13.new_empty(w13.shape[:-1] if bias13 else (0,)), w2.new_empty(w2.shape[:-1] if bias2 else (0,)))
+def _(dy, x, w13, w2, pre, extra, offsets, act, w_layout, bias13, bias2, need_dx=True, need_dw13=True, need_dw2=True):
+    def of(t, wanted, shape):
+        return t.new_empty(shape if wanted else (0,))
+    return (of(x, need_dx, x.shape), of(w13, need_dw13, w13.shape), of(w2, need_dw2, w2.shape),
+            of(w13, bias13, w13.shape[:-1]), of(w2, bias2, w2.shape[:-1]))
 
 
 def _ffn_setup(ctx, inputs, output):
-    x, w13, w2, b13, b2, offsets, ctx.act, ctx.w_layout, ctx.save = inputs
-    ctx.has_bias = b13 is not None, b2 is not None
+    x, w13, w2, _, _, offsets, ctx.act, ctx.w_layout, ctx.save = inputs
     ctx.save_for_backward(x, w13, w2, offsets, output[1], output[2])
     ctx.mark_non_differentiable(output[1], output[2])
 
@@ -638,9 +647,10 @@ def _ffn_setup(ctx, inputs, output):
 def _ffn_grad(ctx, dy, *_):
     _no_save(ctx.save)
     x, w13, w2, offsets, pre, extra = ctx.saved_tensors
+    need = (tuple(ctx.needs_input_grad) + (False,) * 5)[:5]
     dx, dw13, dw2, db13, db2 = feed_forward_backward(_incoming(dy), x, w13, w2, pre, extra, offsets, ctx.act, ctx.w_layout,
-                                                     *ctx.has_bias)
-    return (dx, dw13, dw2, db13 if ctx.has_bias[0] else None, db2 if ctx.has_bias[1] else None, None, None, None, None)
+                                                     need[3], need[4], need[0], need[1], need[2])
+    return (*(g if n else None for g, n in zip((dx, dw13, dw2, db13, db2), need)), None, None, None, None)
 
 
 feed_forward.register_autograd(_ffn_grad, setup_context=_ffn_setup)
