@@ -299,8 +299,8 @@ def glu_linear(x, w, bias=None, residual=None, *, act="none", offsets=None, save
     pre = x.new_empty((M, N), dtype=torch.float16) if save_pre else None
     nbytes = _size("glu_linear_work_bytes", M, N, K, groups, int(offsets is not None))
     work = x.new_empty((nbytes,), dtype=torch.uint8) if nbytes > 0 else None
-    _call("glu_linear", LINEAR_ACT[act], M, N, K, groups, _ptr(offsets), _ptr(x), ld_x, _ptr(w), _ptr(bias),
-          _ptr(residual), ld_res, _ptr(y), ld_y, _ptr(pre), _ptr(work), nbytes, _stream(x))
+    _launch(x, "glu_linear", LINEAR_ACT[act], M, N, K, groups, _ptr(offsets), _ptr(x), ld_x, _ptr(w), _ptr(bias),
+            _ptr(residual), ld_res, _ptr(y), ld_y, _ptr(pre), _ptr(work), nbytes)
     return (y, pre) if save_pre else y
 
 
@@ -321,8 +321,8 @@ def glu_linear_bwd(dy, x, w, *, pre=None, act="none", offsets=None, bias=False, 
     db = x.new_empty(w.shape[:-1] if bias else (0,))
     nbytes = _size("glu_linear_bwd_work_bytes", a, M, N, K, groups, int(offsets is not None), int(bias))
     work = x.new_empty((nbytes,), dtype=torch.uint8) if nbytes > 0 else None
-    _call("glu_linear_bwd", a, M, N, K, groups, _ptr(offsets), _ptr(dy), ld_dy, _ptr(x), ld_x, _ptr(w), _ptr(pre),
-          _ptr(dx), K, _ptr(dw), _ptr(db), _ptr(work), nbytes, _stream(x))
+    _launch(x, "glu_linear_bwd", a, M, N, K, groups, _ptr(offsets), _ptr(dy), ld_dy, _ptr(x), ld_x, _ptr(w), _ptr(pre),
+            _ptr(dx), K, _ptr(dw), _ptr(db), _ptr(work), nbytes)
     return dx, dw, db
 
 
