@@ -67,8 +67,11 @@ def _launch(t, name, *args):
         return _call(name, *args, _stream(t))
 
 
-# Makes a tensor on the current GPU; what compiled graphs make theirs with (0.8 us where new_empty takes 1.4).
-_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+_GPU = torch.device("cuda")   # the current one
+
+
+def _strided(shape, stride, dtype):
+    return torch.empty_strided(shape, stride, dtype=dtype, device=_GPU)   # 1.3 us where new_empty takes 1.5
 
 
 def _contiguous(shape, dtype):
