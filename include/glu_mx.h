@@ -529,7 +529,9 @@ glu_status glu_quant_fp8_weight(int64_t groups, int64_t N, int64_t K, const uint
                                 float* st, void* stream);
 
 /* y = x W^T + bias + residual of such operands, [M, N] BF16: products of codes summed over each block
- * of 128 on the matrix cores, the blocks' sums scaled and added in FP32, rounded once.
+ * of 128 on the matrix cores, the blocks' sums scaled and added in FP32, rounded once.  Two scales may be
+ * of any size, also where their product passes FP32's range and the scaled sum does not; a product below
+ * 2^-126 is rounded to FP32's subnormal numbers.
  * xq [M, K], xs [K/128, M]; wq [groups, N, K]; ws [groups, N/128, K/128] (GLU_FP8_W_BLOCK) or [groups,
  * K/128, N] (GLU_FP8_W_ROW: W was quantized along the sum); bias [groups, N] or NULL, residual [M, N] or
  * NULL, BF16; offsets and groups as for glu_linear.  K, the length of a code row, is a multiple of 16 up
