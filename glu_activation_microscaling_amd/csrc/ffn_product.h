@@ -949,19 +949,6 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_product(typename ArgsOf<MODE =
   product_tile<MODE, ACT, WI, WJ, TI, TJ, NS>(a, tiles_i, tiles_j, splits, blockIdx.x, gridDim.x, smem);
 }
 
-// Both gradients of a product without groups, each whole in its own workgroups: dx = dp W in the first ones, filled
-// up to a multiple of 8 so that the rest, dW = dp^T x, start on the first XCD too.
-template <int WI, int WJ, int TI, int TJ, int NS>
-__global__ __launch_bounds__(64 * WI * WJ) void k_gradients(ProductArgs d, uint32_t d_i, uint32_t d_j, ProductArgs w,
-                                                            uint32_t w_i, uint32_t w_j) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kProductLds<16 * WI * TI, 16 * WJ * TJ, NS>];
-  const uint32_t nd = d_i * d_j, first = (nd + 7u) / 8u * 8u;
-  if (blockIdx.x >= first)
-    product_tile<WGRAD, LIN_NONE, WI, WJ, TI, TJ, NS>(w, w_i, w_j, 1, blockIdx.x - first, w_i * w_j, smem);
-  else if (blockIdx.x < nd)
-    product_tile<DGRAD, LIN_NONE, WI, WJ, TI, TJ, NS>(d, d_i, d_j, 1, blockIdx.x, nd, smem);
-}
-
 // Joins the parts of split sums and finishes them: eight columns a thread, the parts in order.
 // Bound by memory (the parts are in the caches): [968, 2048] in four parts 7.3 us.
 template <int MODE, int ACT>
@@ -1193,16 +1180,6 @@ ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t grou
   return joint < 0 ? p : plan_one(mode, I, J, K, groups, grouped, true);
 }
 
-hipError_t launch_gradients(int kind, const ProductArgs& d, const ProductArgs& w, hipStream_t s) {
-  auto go = [&](auto KIND) {
-    constexpr TileShape t = kShape[decltype(KIND)::value];
-    const int64_t j = ceil_div(d.J, t.cols()), di = ceil_div(d.I, t.rows()), wi = ceil_div(w.I, t.rows());
-    return launch_kernel(k_gradients<t.wi, t.wj, t.ti, t.tj, t.stages>, dim3((unsigned)((di * j + 7) / 8 * 8 + wi * j)),
-                         dim3(64 * t.wi * t.wj), s, d, (uint32_t)di, (uint32_t)j, w, (uint32_t)wi, (uint32_t)j);
-  };
-  return kind == TILE_128 ? go(std::integral_constant<int, TILE_128>{}) : go(std::integral_constant<int, TILE_256_128>{});
-}
-
 int64_t product_work_bytes(int mode, int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped) {
   const ProductPlan p = plan_product(mode, I, J, K, groups, grouped);
   return p.splits > 1 ? 4 * p.splits * (mode == WGRAD ? groups : 1) * I * J : 0;
@@ -1237,36 +1214,6 @@ hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
   return launch_kernel(k_product_join<MODE, ACT>, dim3(grid_for(ceil_div(octets, 256), 4096)), dim3(256), s, a,
                        (uint32_t)p.splits);
 }
-
-// ---- column sums in parts --------------------------------------------------------------------
-
-// 64 columns a workgroup, every fourth part a wave.
-__global__ __launch_bounds__(256) void k_linear_join(const float* sums, int64_t parts, int64_t n, uint16_t* out) {
-  __shared__ float part[4][64];
-  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-  const int64_t i = 64 * (int64_t)blockIdx.x + lane;
-  float s = 0.0f;
-  if (i < n) {
-#pragma unroll 4
-    for (int64_t p = wave; p < parts; p += 4) s += sums[p * n + i];
-  }
-  part[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && i < n)
-    out[i] = (uint16_t)pack_bf16((part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]), 0.0f);
-}
-
-// Parts each group's rows are cut into for the column sums: enough workgroups to fill the chip,
-// with 64 rows or more of an average group each.
-int64_t grad_parts(int64_t M, int64_t N, int64_t groups) {
-  if (N == 0) return 1;
-  const int64_t tiles = (N + 255) / 256 * groups, want = (1024 + tiles - 1) / tiles;
-  const int64_t most = (M / groups + 63) / 64;
-  const int64_t p = want < most ? want : most;
-  return p < 1 ? 1 : p;
-}
-
-int64_t round16(int64_t b) { return (b + 15) / 16 * 16; }
 
 }  // namespace
 }  // namespace glu

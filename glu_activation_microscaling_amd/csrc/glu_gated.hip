@@ -10,6 +10,7 @@
 // gradient it is kept as BF16, the type the GLU takes its operands in, with four more bits of each
 // value beside it, or as MXFP8 codes of BF16 values; the gradient is that of the GLU at the values
 // kept.  dp is rounded to BF16 for the matrix cores; dbias sums it unrounded.
+#include "ffn_column_sums.h"
 #include "ffn_product.h"
 #include "gated_launch.h"
 

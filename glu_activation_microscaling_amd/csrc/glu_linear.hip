@@ -11,6 +11,7 @@
 // constant beyond it to more digits than BF16 has, and FP16's 11 bits keep act' eight times
 // nearer than BF16's 8 would.  dp is rounded to BF16, the type the matrix cores multiply;
 // db sums it unrounded.
+#include "ffn_column_sums.h"
 #include "ffn_product.h"
 
 namespace glu {
@@ -79,6 +80,41 @@ __global__ __launch_bounds__(256) void k_linear_grad(GradArgs a) {
     for (int w = 0; w < 8; w++) t += part[w][threadIdx.x / 8][threadIdx.x % 8];
     a.sums[((int64_t)blockIdx.z * a.groups + e) * a.N + c] = t;
   }
+}
+
+// Parts each group's rows are cut into for the column sums: enough workgroups to fill the chip,
+// with 64 rows or more of an average group each.
+int64_t grad_parts(int64_t M, int64_t N, int64_t groups) {
+  if (N == 0) return 1;
+  const int64_t tiles = (N + 255) / 256 * groups, want = (1024 + tiles - 1) / tiles;
+  const int64_t most = (M / groups + 63) / 64;
+  const int64_t p = want < most ? want : most;
+  return p < 1 ? 1 : p;
+}
+
+// ---- both gradients in one launch ----------------------------------------------------------
+
+// Both gradients of a product without groups, each whole in its own workgroups: dx = dp W in the first ones, filled
+// up to a multiple of 8 so that the rest, dW = dp^T x, start on the first XCD too.
+template <int WI, int WJ, int TI, int TJ, int NS>
+__global__ __launch_bounds__(64 * WI * WJ) void k_gradients(ProductArgs d, uint32_t d_i, uint32_t d_j, ProductArgs w,
+                                                            uint32_t w_i, uint32_t w_j) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kProductLds<16 * WI * TI, 16 * WJ * TJ, NS>];
+  const uint32_t nd = d_i * d_j, first = (nd + 7u) / 8u * 8u;
+  if (blockIdx.x >= first)
+    product_tile<WGRAD, LIN_NONE, WI, WJ, TI, TJ, NS>(w, w_i, w_j, 1, blockIdx.x - first, w_i * w_j, smem);
+  else if (blockIdx.x < nd)
+    product_tile<DGRAD, LIN_NONE, WI, WJ, TI, TJ, NS>(d, d_i, d_j, 1, blockIdx.x, nd, smem);
+}
+
+hipError_t launch_gradients(int kind, const ProductArgs& d, const ProductArgs& w, hipStream_t s) {
+  auto go = [&](auto KIND) {
+    constexpr TileShape t = kShape[decltype(KIND)::value];
+    const int64_t j = ceil_div(d.J, t.cols()), di = ceil_div(d.I, t.rows()), wi = ceil_div(w.I, t.rows());
+    return launch_kernel(k_gradients<t.wi, t.wj, t.ti, t.tj, t.stages>, dim3((unsigned)((di * j + 7) / 8 * 8 + wi * j)),
+                         dim3(64 * t.wi * t.wj), s, d, (uint32_t)di, (uint32_t)j, w, (uint32_t)wi, (uint32_t)j);
+  };
+  return kind == TILE_128 ? go(std::integral_constant<int, TILE_128>{}) : go(std::integral_constant<int, TILE_256_128>{});
 }
 
 }  // namespace
