@@ -6,6 +6,7 @@
 
 #include "ffn_device.h"
 #include "ffn_launch.h"
+#include "ffn_plan.h"
 #include "ffn_split.h"
 #include "mx_block.h"
 
@@ -57,8 +58,6 @@ hipError_t with_linear_act(int act, F&& f) {
 // C[i, j] = sum_k A(i, k) B(j, k).  An operand is stored with k along its rows (element (i, k)
 // at i ld + k) or transposed (at k ld + i).
 // GATED: C[i, n] = act(gate) * up of two such sums, B's rows in pairs (see GatedOperand).
-enum { FWD, DGRAD, WGRAD, GATED };
-
 struct ProductArgs {
   int64_t I, J, K;           // rows of C, columns of C, length of the sum
   int64_t groups;
@@ -92,9 +91,6 @@ template <>
 struct ArgsOf<true> {
   using type = GatedArgs;
 };
-// Columns of a gated product's sums: 16 gate and 16 up for each 16 outputs.
-__host__ __device__ constexpr int64_t gated_columns(int64_t J) { return (J + 15) / 16 * 32; }
-
 // Row segments of grouped products: 0 holds the rows before the first group, e + 1 those of group e,
 // groups + 1 those after the last group.  The first and the last are of no group and count as group
 // number `groups`.
@@ -173,8 +169,6 @@ __device__ __forceinline__ const uint16_t* uniform(const uint16_t* p) {
 typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
-
-constexpr uint32_t BK = 64;   // elements of the sum per step: one 128-byte line of a row
 
 // One operand of a tile: B_ rows of the operand by BK elements of the sum per step, copied
 // straight into LDS in blocks of 1 KiB (16 bytes a lane) and read back as 16 x 32 fragments
@@ -976,8 +970,6 @@ __global__ __launch_bounds__(256) void k_product_join(ProductArgs a, uint32_t sp
 // load takes 128 bytes of a row.  KW waves share the sum, taking chunks of 128 elements in turn, and
 // join through LDS, so a call is one launch whatever its extents.  The next chunks of W are in
 // flight while the present ones are multiplied.  [1, 2048, 16384]: 13.2 to 14.9 us (4.5 to 5.1 TB/s).
-constexpr int FEW_WAVES = 8, FEW_ROWS = 8, FEW_COLS = 8, FEW_CHUNK = 128;
-
 // grid: column tiles of FEW_COLS FEW_WAVES / KW
 template <int ACT, int KW>
 __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_few_rows(ProductArgs a) {
@@ -1042,143 +1034,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_few_rows(ProductArgs a) {
   finish<FWD, ACT, 4>(a, 0, row, col, v);
 }
 
-// ---- which kernel ----------------------------------------------------------------------------
-
-// The tiled kernel's sizes: waves and 16 x 16 tiles a wave along the rows and the columns, LDS
-// stages.  The larger the tile, the fewer bytes go into LDS for a product (L1 delivers 64 bytes a
-// cycle: half the products' time at 256 x 256) and the more of the chip idles at the end.
-//   32 x 128, two workgroups a compute unit: a few rows of each of many groups, a pass over W.
-struct TileShape {
-  int wi, wj, ti, tj, stages;
-  constexpr int rows() const { return 16 * wi * ti; }
-  constexpr int cols() const { return 16 * wj * tj; }
-};
-enum { TILE_256, TILE_256_128, TILE_128, TILE_32, FEW };
-constexpr TileShape kShape[4] = {{2, 4, 8, 4, 2}, {4, 2, 4, 4, 3}, {2, 4, 4, 2, 3}, {1, 4, 2, 2, 4}};
-struct ProductPlan {
-  int kind;
-  int64_t share;             // FEW: waves sharing a sum
-  int64_t tiles_i, tiles_j, splits;
-  double us;                 // the rule's estimate, of the tiled ones
-};
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// What a tile takes, in microseconds a step of BK elements and for its start and end, from calls of
-// one round of workgroups (2048 to 8192 rows, sums of 1024 to 8192 elements), and what joining the
-// parts of a split sum takes.  The least total over the first three sizes decides.  Measured for
-// [I, J, K], 256x256 / 256x128 / 128x128:
-//   [ 1000, 1000, 1000]  22.5 / 15.8 / 11.2      [ 4096, 4096, 1024]  31.5 /  41.6 /  45.7
-//   [  968, 2048,16384]   237 / 65.8 / 72.0      [ 4096, 4096, 4096]  95.7 / 113.7 / 136.3
-//   [ 2048, 4096, 4096]  72.9 / 58.2 / 69.1      [16384, 2048, 2048]   102 /   126 /   151
-// (of 33 such shapes the rule takes the fastest of the three on 31 and is 0.5% and 6% behind on the others).
-constexpr int64_t kUnits = 256;
-constexpr double kStepUs[3] = {1.22, 0.85, 0.5}, kTileUs[3] = {15.0, 5.0, 4.0}, kJoinUs = 2.5, kJoinTBps = 5.0;
-constexpr double kStepFewUs[3] = {1.22, 0.85, 0.41};   // of a step while at most half the chip works
-constexpr int64_t kLeastPart = 512;   // elements of a split sum's part: 256 costs up to 5 us more, and gains 0.5
-
-// The number of parts of a sum that takes the least time by these figures: one, a power of two or the most, at
-// least kLeastPart elements each and one round of workgroups in all.  Measured in a graph, 128 x 128 tiles, the most
-// parts / the rule's: [2048, 1024, 1024] 20.2 (2) / 10.6 us (1), [512, 2048, 2048] 20.4 (4) / 17.7 (2; 16.0 whole),
-// [968, 2048, 2048] 20.3 (2) / 16.8 (1), [1021, 1000, 2056] 20.2 (4) / 18.6 (2; 22.9 whole), [1024, 1024, 4096] 20.0 (4)
-// / the same (26 whole).
-struct Parts {
-  int64_t splits;
-  double us;
-};
-Parts best_parts(int kind, int64_t tiles, int64_t K, int64_t steps, int64_t outputs, bool whole) {
-  const int64_t fit = whole ? 1 : K / kLeastPart < kUnits / tiles ? K / kLeastPart : kUnits / tiles, most = fit < 1 ? 1 : fit;
-  Parts best{0, 0.0};
-  for (int64_t splits = 1;;) {
-    const double step = tiles * splits <= kUnits / 2 ? kStepFewUs[kind] : kStepUs[kind];
-    double us = (kTileUs[kind] + step * ceil_div(steps, splits)) * ceil_div(tiles * splits, kUnits);
-    if (splits > 1) us += kJoinUs + 8e-6 / kJoinTBps * splits * outputs;
-    if (best.splits == 0 || us < best.us) best = {splits, us};
-    if (splits == most) return best;
-    splits = 2 * splits < most ? 2 * splits : most;
-  }
-}
-
-// A rule on extents alone, so that the scratch memory of split sums can be sized before the
-// launch.  whole: sums are not cut.
-ProductPlan plan_one(int mode, int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped, bool whole) {
-  ProductPlan p{};
-  p.splits = 1;
-  if (I == 0 || J == 0) return p;   // nothing to launch
-  if (mode == FWD && !grouped && I <= FEW_ROWS) {
-    // [I, 2048, 16384], few rows against 128x128 tiles: 14.7 / 20.7 us for one row, 18.4 / 21.3 for 8
-    p.kind = FEW;
-    // waves sharing a sum: as few as give 16 waves a compute unit, with four chunks or more each
-    const int64_t cols = ceil_div(J, FEW_COLS);
-    p.share = 1;
-    while (p.share < FEW_WAVES && cols * p.share < 16 * kUnits && K >= 8 * p.share * FEW_CHUNK) p.share *= 2;
-    p.tiles_j = ceil_div(cols * p.share, FEW_WAVES);
-    return p;
-  }
-  if (mode == FWD && grouped && I <= kShape[TILE_32].rows() / 2 * groups) {
-    // 32 groups of W [2048, 2048], 32x128 against 128x128 tiles: 48.7 / 54 us for 8 rows a group on
-    // average, 49.5 / 54 for 16, 58 / 54 for 32 (groups of more than 32 rows read W twice)
-    p.kind = TILE_32;
-    p.tiles_i = ceil_div(I, kShape[TILE_32].rows()) + groups + 1;
-    p.tiles_j = ceil_div(J, kShape[TILE_32].cols());
-    return p;
-  }
-  // groups: each ends inside a tile, half a tile more on average; at most one tile more for each of
-  // the groups + 2 segments but one
-  const bool cut = grouped && mode != WGRAD;
-  const int64_t extra = cut ? groups + 1 : 0, outer = mode == WGRAD ? groups : 1;
-  const int64_t steps = ceil_div(mode == WGRAD && grouped ? ceil_div(K, groups) : K, BK);
-  double best = 0.0;
-  for (int kind = TILE_256; kind <= TILE_128; kind++) {
-    const int64_t ti = ceil_div(I, kShape[kind].rows()), tj = ceil_div(J, kShape[kind].cols());
-    const int64_t tiles = (ti + (cut ? groups / 2 : 0)) * tj * outer;
-    const Parts parts = best_parts(kind, tiles, K, steps, I * J, whole || grouped || kind == TILE_256);
-    if (best == 0.0 || parts.us < best) {
-      best = parts.us;
-      p.kind = kind;
-      p.tiles_i = ti + extra;
-      p.tiles_j = tj;
-      p.splits = parts.splits;
-    }
-  }
-  p.us = best;
-  return p;
-}
-
-// Both gradients in one launch, for x [M, K] and dp [M, N] without groups, every sum in one piece: when all tiles of
-// both run at once and that is estimated to take less than one product after the other.  The parts of a sum must not
-// depend on whether the other gradient is formed (they show in the last bits), so a gradient formed alone is not cut
-// either where this is taken, and what the two gain together has to be more than what they lose alone.  The
-// tiles' kind, or -1.  Measured for [M, N, K], in a graph, one after the other / together: [256, 512, 512] 12.1 / 6.7
-// us, [1000, 1000, 1000] 21.2 / 11.7, [1024, 2048, 2048] 30.4 / 26.8, [1021, 2000, 2056] 38.5 / 31.3; where one alone would
-// be cut, and it alone cut / whole: [3000, 1000, 1000] 33.3 / 26.2, dW 20.5 / 25.2; [2000, 512, 512] 20.7 / 18.0, dW 13.4 /
-// 17.5 (the rule takes the gain for 5.9); not taken [512, 2048, 512], 19.9 / 16.1, dx 12.4 / 17.
-constexpr double kLaunchUs = 3.5;   // a launch and the gap before it
-int plan_gradients(int64_t M, int64_t N, int64_t K) {
-  if (M == 0 || N == 0 || K == 0) return -1;
-  const double apart = plan_one(DGRAD, M, K, N, 1, false, false).us + plan_one(WGRAD, N, K, M, 1, false, false).us;
-  const double uncut = plan_one(DGRAD, M, K, N, 1, false, true).us + plan_one(WGRAD, N, K, M, 1, false, true).us;
-  double best = apart + kLaunchUs - (uncut - apart);
-  int kind = -1;
-  for (int k = TILE_256_128; k <= TILE_128; k++) {
-    const int64_t rows = kShape[k].rows(), j = ceil_div(K, kShape[k].cols());
-    const int64_t tiles = ceil_div(M, rows) * j + ceil_div(N, rows) * j;
-    if (tiles > kUnits) continue;
-    const double us = kTileUs[k] + (tiles <= kUnits / 2 ? kStepFewUs[k] : kStepUs[k]) * ceil_div(M > N ? M : N, BK);
-    if (us < best) {
-      best = us;
-      kind = k;
-    }
-  }
-  return kind;
-}
-
-ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped) {
-  const ProductPlan p = plan_one(mode, I, J, K, groups, grouped, false);
-  if (p.splits == 1 || (mode != DGRAD && mode != WGRAD)) return p;
-  const int joint = mode == DGRAD ? plan_gradients(I, K, J) : plan_gradients(K, I, J);
-  return joint < 0 ? p : plan_one(mode, I, J, K, groups, grouped, true);
-}
+// ---- launches ----------------------------------------------------------------------------
 
 int64_t product_work_bytes(int mode, int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped) {
   const ProductPlan p = plan_product(mode, I, J, K, groups, grouped);

@@ -3,13 +3,12 @@
 #pragma once
 
 #include "ffn_launch.h"
+#include "ffn_plan.h"
 
 namespace glu {
 
-constexpr int64_t kFp8Block = 128;
 enum { FP8_W_BLOCK = 0, FP8_W_ROW = 1 };
 
-inline int64_t fp8_blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
 inline int64_t fp8_padded(int64_t n) { return (n + 15) / 16 * 16; }
 
 struct Fp8QuantArgs {

@@ -616,60 +616,7 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_fp8_few(Fp8Args a) {
   finish<FWD, LIN_NONE, 4>(a, 0, row, col, v);
 }
 
-// ---- which kernel ----------------------------------------------------------------------------
-
-// What a tile takes, in microseconds a block of the sum and for its start and end, from calls of one to eight
-// rounds of workgroups, and what joining the parts of a split sum takes; the least total over the first
-// three sizes decides.  Measured for [I, J, K], 256x256 / 256x128 / 128x128 (parts of the sum):
-//   [ 1021, 1000, 2048]  30 / 20.7 / 15.0             [ 4096, 4096, 4096]  61.6 / 76.3 / 95.8
-//   [  968, 2048,16384]  50.5 (8) / 49.8 (4) / 54.4 (2)   [16384, 2048, 2048]  69.6 / 88.4 / 110
-//   [ 2048, 4096, 4096]  49.0 / 41.4 / 49.3           16 groups [8192, 4096, 2048]  102 / 122 / 139
-constexpr TileShape kFp8Shape[4] = {{2, 4, 8, 4, 2}, {4, 2, 4, 4, 3}, {2, 4, 4, 2, 3}, {1, 4, 2, 2, 4}};
-constexpr double kFp8StepUs[3] = {1.55, 1.05, 0.70}, kFp8TileUs[3] = {10.0, 6.0, 3.5}, kFp8JoinUs = 5.0,
-                 kFp8JoinTBps = 8.0;
-constexpr int64_t kFp8LeastPart = 8;   // blocks of a split sum's part
-
-int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
-
-ProductPlan plan_fp8(int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped) {
-  ProductPlan p{};
-  p.splits = 1;
-  if (I == 0 || J == 0) return p;
-  const int64_t blocks = fp8_blocks(K);
-  if (!grouped && I <= FEW_ROWS) {
-    p.kind = FEW;
-    const int64_t cols = ceil_div(J, FEW_COLS);
-    p.share = 1;
-    while (p.share < FEW_WAVES && cols * p.share < 16 * kUnits && blocks >= 4 * p.share) p.share *= 2;
-    p.tiles_j = ceil_div(cols * p.share, FEW_WAVES);
-    return p;
-  }
-  if (grouped && I <= kFp8Shape[TILE_32].rows() / 2 * groups) {
-    p.kind = TILE_32;
-    p.tiles_i = ceil_div(I, kFp8Shape[TILE_32].rows()) + groups + 1;
-    p.tiles_j = ceil_div(J, kFp8Shape[TILE_32].cols());
-    return p;
-  }
-  double best = 0.0;
-  for (int kind = TILE_256; kind <= TILE_128; kind++) {
-    const int64_t ti = ceil_div(I, kFp8Shape[kind].rows()), tj = ceil_div(J, kFp8Shape[kind].cols());
-    const int64_t tiles = (ti + (grouped ? groups / 2 : 0)) * tj;
-    const int64_t most = grouped ? 1 : min64(kUnits / tiles, blocks / kFp8LeastPart);
-    for (int q = 0; q < (most > 1 ? 2 : 1); q++) {   // one part, or the most
-      const int64_t splits = q == 0 ? 1 : most;
-      double us = (kFp8TileUs[kind] + kFp8StepUs[kind] * ceil_div(blocks, splits)) * ceil_div(tiles * splits, kUnits);
-      if (splits > 1) us += kFp8JoinUs + 8e-6 / kFp8JoinTBps * splits * I * J;
-      if (best == 0.0 || us < best) {
-        best = us;
-        p.kind = kind;
-        p.tiles_i = ti + (grouped ? groups + 1 : 0);
-        p.tiles_j = tj;
-        p.splits = splits;
-      }
-    }
-  }
-  return p;
-}
+// ---- launches ----------------------------------------------------------------------------
 
 template <int W_SCALES>
 hipError_t launch_fp8_product(const Fp8Args& a, int64_t codes, hipStream_t s) {

@@ -175,53 +175,11 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_gated_few(GatedArgs a) {
   finish_gated<ACT, 4>(a, 0, row, n, g, u, G, V);
 }
 
-// ---- which kernel ----------------------------------------------------------------------------
-
-// The tile sizes of the linear products, each with waves of 64 columns of the sums (32 outputs).  The rule
-// counts the time of the products' loops, the same here ([1021, 2 x 1000, 2056] 128 x 128 in one piece 26 us, in two
-// parts 18 and 6 to join them); the epilogue adds up to 5 us a 256 x 256 tile where gate and up are kept.
-constexpr TileShape kGatedShape[4] = {{2, 4, 8, 4, 2}, {4, 2, 4, 4, 3}, {4, 2, 2, 4, 3}, {2, 2, 1, 4, 4}};
-
-// Codes need whole blocks of 32 outputs, which the few rows' kernel does not have.
-ProductPlan plan_gated(int save, int64_t I, int64_t N, int64_t K, int64_t groups, bool grouped) {
-  const int64_t J = gated_columns(N);
-  ProductPlan p{};
-  p.splits = 1;
-  if (I == 0 || N == 0) return p;
-  if (!grouped && I <= FEW_ROWS && save != SAVE_MXFP8) {
-    p.kind = FEW;
-    const int64_t cols = ceil_div(N, FEW_COLS);
-    p.share = 1;
-    while (p.share < FEW_WAVES / 2 && 2 * cols * p.share < 16 * kUnits && K >= 8 * p.share * FEW_CHUNK) p.share *= 2;
-    p.tiles_j = ceil_div(2 * cols * p.share, FEW_WAVES);
-    return p;
-  }
-  if (grouped && I <= kGatedShape[TILE_32].rows() / 2 * groups) {
-    p.kind = TILE_32;
-    p.tiles_i = ceil_div(I, kGatedShape[TILE_32].rows()) + groups + 1;
-    p.tiles_j = ceil_div(J, kGatedShape[TILE_32].cols());
-    return p;
-  }
-  const int64_t extra = grouped ? groups + 1 : 0, steps = ceil_div(K, BK);
-  double best = 0.0;
-  for (int kind = TILE_256; kind <= TILE_128; kind++) {
-    const int64_t ti = ceil_div(I, kGatedShape[kind].rows()), tj = ceil_div(J, kGatedShape[kind].cols());
-    const int64_t tiles = (ti + (grouped ? groups / 2 : 0)) * tj;
-    const Parts parts = best_parts(kind, tiles, K, steps, I * J, grouped || kind == TILE_256);
-    if (best == 0.0 || parts.us < best) {
-      best = parts.us;
-      p.kind = kind;
-      p.tiles_i = ti + extra;
-      p.tiles_j = tj;
-      p.splits = parts.splits;
-    }
-  }
-  return p;
-}
+// ---- launches ----------------------------------------------------------------------------
 
 template <int ACT>
 hipError_t launch_gated(const GatedArgs& a, int save, hipStream_t s) {
-  const ProductPlan p = plan_gated(save, a.I, a.J, a.K, a.groups, a.offsets != nullptr);
+  const ProductPlan p = plan_gated(save == SAVE_MXFP8, a.I, a.J, a.K, a.groups, a.offsets != nullptr);
   if (p.kind == FEW) {
     auto go = [&](auto KW) {
       return launch_kernel(k_gated_few<ACT, decltype(KW)::value>, dim3((unsigned)p.tiles_j), dim3(64 * FEW_WAVES), s, a);
@@ -270,7 +228,7 @@ GatedBwdWork gated_bwd_work(int64_t M, int64_t N, int64_t K, int64_t groups, boo
 }  // namespace
 
 int64_t gated_linear_work_bytes(int save, int64_t M, int64_t N, int64_t K, int64_t groups, bool grouped) {
-  const ProductPlan p = plan_gated(save, M, N, K, groups, grouped);
+  const ProductPlan p = plan_gated(save == SAVE_MXFP8, M, N, K, groups, grouped);
   return p.splits > 1 ? 4 * p.splits * M * gated_columns(N) : 0;
 }
 

@@ -1,0 +1,26 @@
+"""The rules that pick a product's kernel: each kernel is taken somewhere, and the parts of a gradient's sum do not
+depend on the other gradient (no GPU)."""
+import itertools
+
+import pytest
+
+from product_plans import available, plans
+
+pytestmark = pytest.mark.skipif(not available, reason="g++ not available")
+
+
+def test_each_kernel_is_taken_somewhere():
+    sizes = [(M, N, K, 0) for M, N, K in itertools.product((1, 40, 300, 3000, 16384), (136, 1000, 7168), (264, 2048, 16384))]
+    sizes += [(M, N, K, 16) for M, N, K in itertools.product((100, 4000, 16384), (1000, 2048), (264, 2048))]
+    for op in ("linear", "gated", "gated8", "fp8"):
+        taken = {k for k, _ in plans([(op, *s) for s in sizes])}
+        assert taken == {"256x256", "256x128", "128x128", "32x128"} | (set() if op == "gated8" else {"few rows"}), op
+
+
+def test_a_gradients_parts_do_not_depend_on_the_other():
+    extents = (8, 64, 256, 512, 1000, 1024, 2048, 3000, 4096)
+    sizes = [(M, N, K, 0) for M, N, K in itertools.product(extents, repeat=3)]
+    both, dx, dw = (plans([(op, *s) for s in sizes]) for op in ("both", "dx", "dw"))
+    joint = [i for i, (kernel, _) in enumerate(both) if kernel is not None]
+    assert len(joint) > 50 and all(dx[i][1] == 1 and dw[i][1] == 1 for i in joint)
+    assert sum(p > 1 for _, p in dx) > 50
