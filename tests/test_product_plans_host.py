@@ -1,12 +1,26 @@
-"""The rules that pick a product's kernel: each kernel is taken somewhere, and the parts of a gradient's sum do not
-depend on the other gradient (no GPU)."""
+"""The rules that pick a product's kernel: the shapes that tests name a kernel for take it, and the parts of a
+gradient's sum do not depend on the other gradient (no GPU)."""
 import itertools
 
 import pytest
 
+import test_gpu_large_tiles as large
 from product_plans import available, plans
 
 pytestmark = pytest.mark.skipif(not available, reason="g++ not available")
+
+
+def test_large_tiles():
+    queries, want = [], []
+    for ops, cases in ((("gated", "gated8"), large.GATED), (("fp8",), large.FP8)):
+        for (M, N, K, kernel), op in itertools.product(cases, ops):
+            queries.append((op, M, N, K, 0))
+            want.append((kernel, 1))
+    for ops, cases in ((("gated", "gated8"), large.GATED_GROUPS), (("fp8",), large.FP8_GROUPS)):
+        for (counts, before, after, N, K, kernel), op in itertools.product(cases, ops):
+            queries.append((op, before + sum(counts) + after, N, K, len(counts)))
+            want.append((kernel, 1))
+    assert plans(queries) == want
 
 
 def test_each_kernel_is_taken_somewhere():
