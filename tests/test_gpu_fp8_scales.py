@@ -22,7 +22,8 @@ def code(t):
 
 # up to 8 rows; each tile size; a sum in parts
 SHAPES = [(3, 136, 256, None), (8, 24, 4096, None), (40, 136, 256, None), (300, 264, 16384, None), (4000, 2008, 512, None),
-          (2500, 1032, 256, None), (4096, 4104, 256, None), (40, 136, 256, [0, 8, 8, 30, 38]), (700, 264, 256, [5, 300, 690])]
+          (2500, 1032, 256, None), (4096, 4096, 256, None), (4096, 4104, 256, None), (40, 136, 256, [0, 8, 8, 30, 38]),
+          (700, 264, 256, [5, 300, 690])]
 
 
 @pytest.mark.parametrize("M,N,K,offsets", SHAPES)

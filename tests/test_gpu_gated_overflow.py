@@ -15,7 +15,10 @@ def n(*shape, seed=0, scale=1.0):
 
 
 # every kernel of the projections: up to 8 rows, parts that are joined, each tile size
-@pytest.mark.parametrize("M,N,K", [(3, 72, 264), (40, 72, 4104), (300, 72, 264), (3000, 1032, 64), (4096, 2056, 264)])
+SHAPES = [(3, 72, 264), (40, 72, 4104), (300, 72, 264), (3000, 1032, 64), (4096, 2056, 264), (3100, 1288, 776)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 def test_what_is_kept(gpu, M, N, K, sign):
     x, w, row, over = n(M, K), n(2 * N, K, seed=1, scale=K ** -0.5).abs(), M // 2, 40

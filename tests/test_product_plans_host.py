@@ -4,6 +4,8 @@ import itertools
 
 import pytest
 
+import test_gpu_fp8_scales as scales
+import test_gpu_gated_overflow as overflow
 import test_gpu_large_tiles as large
 from product_plans import available, plans
 
@@ -21,6 +23,16 @@ def test_large_tiles():
             queries.append((op, before + sum(counts) + after, N, K, len(counts)))
             want.append((kernel, 1))
     assert plans(queries) == want
+
+
+def test_extremes_reach_every_kernel():
+    tiles = {"256x256", "256x128", "128x128"}
+    taken = plans([("fp8", M, N, K, 0 if off is None else len(off) - 1) for M, N, K, off in scales.SHAPES])
+    assert {k for k, _ in taken} == tiles | {"32x128", "few rows"} and any(p > 1 for _, p in taken)
+    taken = plans([("gated", *s, 0) for s in overflow.SHAPES])
+    assert {k for k, _ in taken} == tiles | {"few rows"} and any(p > 1 for _, p in taken)
+    assert plans([("fp8", M, N, 1 << 22, 0) for M, N in ((1, 16), (20, 136), (300, 264))]) == [("few rows", 1), ("128x128", 128),
+                                                                                          ("256x256", 64)]
 
 
 def test_each_kernel_is_taken_somewhere():
