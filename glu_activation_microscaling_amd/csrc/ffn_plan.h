@@ -32,35 +32,47 @@ struct ProductPlan {
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// What a tile takes, in microseconds a step of BK elements and for its start and end, from calls of
-// one round of workgroups (2048 to 8192 rows, sums of 1024 to 8192 elements), and what joining the
-// parts of a split sum takes.  The least total over the first three sizes decides.  Measured for
-// [I, J, K], 256x256 / 256x128 / 128x128:
-//   [ 1000, 1000, 1000]  22.5 / 15.8 / 11.2      [ 4096, 4096, 1024]  31.5 /  41.6 /  45.7
-//   [  968, 2048,16384]   237 / 65.8 / 72.0      [ 4096, 4096, 4096]  95.7 / 113.7 / 136.3
-//   [ 2048, 4096, 4096]  72.9 / 58.2 / 69.1      [16384, 2048, 2048]   102 /   126 /   151
-// (of 33 such shapes the rule takes the fastest of the three on 31 and is 0.5% and 6% behind on the others).
 constexpr int64_t kUnits = 256;
-constexpr double kStepUs[3] = {1.22, 0.85, 0.5}, kTileUs[3] = {15.0, 5.0, 4.0}, kJoinUs = 2.5, kJoinTBps = 5.0;
-constexpr double kStepFewUs[3] = {1.22, 0.85, 0.41};   // of a step while at most half the chip works
-constexpr int64_t kLeastPart = 512;   // elements of a split sum's part: 256 costs up to 5 us more, and gains 0.5
 
-// The number of parts of a sum that takes the least time by these figures: one, a power of two or the most, at
-// least kLeastPart elements each and one round of workgroups in all.  Measured in a graph, 128 x 128 tiles, the most
-// parts / the rule's: [2048, 1024, 1024] 20.2 (2) / 10.6 us (1), [512, 2048, 2048] 20.4 (4) / 17.7 (2; 16.0 whole),
-// [968, 2048, 2048] 20.3 (2) / 16.8 (1), [1021, 1000, 2056] 20.2 (4) / 18.6 (2; 22.9 whole), [1024, 1024, 4096] 20.0 (4)
-// / the same (26 whole).
+// What a tile takes, in microseconds a step of the sum and for its start and end, and what joining the parts of a split
+// sum takes.  The least total over the first three sizes decides.
+struct ProductCost {
+  double step[3];            // while more than half the chip works
+  double few[3];             // while at most half of it does
+  double tile[3];
+  // how much longer a step takes where operand rows start off a 128-byte line, so that a load asks for two lines
+  double off_line[3], off_line_few[3];
+  double join_us, join_tbps;
+  int64_t least;             // elements of a part of the sum
+};
+// Fitted to the linear products, their gradients and products of groups at each size and count of parts, 181 calls of
+// up to eight rounds of workgroups: of them the rule takes the fastest or is within 3% of it but for seven (3 to 8%).
+// Measured for [I, J, K], in a graph, 256x256 / 256x128 / 128x128:
+//   [ 1000, 1000, 1000]  22.2 / 19.2 / 13.6      [ 4096, 4096, 1024]  31.7 /  40.2 /  45.7
+//   [  968, 2048, 4096]  66.2 / 43.8 / 29.9      [ 4096, 4096, 4096]  94.1 / 113.6 / 132.5
+//   [ 2048, 4096, 4096]  75.6 / 58.4 / 68.4      [ 6000, 4096, 2048]  91.1 /  93.6 / 111.1
+//   gradient of x [2048, 8192, 512]  23.5 / 30.3 / 31.9      of W, 8 groups, 4096 rows, [4096, 2048]  85.6 / 111 / 123
+// and in 1 / 2 / 3 / 4 parts, 128x128: [512, 2048, 2048] 16.9 / 19.1 / 19.1 / 20.6, [1021, 1000, 2056] 23.3 / 19.0 / 19.4 /
+// 20.2, [1024, 1024, 4096] 28.3 / 22.6 / 20.7 / 21.2.
+constexpr ProductCost kLinearCost = {{1.0, 0.76, 0.48}, {0.95, 0.65, 0.40}, {12.0, 7.5, 4.7}, {1.0, 1.1, 1.4}, {1.0, 1.05, 1.2},
+                                     4.0, 6.0, 512};
+
+// The number of parts of a sum that takes the least time: one, a power of two or the most, at least cost.least
+// elements each and one round of workgroups in all.
 struct Parts {
   int64_t splits;
   double us;
 };
-inline Parts best_parts(int kind, int64_t tiles, int64_t K, int64_t steps, int64_t outputs, bool whole) {
-  const int64_t fit = whole ? 1 : K / kLeastPart < kUnits / tiles ? K / kLeastPart : kUnits / tiles, most = fit < 1 ? 1 : fit;
+inline Parts best_parts(const ProductCost& cost, int kind, int64_t tiles, int64_t K, int64_t steps, int64_t outputs, bool whole,
+                        bool off_line) {
+  const int64_t fit = whole ? 1 : K / cost.least < kUnits / tiles ? K / cost.least : kUnits / tiles, most = fit < 1 ? 1 : fit;
   Parts best{0, 0.0};
   for (int64_t splits = 1;;) {
-    const double step = tiles * splits <= kUnits / 2 ? kStepFewUs[kind] : kStepUs[kind];
-    double us = (kTileUs[kind] + step * ceil_div(steps, splits)) * ceil_div(tiles * splits, kUnits);
-    if (splits > 1) us += kJoinUs + 8e-6 / kJoinTBps * splits * outputs;
+    const bool half = tiles * splits <= kUnits / 2;
+    double step = half ? cost.few[kind] : cost.step[kind];
+    if (off_line) step *= half ? cost.off_line_few[kind] : cost.off_line[kind];
+    double us = (cost.tile[kind] + step * ceil_div(steps, splits)) * ceil_div(tiles * splits, kUnits);
+    if (splits > 1) us += cost.join_us + 8e-6 / cost.join_tbps * splits * outputs;
     if (best.splits == 0 || us < best.us) best = {splits, us};
     if (splits == most) return best;
     splits = 2 * splits < most ? 2 * splits : most;
@@ -100,7 +112,8 @@ inline ProductPlan plan_one(int mode, int64_t I, int64_t J, int64_t K, int64_t g
   for (int kind = TILE_256; kind <= TILE_128; kind++) {
     const int64_t ti = ceil_div(I, kShape[kind].rows()), tj = ceil_div(J, kShape[kind].cols());
     const int64_t tiles = (ti + (cut ? groups / 2 : 0)) * tj * outer;
-    const Parts parts = best_parts(kind, tiles, K, steps, I * J, whole || grouped || kind == TILE_256);
+    const Parts parts = best_parts(kLinearCost, kind, tiles, K, steps, I * J, whole || grouped || kind == TILE_256,
+                                   mode == FWD && K % BK != 0);
     if (best == 0.0 || parts.us < best) {
       best = parts.us;
       p.kind = kind;
@@ -132,7 +145,8 @@ inline int plan_gradients(int64_t M, int64_t N, int64_t K) {
     const int64_t rows = kShape[k].rows(), j = ceil_div(K, kShape[k].cols());
     const int64_t tiles = ceil_div(M, rows) * j + ceil_div(N, rows) * j;
     if (tiles > kUnits) continue;
-    const double us = kTileUs[k] + (tiles <= kUnits / 2 ? kStepFewUs[k] : kStepUs[k]) * ceil_div(M > N ? M : N, BK);
+    const ProductCost& c = kLinearCost;
+    const double us = c.tile[k] + (tiles <= kUnits / 2 ? c.few[k] : c.step[k]) * ceil_div(M > N ? M : N, BK);
     if (us < best) {
       best = us;
       kind = k;
@@ -153,10 +167,16 @@ inline ProductPlan plan_product(int mode, int64_t I, int64_t J, int64_t K, int64
 // Columns of a gated product's sums: 16 gate and 16 up for each 16 outputs.
 constexpr int64_t gated_columns(int64_t J) { return (J + 15) / 16 * 32; }
 
-// The tile sizes of the linear products, each with waves of 64 columns of the sums (32 outputs).  The rule
-// counts the time of the products' loops, the same here ([1021, 2 x 1000, 2056] 128 x 128 in one piece 26 us, in two
-// parts 18 and 6 to join them); the epilogue adds up to 5 us a 256 x 256 tile where gate and up are kept.
+// The tile sizes of the linear products, each with waves of 64 columns of the sums (32 outputs).  Their loops take the
+// linear products' time; a tile's end takes 1 us more, and up to 5 a 256 x 256 tile where gate and up are kept.  Of 79 calls
+// as above the rule is 3 to 7% behind on twelve: where three or six parts would be best, and [1021, 2 x 1000, 2056], which
+// it leaves whole.  With codes, in a graph, 256x256
+// / 256x128 / 128x128: [968, 2 x 1024, 2048] 43.0 / 28.2 / 19.5, [2048, 2 x 2048, 4096] 83.3 / 60.5 / 75.1, [4096, 2 x 2048,
+// 1024] 36.4 / 44.7 / 55.4, 16 groups, 8192 rows, [2 x 2048, 1024] 99.3 / 129 / 143; in 1 / 2 / 4 parts, 128x128, [1021, 2 x
+// 1000, 2056] 25.7 / 24.4 / 30.8, [128, 2 x 4096, 4096] 30.3 / 24.0 / 22.9.
 constexpr TileShape kGatedShape[4] = {{2, 4, 8, 4, 2}, {4, 2, 4, 4, 3}, {4, 2, 2, 4, 3}, {2, 2, 1, 4, 4}};
+constexpr ProductCost kGatedCost = {{1.1, 0.76, 0.48}, {0.95, 0.65, 0.40}, {13.5, 8.0, 5.5}, {1.0, 1.1, 1.4}, {1.0, 1.05, 1.2},
+                                    4.0, 6.0, 512};
 
 // Codes need whole blocks of 32 outputs, which the few rows' kernel does not have.
 inline ProductPlan plan_gated(bool codes, int64_t I, int64_t N, int64_t K, int64_t groups, bool grouped) {
@@ -183,7 +203,7 @@ inline ProductPlan plan_gated(bool codes, int64_t I, int64_t N, int64_t K, int64
   for (int kind = TILE_256; kind <= TILE_128; kind++) {
     const int64_t ti = ceil_div(I, kGatedShape[kind].rows()), tj = ceil_div(J, kGatedShape[kind].cols());
     const int64_t tiles = (ti + (grouped ? groups / 2 : 0)) * tj;
-    const Parts parts = best_parts(kind, tiles, K, steps, I * J, grouped || kind == TILE_256);
+    const Parts parts = best_parts(kGatedCost, kind, tiles, K, steps, I * J, grouped || kind == TILE_256, K % BK != 0);
     if (best == 0.0 || parts.us < best) {
       best = parts.us;
       p.kind = kind;
@@ -200,16 +220,16 @@ inline ProductPlan plan_gated(bool codes, int64_t I, int64_t N, int64_t K, int64
 constexpr int64_t kFp8Block = 128;   // elements of the sum with a scale of their own
 inline int64_t fp8_blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
 
-// What a tile takes, in microseconds a block of the sum and for its start and end, from calls of one to eight
-// rounds of workgroups, and what joining the parts of a split sum takes; the least total over the first
-// three sizes decides.  Measured for [I, J, K], 256x256 / 256x128 / 128x128 (parts of the sum):
-//   [ 1021, 1000, 2048]  30 / 20.7 / 15.0             [ 4096, 4096, 4096]  61.6 / 76.3 / 95.8
-//   [  968, 2048,16384]  50.5 (8) / 49.8 (4) / 54.4 (2)   [16384, 2048, 2048]  69.6 / 88.4 / 110
-//   [ 2048, 4096, 4096]  49.0 / 41.4 / 49.3           16 groups [8192, 4096, 2048]  102 / 122 / 139
+// A step is a block of the sum.  22 calls of one to four rounds at each size and count of parts: the rule takes the
+// fastest or is within 1% of it but for two, 7 and 8% behind, where three or six parts would be best.  Measured for
+// [I, J, K], in a graph, 256x256 / 256x128 / 128x128 (parts of the sum):
+//   [ 1021, 1000, 2048]  24.9 / 20.7 / 14.3              [ 4096, 4096, 4096]  58.7 / 78.1 / 93.3
+//   [  968, 2048,16384]  47.7 (8) / 48.2 (4) / 52.2 (2)   [16384, 2048, 2048]  68.0 / 90.8 / 108
+//   [ 2048, 4096, 4096]  44.2 / 41.4 / 49.2              [ 6000, 4096, 2048]  58.0 / 65.9 / 79.4
+//   [   16, 2048, 2048]  24.1 / 19.4 / 13.1, 128x128 in 2 / 4 / 8 parts 11.1 / 9.7 / 9.7
 constexpr TileShape kFp8Shape[4] = {{2, 4, 8, 4, 2}, {4, 2, 4, 4, 3}, {2, 4, 4, 2, 3}, {1, 4, 2, 2, 4}};
-constexpr double kFp8StepUs[3] = {1.55, 1.05, 0.70}, kFp8TileUs[3] = {10.0, 6.0, 3.5}, kFp8JoinUs = 5.0,
-                 kFp8JoinTBps = 8.0;
-constexpr int64_t kFp8LeastPart = 8;   // blocks of a split sum's part
+constexpr ProductCost kFp8Cost = {{1.40, 1.04, 0.62}, {1.12, 0.98, 0.58}, {7.6, 5.2, 4.8}, {1.0, 1.0, 1.0}, {1.0, 1.0, 1.0},
+                                  4.0, 6.5, 512};
 
 inline ProductPlan plan_fp8(int64_t I, int64_t J, int64_t K, int64_t groups, bool grouped) {
   ProductPlan p{};
@@ -234,18 +254,13 @@ inline ProductPlan plan_fp8(int64_t I, int64_t J, int64_t K, int64_t groups, boo
   for (int kind = TILE_256; kind <= TILE_128; kind++) {
     const int64_t ti = ceil_div(I, kFp8Shape[kind].rows()), tj = ceil_div(J, kFp8Shape[kind].cols());
     const int64_t tiles = (ti + (grouped ? groups / 2 : 0)) * tj;
-    const int64_t most = grouped ? 1 : kUnits / tiles < blocks / kFp8LeastPart ? kUnits / tiles : blocks / kFp8LeastPart;
-    for (int q = 0; q < (most > 1 ? 2 : 1); q++) {   // one part, or the most
-      const int64_t splits = q == 0 ? 1 : most;
-      double us = (kFp8TileUs[kind] + kFp8StepUs[kind] * ceil_div(blocks, splits)) * ceil_div(tiles * splits, kUnits);
-      if (splits > 1) us += kFp8JoinUs + 8e-6 / kFp8JoinTBps * splits * I * J;
-      if (best == 0.0 || us < best) {
-        best = us;
-        p.kind = kind;
-        p.tiles_i = ti + (grouped ? groups + 1 : 0);
-        p.tiles_j = tj;
-        p.splits = splits;
-      }
+    const Parts parts = best_parts(kFp8Cost, kind, tiles, K, blocks, I * J, grouped, false);
+    if (best == 0.0 || parts.us < best) {
+      best = parts.us;
+      p.kind = kind;
+      p.tiles_i = ti + (grouped ? groups + 1 : 0);
+      p.tiles_j = tj;
+      p.splits = parts.splits;
     }
   }
   return p;

@@ -50,3 +50,19 @@ def test_a_gradients_parts_do_not_depend_on_the_other():
     joint = [i for i, (kernel, _) in enumerate(both) if kernel is not None]
     assert len(joint) > 50 and all(dx[i][1] == 1 and dw[i][1] == 1 for i in joint)
     assert sum(p > 1 for _, p in dx) > 50
+
+
+def test_measured_shapes_take_the_fastest():
+    """Calls whose times at each tile size and count of parts stand beside the rules."""
+    fastest = {
+        ("linear", 1000, 1000, 1000, 0): ("128x128", 1), ("linear", 512, 2048, 2048, 0): ("128x128", 1),
+        ("linear", 1021, 1000, 2056, 0): ("128x128", 2), ("linear", 968, 2048, 4096, 0): ("128x128", 2),
+        ("linear", 968, 2048, 16384, 0): ("256x128", 4), ("linear", 2048, 4096, 4096, 0): ("256x128", 1),
+        ("linear", 4096, 4096, 1024, 0): ("256x256", 1), ("linear", 6000, 4096, 2048, 0): ("256x256", 1),
+        ("linear", 5000, 4096, 1024, 0): ("256x256", 1), ("dx", 2048, 512, 8192, 0): ("256x256", 1),
+        ("dx", 2048, 512, 2048, 0): ("128x128", 1), ("dw", 4096, 4096, 2048, 8): ("256x256", 1),
+        ("linear", 8192, 4096, 1024, 16): ("256x256", 1), ("gated", 8192, 2048, 1024, 16): ("256x256", 1),
+        ("gated8", 968, 1024, 2048, 0): ("128x128", 1), ("gated8", 2048, 2048, 4096, 0): ("256x128", 1),
+        ("fp8", 6000, 4096, 2048, 0): ("256x256", 1), ("fp8", 16, 2048, 2048, 0): ("128x128", 4),
+        ("fp8", 1021, 1000, 2048, 0): ("128x128", 1), ("fp8", 2048, 4096, 4096, 0): ("256x128", 1)}
+    assert dict(zip(fastest, plans(list(fastest)))) == fastest
