@@ -139,10 +139,12 @@ __device__ __forceinline__ void fp8_store(const Fp8Args& a, const Fp8Tile& o, ui
 
 // The loops below multiply the two scales of a sum first, which takes a multiplication a row or column where the sums
 // are many.  Two scales can be too large for that and still belong to a finite result, zero among them (the
-// largest magnitudes of a block of x and of W then multiply to more than 2^145).  So the loops keep the largest product
-// of scales that they met (NaN aside), and where that is infinite the wave forms its sums again, the smaller scale
-// first, straight from memory.  [16384, 7168, 2048] 232 / 234 us without and with that test, 3900 where all scales are
-// too large.  (A product too small for FP32 is rounded to its subnormal numbers: an error of up to 2^-125 a block.)
+// largest magnitudes of a block of x and of W then multiply to more than 2^145).  The sum is infinite or NaN then, and
+// stays so: the wave forms its sums again, the smaller scale first, straight from memory.  The largest tile knows
+// from the largest product of scales that it met (NaN aside), 1 us of 230 at [16384, 7168, 2048]; the others, whose
+// steps have no time to spare for that (2% at [2048, 4096, 4096]), look at their sums.  [4096, 4096, 2048] takes 39 us,
+// 38 where all scales are NaN, 580 where all are too large.  (A product too small for FP32 is rounded to its
+// subnormal numbers: an error of up to 2^-125 a block.)
 template <int N>
 __device__ __forceinline__ float largest(float m, const float (&v)[N]) {
 #pragma unroll
@@ -161,10 +163,22 @@ __device__ __forceinline__ float add_scaled(float acc, float p, float sx, float 
   const bool less = __builtin_fabsf(sx) < __builtin_fabsf(sw);   // a NaN stays whichever it is
   return __builtin_fmaf(p * (less ? sx : sw), less ? sw : sx, acc);
 }
+template <int TI, int TJ>
+__device__ __forceinline__ bool all_finite(const v4f (&acc)[TI][TJ]) {
+  v4f none = (v4f)0.0f;   // NaN where a sum is infinite or NaN
+#pragma unroll
+  for (int i = 0; i < TI; i++)
+#pragma unroll
+    for (int j = 0; j < TJ; j++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) none[e] = __builtin_fmaf(acc[i][j][e], 0.0f, none[e]);
+  return (none[0] + none[1]) + (none[2] + none[3]) == 0.0f;
+}
+// suspect: the lane's sums may be of such scales.
 template <int W_SCALES, int TI, int TJ>
-__device__ __forceinline__ void fp8_large_scales(v4f (&acc)[TI][TJ], float most, const Fp8Args& a, const Fp8Tile& o,
+__device__ __forceinline__ void fp8_large_scales(v4f (&acc)[TI][TJ], bool suspect, const Fp8Args& a, const Fp8Tile& o,
                                                  uint32_t row0, uint32_t col0, uint32_t lane) {
-  if (__builtin_expect(__builtin_amdgcn_ballot_w64(most == __builtin_inff()) == 0, true) || col0 >= o.cols) return;
+  if (__builtin_expect(__builtin_amdgcn_ballot_w64(suspect) == 0, true) || col0 >= o.cols) return;
   constexpr bool BLOCK = W_SCALES == FP8_W_BLOCK;
   const uint32_t g = lane >> 4, r = lane & 15u, K = 2u * (uint32_t)a.K;
   const int64_t group = o.t.group;   // a tile of no group has no steps and does not get here
@@ -179,6 +193,21 @@ __device__ __forceinline__ void fp8_large_scales(v4f (&acc)[TI][TJ], float most,
     if constexpr (BLOCK) return (v4f)ws[s];
     else return col < o.cols ? *reinterpret_cast<const v4f*>(ws + s * a.J + col) : (v4f)0.0f;
   };
+  float most = 0.0f;   // the largest product of two scales, NaN and infinite ones aside
+  for (uint32_t s = o.s0; s < o.s1; s++) {
+    float x = 0.0f, w = 0.0f;
+    auto take = [](float& m, float v) {
+      v = __builtin_fabsf(v);
+      m = v > m && v < __builtin_inff() ? v : m;
+    };
+    for (int i = 0; i < TI; i++) take(x, x_scale(s, i));
+    for (int j = 0; j < TJ; j++) {
+      const v4f v = w_scale(s, j);
+      for (int e = 0; e < 4; e++) take(w, v[e]);
+    }
+    most = __builtin_fmaxf(most, x * w);
+  }
+  if (__builtin_amdgcn_ballot_w64(most == __builtin_inff()) == 0) return;   // the sums are what they should be
   const auto rx = rsrc(uniform(a.a + o.t.i0 * a.ld_a)), rw = rsrc(uniform(a.b + group * a.b_group + o.j0 * a.ld_b));
   auto frag = [&](__amdgpu_buffer_rsrc_t from, uint32_t row, uint32_t rows, uint32_t s) {
     u32x4 v[2];
@@ -267,7 +296,6 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_fp8_product(Fp8Args a, uint32_
 #pragma unroll
     for (int q = 0; q < NS - 1; q++) issue(s0 + q, smem + q * STAGE);
     uint32_t now = 0;
-    float most = 0.0f;   // the largest product of two scales
     for (uint32_t s = s0; s < s1; s++) {
       wait_vm<(NS - 2) * LOADS>();
       lds_barrier();   // every wave's loads of this step have landed, and the step before has been read
@@ -290,7 +318,6 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_fp8_product(Fp8Args a, uint32_
         sx[i] = sc[16 * (TI * wi + i) + r];
       }
       __builtin_amdgcn_sched_barrier(0);   // these reads come back while the loads are started
-      most = __builtin_fmaxf(most, largest(0.0f, sx) * (W_SCALES == FP8_W_BLOCK ? __builtin_fabsf(sw[0][0]) : largest(0.0f, sw)));
       issue(s + NS - 1, smem + (now == 0 ? (NS - 1) * STAGE : now - STAGE));
 #pragma unroll
       for (int i = 0; i < TI; i++)
@@ -304,7 +331,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_fp8_product(Fp8Args a, uint32_
     }
     wait_vm<0>();
     lds_barrier();   // the stages hold the sums next
-    fp8_large_scales<W_SCALES>(acc, most, a, o, 16u * TI * wi, 16u * TJ * wj, lane);
+    fp8_large_scales<W_SCALES>(acc, !all_finite(acc), a, o, 16u * TI * wi, 16u * TJ * wj, lane);
   }
 
   if (splits > 1) {
@@ -514,7 +541,7 @@ __global__ __launch_bounds__(512) void k_fp8_turns(Fp8Args a, uint32_t tiles_i, 
     else turns(std::false_type{});
     wait_vm<0>();
     lds_barrier();   // the stages hold the sums next
-    fp8_large_scales<W_SCALES>(acc, most, a, o, 128u * wi, 64u * wj, lane);
+    fp8_large_scales<W_SCALES>(acc, most == __builtin_inff(), a, o, 128u * wi, 64u * wj, lane);
   }
 
   // acc[i][j][e] is row 16 i + r and column 16 j + 4 g + e of the wave's
