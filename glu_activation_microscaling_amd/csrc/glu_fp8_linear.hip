@@ -354,17 +354,10 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_fp8_product(Fp8Args a, uint32_
   });
 }
 
-// The largest tile, 256 x 256, 8 waves of 128 x 64 as 4 x 2 tiles of 32 x 32.
-//
-// Waves 0 .. 3 (one a SIMD) read a step's fragments while waves 4 .. 7 multiply, and the other way round;
-// each turn ends with a barrier.  The first half reads step s in turn 2 s and multiplies in turn 2 s + 1, the
-// second half one turn later.  Starting loads takes a wave a while (the CU takes some 45 bytes a clock), so
-// that is done in the reading turns alone, and each half has two turns to see its loads landed:
-//   the first half starts in turn 2 s the loads of step s + 1 of its own rows of A and of the low columns
-//     of B (both halves have read step s - 1 of those by the end of turn 2 s - 1: two stages);
-//   the second half in turn 2 s + 1 those of step s + 1 of its own rows of A, which it reads in turn 2 s + 3,
-//     and of step s + 2 of the high columns of B, which the first half reads in turn 2 s + 4: three stages.
-// Registers hold B's fragments and half of A's; the others are read while multiplying.
+// The largest tile, 256 x 256, 8 waves of 128 x 64 as 8 x 4 tiles of 16 x 16.  The halves of the waves take turns and
+// load as in the largest tile of the BF16 products (product_tile in ffn_product.h), a block of the sum a step; the rows'
+// scales come with the low columns of B, the columns' with the high ones.  (Starting loads takes a wave a
+// while, the CU taking some 45 bytes a clock.)
 //
 // Beside a 16 x 16 x 128 product the vector unit has time for the four additions it needs, and little
 // else: the scales are read and multiplied in the reading turn.
