@@ -970,54 +970,11 @@ __global__ __launch_bounds__(256) void k_product_join(ProductArgs a, uint32_t sp
 // load takes 128 bytes of a row.  KW waves share the sum, taking chunks of 128 elements in turn, and
 // join through LDS, so a call is one launch whatever its extents.  The next chunks of W are in
 // flight while the present ones are multiplied.  [1, 2048, 16384]: 13.2 to 14.9 us (4.5 to 5.1 TB/s).
-//
-// A wave's share of such sums, chunks from element `first` of the sum, `stride` apart: rows of W and of x at the
-// lane's offsets (element `mine` of its row's first chunk), as 16 x 16 x 32 tiles added to acc.
-__device__ __forceinline__ void few_sum(v4f& acc, __amdgpu_buffer_rsrc_t rw, uint32_t wo, __amdgpu_buffer_rsrc_t rx, uint32_t xo,
-                                        uint32_t mine, uint32_t first, uint32_t stride, uint32_t k1) {
-  constexpr int U = 4, STEPS = 2;   // chunks per stage; tiles per chunk
-  v8bf w[2][U][STEPS];
-  auto load_w = [&](uint32_t k, int s) {
-#pragma unroll
-    for (int c = 0; c < U; c++)
-#pragma unroll
-      for (int u = 0; u < STEPS; u++) {
-        const uint32_t kk = k + stride * c + FEW_CHUNK / STEPS * u;
-        w[s][c][u] = __builtin_bit_cast(
-            v8bf, __builtin_amdgcn_raw_buffer_load_b128(rw, kk + mine < k1 ? wo : kOob, (int)(2u * kk), 0));
-      }
-  };
-  // x of this stage before W of the next: loads return in order, and the products wait for x
-  auto step = [&](uint32_t k, int s) {
-    v8bf x[U][STEPS];
-#pragma unroll
-    for (int c = 0; c < U; c++)
-#pragma unroll
-      for (int u = 0; u < STEPS; u++) {
-        const uint32_t kk = k + stride * c + FEW_CHUNK / STEPS * u;
-        x[c][u] = __builtin_bit_cast(
-            v8bf, __builtin_amdgcn_raw_buffer_load_b128(rx, kk + mine < k1 ? xo : kOob, (int)(2u * kk), 0));
-      }
-    __builtin_amdgcn_sched_barrier(0);
-    if (k + stride * U < k1) load_w(k + stride * U, 1 - s);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int c = 0; c < U; c++)
-#pragma unroll
-      for (int u = 0; u < STEPS; u++)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[s][c][u], x[c][u], acc, 0, 0, 0);
-  };
-  load_w(first, 0);
-  for (uint32_t k = first; k < k1; k += 2 * stride * U) {
-    step(k, 0);
-    if (k + stride * U < k1) step(k + stride * U, 1);
-  }
-}
-
 // grid: column tiles of FEW_COLS FEW_WAVES / KW
 template <int ACT, int KW>
 __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_few_rows(ProductArgs a) {
   __shared__ v4f sums[FEW_WAVES][64];
+  constexpr int U = 4, STEPS = 2;   // chunks per stage; tiles per chunk
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n0 = FEW_COLS * ((int64_t)blockIdx.x * (FEW_WAVES / KW) + wave / KW);
@@ -1028,7 +985,42 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_few_rows(ProductArgs a) {
     const uint32_t wo = n0 + r < a.J ? 2u * (r * (uint32_t)a.ld_b + mine) : kOob;
     const uint32_t xo = r < a.I ? 2u * (r * (uint32_t)a.ld_a + mine) : kOob;
     const auto rw = rsrc(uniform(a.b + n0 * a.ld_b)), rx = rsrc(uniform(a.a));
-    few_sum(acc, rw, wo, rx, xo, mine, first, stride, k1);
+    v8bf w[2][U][STEPS];
+    auto load_w = [&](uint32_t k, int s) {
+#pragma unroll
+      for (int c = 0; c < U; c++)
+#pragma unroll
+        for (int u = 0; u < STEPS; u++) {
+          const uint32_t kk = k + stride * c + FEW_CHUNK / STEPS * u;
+          w[s][c][u] = __builtin_bit_cast(
+              v8bf, __builtin_amdgcn_raw_buffer_load_b128(rw, kk + mine < k1 ? wo : kOob, (int)(2u * kk), 0));
+        }
+    };
+    // x of this stage before W of the next: loads return in order, and the products wait for x
+    auto step = [&](uint32_t k, int s) {
+      v8bf x[U][STEPS];
+#pragma unroll
+      for (int c = 0; c < U; c++)
+#pragma unroll
+        for (int u = 0; u < STEPS; u++) {
+          const uint32_t kk = k + stride * c + FEW_CHUNK / STEPS * u;
+          x[c][u] = __builtin_bit_cast(
+              v8bf, __builtin_amdgcn_raw_buffer_load_b128(rx, kk + mine < k1 ? xo : kOob, (int)(2u * kk), 0));
+        }
+      __builtin_amdgcn_sched_barrier(0);
+      if (k + stride * U < k1) load_w(k + stride * U, 1 - s);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int c = 0; c < U; c++)
+#pragma unroll
+        for (int u = 0; u < STEPS; u++)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[s][c][u], x[c][u], acc, 0, 0, 0);
+    };
+    load_w(first, 0);
+    for (uint32_t k = first; k < k1; k += 2 * stride * U) {
+      step(k, 0);
+      if (k + stride * U < k1) step(k + stride * U, 1);
+    }
   }
   sums[wave][lane] = acc;
   __syncthreads();

@@ -107,11 +107,14 @@ __global__ __launch_bounds__(256) void k_gated_join(GatedArgs a, uint32_t splits
 // Up to 8 rows of one group: a pass over W at memory speed, as the linear products' (k_few_rows): a wave
 // takes 8 rows of W of one kind straight from memory into 16 x 16 x 32 tiles whose other halves are
 // the same rows 32 elements on.  Of 2 KW waves that share 8 outputs, KW take the gates and KW the ups,
-// each kind cutting the sum among them; they meet in LDS.  [1, 2 x 16384, 2048]: 26.5 us (134 MB, 5.1 TB/s).
+// each kind cutting the sum among them; they meet in LDS.  [1, 2 x 16384, 2048]: 26.5 us (134 MB, 5.1 TB/s).  (The loop
+// is that of k_few_rows again: as a function of both, its first loads start in another order, 14.4 us for 14.1 at
+// [1, 2048, 16384].)
 // grid: tiles of 8 outputs for 2 KW waves
 template <int ACT, int KW>
 __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_gated_few(GatedArgs a) {
   __shared__ v4f sums[FEW_WAVES][64];
+  constexpr int U = 4, STEPS = 2;   // chunks per stage; tiles per chunk
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t n0 = FEW_COLS * ((int64_t)blockIdx.x * (FEW_WAVES / 2 / KW) + wave / (2 * KW));
@@ -124,7 +127,42 @@ __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_gated_few(GatedArgs a) {
     const uint32_t wo = n0 + r < a.J ? 2u * (r * (uint32_t)step + mine) : kOob;
     const uint32_t xo = r < a.I ? 2u * (r * (uint32_t)a.ld_a + mine) : kOob;
     const auto rw = rsrc(uniform(a.b + n0 * step + (!up ? 0 : a.paired ? a.K : a.J * a.K))), rx = rsrc(uniform(a.a));
-    few_sum(acc, rw, wo, rx, xo, mine, first, stride, k1);
+    v8bf w[2][U][STEPS];
+    auto load_w = [&](uint32_t k, int s) {
+#pragma unroll
+      for (int c = 0; c < U; c++)
+#pragma unroll
+        for (int u = 0; u < STEPS; u++) {
+          const uint32_t kk = k + stride * c + FEW_CHUNK / STEPS * u;
+          w[s][c][u] = __builtin_bit_cast(
+              v8bf, __builtin_amdgcn_raw_buffer_load_b128(rw, kk + mine < k1 ? wo : kOob, (int)(2u * kk), 0));
+        }
+    };
+    // x of this stage before W of the next: loads return in order, and the products wait for x
+    auto step_of = [&](uint32_t k, int s) {
+      v8bf x[U][STEPS];
+#pragma unroll
+      for (int c = 0; c < U; c++)
+#pragma unroll
+        for (int u = 0; u < STEPS; u++) {
+          const uint32_t kk = k + stride * c + FEW_CHUNK / STEPS * u;
+          x[c][u] = __builtin_bit_cast(
+              v8bf, __builtin_amdgcn_raw_buffer_load_b128(rx, kk + mine < k1 ? xo : kOob, (int)(2u * kk), 0));
+        }
+      __builtin_amdgcn_sched_barrier(0);
+      if (k + stride * U < k1) load_w(k + stride * U, 1 - s);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int c = 0; c < U; c++)
+#pragma unroll
+        for (int u = 0; u < STEPS; u++)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[s][c][u], x[c][u], acc, 0, 0, 0);
+    };
+    load_w(first, 0);
+    for (uint32_t k = first; k < k1; k += 2 * stride * U) {
+      step_of(k, 0);
+      if (k + stride * U < k1) step_of(k + stride * U, 1);
+    }
   }
   sums[wave][lane] = acc;
   __syncthreads();
