@@ -540,16 +540,16 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& a, int64_t group
 //
 // Bound by the matrix cores at large sizes; what is lost there is the start and the end of a tile,
 // which nothing overlaps (one workgroup fills a compute unit's LDS).  Measured on an MI355X:
-//   256x256  [16384, 7168, 2048] (I, J, K) alone 343 to 354 us (1.4 PFLOP/s), with bias, GELU, residual
+//   256x256  [16384, 7168, 2048] (I, J, K) alone 343 to 362 us (1.4 PFLOP/s), with bias, GELU, residual
 //            and saved pre-activation 434 to 456; gradient of x 329 to 343, of W 357 to 378
 //            8192^3 711 (1.55 PFLOP/s; 601 on zeros)
 //            16 groups, 16384 rows, [4096, 2048]: 257 to 270, gradients 266 to 291 and 274 to 294
-//            gated, [16384, 2 x 7168, 2048]: 770 to 786 with gate and up kept (716 for the product alone); 16
-//            groups, 16384 rows, [2 x 2048, 2048]: 268 to 285 with them kept as MXFP8; [968, 2 x 16384, 2048] 104
+//            gated, [16384, 2 x 7168, 2048]: 770 to 842 with gate and up kept (716 for the product alone); 16
+//            groups, 16384 rows, [2 x 2048, 2048]: 268 to 326 with them kept as MXFP8; [968, 2 x 16384, 2048] 104 to 113
 //   256x128  [968, 2048, 16384] in four parts 59 us (1.1 PFLOP/s), and 7 to join them
 //   128x128  [1021, 1000, 2056] in two parts 16.0 us, and 4.4 to join them
 //   both gradients of it in one launch of 256x128 tiles 20.5 us (one after the other 14.6 and 13.8)
-//   32x128   32 groups, 256 rows, [2048, 2048], W from memory: 49 us (5.5 TB/s)
+//   32x128   32 groups, 256 rows, [2048, 2048], W from memory: 49 us (5.5 TB/s); gated, [2 x 2048, 2048], 97 to 102
 // Tried and slower at [16384, 7168, 2048] (forward with epilogue, eight waves in step, 500 to 540 us): 128x128 tiles 637;
 // 4 waves of 128x128 798; four stages of 32 elements 558; two workgroups of 256x128 and three
 // stages of 32 a compute unit 581; workgroups that stay and load the next tile during the

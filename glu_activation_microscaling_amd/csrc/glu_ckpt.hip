@@ -31,7 +31,7 @@ __device__ __forceinline__ void unpack8(float (&v)[8], u32x4 p) {
   }
 }
 
-// Measured at [16384, 7168] with h: 162 to 173 us (969 MB, 5.6 to 6.0 TB/s); [1021, 1000] 5.0, [128, 128] 3.0.
+// Measured at [16384, 7168] with h: 162 to 178 us (969 MB, 5.4 to 6.0 TB/s); [1021, 1000] 5.0, [128, 128] 2.8 to 3.2.
 // grid: (256 columns, row blocks)
 template <int ACT, int LAYOUT>
 __global__ __launch_bounds__(256) void k_ckpt_fwd(CkptArgs a) {
@@ -101,7 +101,7 @@ __device__ __forceinline__ void widen8(float (&v)[8], u32x4 p, uint32_t rest) {
   v[7] = wide_value<7>(p[3] & 0xffff0000u, rest);
 }
 
-// Measured at [16384, 7168]: from codes with h 217 to 221 us (1234 MB, 5.6 TB/s), from BF16 and four more bits
+// Measured at [16384, 7168]: from codes with h 217 to 224 us (1234 MB, 5.5 TB/s), from BF16 and four more bits
 // without h 250 to 254 (1292 MB, 5.1 TB/s); [1021, 1000] 6.6, with sums 7.6.
 // grid: (256 columns, group, part of the group's rows); with sums and h, group number `groups` is the
 // rows of no group, whose h is formed too.

@@ -101,8 +101,9 @@ __global__ __launch_bounds__(256) void k_fp8_row(Fp8QuantArgs a) {
 // A tile of 128 x 128: thread (lr, lc) has rows 8 lr .. + 7 and columns 8 lc .. + 7.
 //   ROW  codes of each row under the row's scale;  COL  of each column, transposed
 //   BLOCK  one scale for the tile, codes as they are and, with COL, transposed
-// Rows and columns of [16384, 7168] 109 to 114 us (477 MB, 4.3 TB/s: the tile is loaded, turned and stored one after
-// the other, and other workgroups fill the gaps), of [16384, 2048] 35 to 38, weights [7168, 2048] both ways 16 to 17.
+// Rows and columns of [16384, 7168] 108 to 117 us (477 MB, 4.1 to 4.4 TB/s: the tile is loaded, turned and stored one after
+// the other, and other workgroups fill the gaps), of [16384, 2048] 35 to 38, weights [7168, 2048] both ways 16 to 17;
+// of the GLU of [16384, 7168] 168 to 170 (712 MB, 4.2 TB/s).
 struct TileArgs {
   int64_t M, N, ld_in;
   const uint16_t* gate;

@@ -236,8 +236,8 @@ __device__ __forceinline__ void fp8_large_scales(v4f (&acc)[TI][TJ], bool suspec
 }
 
 // WI x WJ waves of TI x TJ tiles of 16 x 16 each, NS stages of one block of the sum in LDS, filled by
-// direct copies NS - 1 blocks ahead.  256 x 128: [968, 2048, 16384] in four parts 44 to 48 us (1.4 PFLOP/s), and 7 to join
-// them; 32 x 128: 32 groups, 256 rows, [2048, 2048] 31 us (4.3 TB/s).
+// direct copies NS - 1 blocks ahead.  256 x 128: [968, 2048, 16384] in four parts 44 to 49 us (1.4 PFLOP/s), and 7 to join
+// them; 32 x 128: 32 groups, 256 rows, [2048, 2048] 31 to 32 us (4.3 TB/s).
 template <int W_SCALES, int WI, int WJ, int TI, int TJ, int NS>
 __global__ __launch_bounds__(64 * WI * WJ) void k_fp8_product(Fp8Args a, uint32_t tiles_i, uint32_t tiles_j,
                                                               uint32_t splits) {
@@ -362,8 +362,8 @@ __global__ __launch_bounds__(64 * WI * WJ) void k_fp8_product(Fp8Args a, uint32_
 // Beside a 16 x 16 x 128 product the vector unit has time for the four additions it needs, and little
 // else: the scales are read and multiplied in the reading turn.
 //
-// Measured, [I, J, K]: [8192, 8192, 8192] 405 us (2.7 PFLOP/s), [16384, 7168, 2048] 226 to 239 (2.0; 16 blocks, of which a
-// tile's start and end cost seven more), [16384, 2048, 7168] 187 to 199, row scales [7168, 2048, 16384] 225 to 238 (the
+// Measured, [I, J, K]: [8192, 8192, 8192] 405 us (2.7 PFLOP/s), [16384, 7168, 2048] 224 to 245 (2.0; 16 blocks, of which a
+// tile's start and end cost seven more), [16384, 2048, 7168] 187 to 209, row scales [7168, 2048, 16384] 225 to 279 (the
 // products of two scales beside the additions), 16 groups, 8192 rows, [4096, 2048] 97 to 105.  All eight waves in step:
 // 8192^3 2.10 PFLOP/s; 32 x 32 x 64 products need more registers than there are.
 template <int W_SCALES>
@@ -563,7 +563,7 @@ __global__ __launch_bounds__(512) void k_fp8_turns(Fp8Args a, uint32_t tiles_i, 
 // Up to 8 rows of one group: a pass over W at memory speed.  A wave takes 8 rows of W straight from
 // memory; rows 8 .. 15 of its 16 x 16 x 128 tiles are the same ones in the next block of the sum, and so
 // are columns 8 .. 15 of x: the halves that match are kept, each under its own block's scales.  KW waves
-// share the sum, two blocks at a time in turn, and join through LDS.  [1, 2048, 16384]: 9.5 us (34 MB, 3.6 TB/s; half
+// share the sum, two blocks at a time in turn, and join through LDS.  [1, 2048, 16384]: 9.0 to 10.1 us (34 MB, 3.6 TB/s; half
 // of it is the start and the join).
 // grid: column tiles of FEW_COLS FEW_WAVES / KW
 template <int W_SCALES, int KW>

@@ -418,7 +418,8 @@ glu_status glu_linear(int act, int64_t M, int64_t N, int64_t K, int64_t groups, 
                       const uint16_t* residual, int64_t ld_res, uint16_t* y, int64_t ld_y, uint16_t* pre,
                       void* work, int64_t work_bytes, void* stream);
 
-/* dp = dy act'(p);  dx = dp W,  dw[e] = dp^T x and db[e] = sum of dp over the rows of group e.
+/* dp = dy act'(p), rounded to BF16 for the products (with act GLU_LINEAR_NONE it is dy);  dx = dp W,
+ * dw[e] = dp^T x and db[e] = sum of dp, unrounded, over the rows of group e.
  * pre is the forward's (NULL when act is GLU_LINEAR_NONE).  dx [M, K], dw [groups, N, K],
  * db [groups, N], BF16, each NULL when not wanted; what is asked for beside it changes no bit of an
  * output.  Rows outside every group give zero rows of dx.
@@ -467,7 +468,7 @@ glu_status glu_moe_combine_bwd(int64_t tokens, int64_t choices, int64_t H, int e
  *   GLU_SAVE_BF16 : pre, BF16 [M, 2N], and extra, four more bits of each value, [M, N] bytes: value n of a
  *                   half in the low (n even) or high nibble of byte n/2 of that half's N/2.  The value
  *                   kept is the FP32 number whose bits are pre << 16 plus the nibble, taken as -8 .. 7,
- *                   << 12: 12 significant bits, so that the gradients are as exact as BF16 lets them be.
+ *                   << 12: 12 significant bits, which move the gradients by 0.0001 (2-norm, relative).
  *   GLU_SAVE_MXFP8: pre, E4M3 codes [M, 2N], and extra, their E8M0 scales [M, 2 ceil(N/32)], of the
  *                   values rounded to BF16: a checkpoint of glu_fwd_ckpt.
  * Otherwise pre and extra are NULL.  N is a multiple of 8 up to 2^19, K as for glu_linear. */
@@ -480,7 +481,9 @@ glu_status glu_gated_linear(int act, int w_layout, int save, int64_t M, int64_t 
 
 /* dp = [dh u act'(g) | dh act(g)] at the gate and up values kept (GLU_SAVE_BF16, with which extra may be
  * NULL: BF16 values alone, or GLU_SAVE_MXFP8);
- * dx = dp W, dw[e] = dp^T x and dbias[e] = sum of dp over the rows of group e.  dx [M, K], dw
+ * dx = dp W, dw[e] = dp^T x and dbias[e] = sum of dp over the rows of group e.  dp is formed in FP32 and rounded
+ * to BF16 for the two products, whose results are off by 0.0024 (2-norm, relative) where their own rounding
+ * makes 0.0017; dbias sums it unrounded.  dx [M, K], dw
  * [groups, 2N, K] and dbias [groups, 2N] in W's order, BF16, each NULL when not wanted; so is h,
  * act(g) u formed again from the values kept (what the next product's weight gradient needs).  Rows
  * of no group give zero rows of dx. */
